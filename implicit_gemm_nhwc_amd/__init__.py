@@ -47,7 +47,7 @@ OUT_DTYPES = {torch.bfloat16: torch.bfloat16, torch.float16: torch.float16,
 REASONS = {0: "ok", 1: "dtype", 2: "stride", 3: "dilation", 4: "padding", 5: "groups",
            6: "shape", 7: "output_shape", 8: "vector_width", 9: "alignment",
            10: "null_pointer", 11: "overlap", 12: "workspace", 13: "size_limit",
-           14: "epilogue"}
+           14: "epilogue", 15: "head_dim", 16: "scale"}
 
 # fused-epilogue activation codes (IGC_ACT_* in include/igemm_conv.h)
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2}
@@ -170,6 +170,13 @@ def _load(path):
     L.conv2d_fwd_general_kernel_name.restype = ctypes.c_char_p
     L.conv2d_fwd_general_workspace_bytes.argtypes = [i64p, i32, i64p, i64p, prm, i32]
     L.conv2d_fwd_general_workspace_bytes.restype = sz
+    buf = ctypes.c_char_p   # the packed argument structs of include/igemm_attn.h
+    for name in ("cross_attn_fwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd"):
+        getattr(L, name).argtypes, getattr(L, name).restype = [buf, vp], i32
+        check = getattr(L, name + "_check")
+        check.argtypes, check.restype = [buf], i32
+    for name in ("cross_attn_fwd_workspace_bytes", "qk_norm_rope_bwd_workspace_bytes"):
+        getattr(L, name).argtypes, getattr(L, name).restype = [buf], sz
     _libs[path] = L
     return L
 
@@ -819,3 +826,10 @@ def conv2d_general(input, filter, *, filter_is_fcrs, stride=1, dilation=1, pad_b
     if rc < 0:
         raise RuntimeError(f"conv2d_fwd_general failed with HIP error {-rc}")
     return out
+
+
+# -------------------------------------------------- attention operators
+from .attention import (  # noqa: E402,F401
+    cross_attention, cross_attn_fwd, cross_attn_fwd_check, cross_attn_fwd_workspace_bytes,
+    qk_norm_rope, qk_norm_rope_bwd, qk_norm_rope_bwd_check, qk_norm_rope_fwd,
+    qk_norm_rope_fwd_check, rope_table, rope_table_2d)

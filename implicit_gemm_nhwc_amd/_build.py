@@ -21,7 +21,11 @@ OBJ_DIR = os.path.join(PKG, "_build")
 ARCH = "gfx950"
 
 # (object name, source, extra defines)
-UNITS = [("igemm_conv", "igemm_conv.hip", [])]
+UNITS = [("igemm_conv", "igemm_conv.hip", []), ("igemm_attn", "igemm_attn.hip", [])]
+for _dt in ("BF16", "FP16"):
+    _d = f"-DIGC_DT=igc::DT_{_dt}"
+    UNITS += [(f"launch_attn_fwd_{_dt.lower()}", "launch_attn_fwd.hip", [_d]),
+              (f"launch_qk_norm_{_dt.lower()}", "launch_qk_norm.hip", [_d])]
 for _dt in ("BF16", "FP16", "FP8"):
     _d = f"-DIGC_DT=igc::DT_{_dt}"
     UNITS += [(f"launch_band_{_dt.lower()}", "launch_band.hip", [_d]),

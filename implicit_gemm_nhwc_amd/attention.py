@@ -1,0 +1,405 @@
+"""Binding of the attention operators of include/igemm_attn.h: cross attention
+to an encoder's states, and the per-head norm of queries and keys with the
+position rotation, each with its backward pass.
+
+Argument marshalling only, as in the package's convolution calls: every step
+runs in the HIP kernels of libigemmconv.so, and there is no fallback.
+InvalidArgument is raised for tensors the C ABI cannot describe, Declined
+(with the library's reason) for what its gate refuses.
+
+Tensors are [batch, token, head, D], D adjacent, any other strides that are
+multiples of 16 bytes; an NHWC map [N, H, W, heads * D] is
+map.view(N, H * W, heads, D).
+
+  cross_attn_fwd, cross_attn_fwd_check, cross_attn_fwd_workspace_bytes,
+  qk_norm_rope_fwd, qk_norm_rope_fwd_check,
+  qk_norm_rope_bwd, qk_norm_rope_bwd_check, qk_norm_rope_bwd_workspace_bytes
+mirror the C entries (1 handled, 0 declined, < 0 HIP error; outputs and
+workspace given); cross_attention, qk_norm_rope and qk_norm_rope_bwd allocate
+their outputs and raise on failure; rope_table and rope_table_2d make the
+rotation's tables.
+"""
+import math
+import struct
+
+import torch
+
+from . import (DTYPE_CODES, REASONS, Declined, InvalidArgument, _ptr, lib)
+
+_TYPES = {torch.bfloat16: 0, torch.float16: 1}
+_ATTN = struct.Struct("@26qdqqq")
+_PART = struct.Struct("@21q")
+_QK_TAIL = struct.Struct("@4qdqq")
+_NO_VIEW = (0, 0, 0, 0)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _view(name, t, dtype, device):
+    """(pointer, batch, token, head stride) of a [batch, token, head, D] tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise InvalidArgument(f"{name} must be a tensor")
+    if t.dim() != 4:
+        raise InvalidArgument(f"{name} must be [batch, token, head, D] (got {tuple(t.shape)})")
+    if t.dtype != dtype:
+        raise InvalidArgument(f"{name} dtype {t.dtype} differs from {dtype}")
+    if t.get_device() != device:
+        raise InvalidArgument(f"{name} is on {t.device}, the other tensors on GPU {device}")
+    sb, st, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
+        raise InvalidArgument(f"{name}: the D values of a head must be adjacent")
+    return t.data_ptr(), sb, st, sh
+
+
+def _small(name, t, dtype, device):
+    """Pointer of a dense side tensor (or None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype:
+        raise InvalidArgument(f"{name} must be {dtype} (got {t.dtype})")
+    if t.get_device() != device:
+        raise InvalidArgument(f"{name} is on {t.device}, the other tensors on GPU {device}")
+    if not t.is_contiguous():
+        raise InvalidArgument(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device(t, name="q"):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise InvalidArgument(f"{name} must be a GPU tensor")
+    return t.get_device()
+
+
+def _work(ws, nbytes, device):
+    """Pointer and bytes of a workspace tensor (or None)."""
+    if ws is None:
+        return 0, 0
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise InvalidArgument("workspace must be contiguous and on the tensors' GPU")
+    have = ws.numel() * ws.element_size()
+    if nbytes and have < nbytes:
+        raise InvalidArgument(f"workspace holds {have} bytes, workspace_bytes says {nbytes}")
+    return ws.data_ptr(), nbytes or have
+
+
+class _on:
+    """Runs the block on the tensors' GPU, and with `stream` (a torch stream
+    or a raw handle) as its current one, so that what is allocated inside
+    belongs to the stream that uses it."""
+
+    def __init__(self, device, stream):
+        self.device = torch.cuda.device(device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        self.stream = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+
+    def __exit__(self, *err):
+        if self.stream is not None:
+            self.stream.__exit__(*err)
+        self.device.__exit__(*err)
+
+
+def _elsewhere(device, stream):
+    return stream is not None or device != torch._C._cuda_getDevice()
+
+
+def _raise(name, rc, check, packed):
+    if rc == 0:
+        reason = check(packed)
+        raise Declined(f"{name} declined: {REASONS.get(reason, reason)}")
+    raise RuntimeError(f"{name} failed with HIP error {-rc}")
+
+
+# --------------------------------------------------------- cross attention
+def _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale):
+    """The call's head of igc_cross_attn: sizes, views, side arrays, scale and
+    type, and the GPU."""
+    device = _device(q)
+    dtype = q.dtype
+    if dtype not in _TYPES and dtype not in DTYPE_CODES:
+        raise InvalidArgument(f"q dtype {dtype} is not bf16 or fp16")
+    qv = _view("q", q, dtype, device)
+    kv = _view("k", k, dtype, device)
+    vv = _view("v", v, dtype, device)
+    b, tq, hq, d = q.shape
+    kb, tk, hk, kd = k.shape
+    if kb != b or kd != d or v.shape != k.shape:
+        raise InvalidArgument(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} "
+                              "do not belong together")
+    if out is None:
+        ov = _NO_VIEW
+    else:
+        ov = _view("out", out, dtype, device)
+        if out.shape != q.shape:
+            raise InvalidArgument(f"out must have q's shape {tuple(q.shape)}")
+    lp = _small("lse", lse, torch.float32, device)
+    if lse is not None and lse.shape != (b, hq, tq):
+        raise InvalidArgument(f"lse must be {(b, hq, tq)} (got {tuple(lse.shape)})")
+    np_ = _small("kv_lens", kv_lens, torch.int32, device)
+    if kv_lens is not None and kv_lens.shape != (b,):
+        raise InvalidArgument(f"kv_lens must be {(b,)} (got {tuple(kv_lens.shape)})")
+    mp = ms = 0
+    if key_mask is not None:
+        if key_mask.dtype not in (torch.uint8, torch.bool):
+            raise InvalidArgument(f"key_mask must be uint8 or bool (got {key_mask.dtype})")
+        if key_mask.get_device() != device:
+            raise InvalidArgument("key_mask is not on the tensors' GPU")
+        if key_mask.shape != (b, tk):
+            raise InvalidArgument(f"key_mask must be {(b, tk)} (got {tuple(key_mask.shape)})")
+        ms, inner = key_mask.stride()
+        if inner != 1 and tk > 1:
+            raise InvalidArgument("key_mask: the keys of a batch entry must be adjacent")
+        mp = key_mask.data_ptr()
+    if scale is None:
+        scale = 1.0 / math.sqrt(d) if d else 1.0
+    code = _TYPES.get(dtype, DTYPE_CODES[dtype] if dtype in DTYPE_CODES else -1)
+    return (b, tq, tk, hq, hk, d, *qv, *kv, *vv, *ov, lp, np_, mp, ms, float(scale), code), device
+
+
+def cross_attn_fwd(q, k, v, out, *, lse=None, kv_lens=None, key_mask=None, scale=None,
+                   workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Enqueue cross attention into out (and lse).  1 handled, 0 declined, < 0
+    HIP error."""
+    head, device = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
+    ws = _work(workspace, workspace_bytes, device)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return lib().cross_attn_fwd(_ATTN.pack(*head, *ws), _raw_stream(device))
+    return lib().cross_attn_fwd(_ATTN.pack(*head, *ws), _raw_stream(device))
+
+
+def cross_attn_fwd_check(q, k, v, out, *, lse=None, kv_lens=None, key_mask=None, scale=None,
+                         workspace=None, workspace_bytes=0) -> int:
+    """Host-only gate of cross_attn_fwd: 0 or a decline reason code."""
+    head, device = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
+    return lib().cross_attn_fwd_check(_ATTN.pack(*head, *_work(workspace, workspace_bytes, device)))
+
+
+def cross_attn_fwd_workspace_bytes(q_shape, k_shape, dtype) -> int:
+    """Workspace of a call of these shapes (0 when none is needed, or when it
+    would be declined)."""
+    b, tq, hq, d = q_shape
+    _, tk, hk, _ = k_shape
+    return lib().cross_attn_fwd_workspace_bytes(
+        _ATTN.pack(b, tq, tk, hq, hk, d, *(0,) * 20, 1.0, DTYPE_CODES.get(dtype, -1), 0, 0))
+
+
+def cross_attention(q, k, v, *, scale=None, kv_lens=None, key_mask=None, return_lse=False,
+                    stream=None):
+    """Attention of q [b, tq, hq, D] to the encoder's states k, v [b, tk, hk,
+    D] (hk dividing hq); scale defaults to 1 / sqrt(D).  kv_lens (int32 [b])
+    and key_mask (uint8 or bool [b, tk], nonzero = attend) say which keys are
+    valid; a row without one gives 0.  Returns out, dense like q, and with
+    return_lse also the fp32 row statistics [b, hq, tq] for
+    cross_attention_bwd."""
+    device = _device(q)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return cross_attention(q, k, v, scale=scale, kv_lens=kv_lens, key_mask=key_mask,
+                                   return_lse=return_lse)
+    if q.dim() != 4:
+        raise InvalidArgument(f"q must be [batch, token, head, D] (got {tuple(q.shape)})")
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = None
+    if return_lse:
+        lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
+                          device=q.device)
+    head, _ = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
+    L = lib()
+    packed = _ATTN.pack(*head, 0, 0)
+    need = L.cross_attn_fwd_workspace_bytes(packed)
+    if need:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        packed = _ATTN.pack(*head, ws.data_ptr(), need)
+    rc = L.cross_attn_fwd(packed, _raw_stream(device))
+    if rc != 1:
+        _raise("cross_attn_fwd", rc, L.cross_attn_fwd_check, packed)
+    return (out, lse) if return_lse else out
+
+
+# ------------------------------------------- norm of queries and keys, rotation
+def _table(name, t, device):
+    if t is None:
+        return 0, 0, 0
+    if t.dim() != 2:
+        raise InvalidArgument(f"{name} must be [rows, rotated values] (got {tuple(t.shape)})")
+    return _small(name, t, torch.float32, device), t.shape[0], t.shape[1]
+
+
+def _part(n, x, grad, out, weight, dweight, table, positions, dtype, device, d):
+    """One igc_qk_part, packed."""
+    if x is None:
+        return _PART.pack(*(0,) * 17, 0, 0, 0, 0)
+    b, t, h, dd = x.shape
+    xv = _view(n, x, dtype, device)
+    if dd != d:
+        raise InvalidArgument(f"{n} has heads of {dd}, not {d}")
+    gv, ov = _NO_VIEW, _NO_VIEW
+    if grad is not None:
+        gv = _view("d" + n, grad, dtype, device)
+        if grad.shape != x.shape:
+            raise InvalidArgument(f"d{n} must have {n}'s shape {tuple(x.shape)}")
+    if out is not None:
+        ov = _view(n + " output", out, dtype, device)
+        if out.shape != x.shape:
+            raise InvalidArgument(f"{n}'s output must have its shape {tuple(x.shape)}")
+    for name, w in ((n + "_weight", weight), (n + "_weight gradient", dweight)):
+        if w is not None and w.shape != (d,):
+            raise InvalidArgument(f"{name} must be {(d,)} (got {tuple(w.shape)})")
+    pp = ps = 0
+    if positions is not None:
+        if positions.dtype != torch.int32:
+            raise InvalidArgument(f"{n}_positions must be int32 (got {positions.dtype})")
+        if positions.get_device() != device:
+            raise InvalidArgument(f"{n}_positions is not on the tensors' GPU")
+        if positions.shape != (b, t):
+            raise InvalidArgument(f"{n}_positions must be {(b, t)} (got "
+                                  f"{tuple(positions.shape)})")
+        ps, inner = positions.stride()
+        if inner != 1 and t > 1:
+            raise InvalidArgument(f"{n}_positions: the tokens of a batch entry must be adjacent")
+        pp = positions.data_ptr()
+    tp, rows, _ = _table(n + "_table", table, device)
+    return _PART.pack(b, t, h, *xv, *gv, *ov, _small(n + "_weight", weight, torch.float32, device),
+                      _small(n + "_weight gradient", dweight, torch.float32, device), tp, rows,
+                      pp, ps)
+
+
+def _qk_pack(q, k, dq, dk, q_out, k_out, q_weight, k_weight, dq_weight, dk_weight, q_table,
+             k_table, q_positions, k_positions, eps, interleaved, ws):
+    first = q if q is not None else k
+    device = _device(first, "q" if q is not None else "k")
+    dtype = first.dtype
+    if dtype not in DTYPE_CODES:
+        raise InvalidArgument(f"dtype {dtype} is not bf16 or fp16")
+    if first.dim() != 4:
+        raise InvalidArgument(f"tensors must be [batch, token, head, D] (got "
+                              f"{tuple(first.shape)})")
+    d = first.shape[3]
+    rots = {t.shape[1] for x, t in ((q, q_table), (k, k_table))
+            if x is not None and t is not None and t.dim() == 2}
+    if len(rots) > 1 or (rots and any(x is not None and t is None
+                                      for x, t in ((q, q_table), (k, k_table)))):
+        raise InvalidArgument("q_table and k_table must rotate the same number of values")
+    rot = rots.pop() if rots else 0
+    return (_part("q", q, dq, q_out, q_weight, dq_weight, q_table, q_positions, dtype, device, d)
+            + _part("k", k, dk, k_out, k_weight, dk_weight, k_table, k_positions, dtype, device, d)
+            + _QK_TAIL.pack(d, rot, 1 if interleaved else 0, DTYPE_CODES[dtype], float(eps),
+                            *ws)), device
+
+
+def qk_norm_rope_fwd(q, k, q_out, k_out, *, q_weight=None, k_weight=None, q_table=None,
+                     k_table=None, q_positions=None, k_positions=None, eps=1e-6,
+                     interleaved=False, stream=None) -> int:
+    """Enqueue the norm and rotation of q and k (either may be None) into
+    q_out, k_out (q and k themselves: in place).  1 handled, 0 declined, < 0
+    HIP error."""
+    packed, device = _qk_pack(q, k, None, None, q_out, k_out, q_weight, k_weight, None, None,
+                              q_table, k_table, q_positions, k_positions, eps, interleaved,
+                              (0, 0))
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return lib().qk_norm_rope_fwd(packed, _raw_stream(device))
+    return lib().qk_norm_rope_fwd(packed, _raw_stream(device))
+
+
+def qk_norm_rope_fwd_check(q, k, q_out, k_out, *, q_weight=None, k_weight=None, q_table=None,
+                           k_table=None, q_positions=None, k_positions=None, eps=1e-6,
+                           interleaved=False) -> int:
+    """Host-only gate of qk_norm_rope_fwd: 0 or a decline reason code."""
+    packed, _ = _qk_pack(q, k, None, None, q_out, k_out, q_weight, k_weight, None, None, q_table,
+                         k_table, q_positions, k_positions, eps, interleaved, (0, 0))
+    return lib().qk_norm_rope_fwd_check(packed)
+
+
+def qk_norm_rope_bwd_check(dq, dk, q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
+                           dq_weight=None, dk_weight=None, q_table=None, k_table=None,
+                           q_positions=None, k_positions=None, eps=1e-6, interleaved=False,
+                           workspace=None, workspace_bytes=0) -> int:
+    """Host-only gate of qk_norm_rope_bwd: 0 or a decline reason code."""
+    device = _device(q if q is not None else k)
+    packed, _ = _qk_pack(q, k, dq, dk, dq_out, dk_out, q_weight, k_weight, dq_weight, dk_weight,
+                         q_table, k_table, q_positions, k_positions, eps, interleaved,
+                         _work(workspace, workspace_bytes, device))
+    return lib().qk_norm_rope_bwd_check(packed)
+
+
+def qk_norm_rope(q, k=None, *, q_weight=None, k_weight=None, q_table=None, k_table=None,
+                 q_positions=None, k_positions=None, eps=1e-6, interleaved=False, stream=None):
+    """The heads of q [b, tq, hq, D] and k [b', tk, hk, D] divided by their
+    root mean square, times the weight (fp32 [D] or None), their first
+    table.shape[1] values rotated in pairs by the table row (fp32 {cosines,
+    sines}, rope_table) of their position (int32 [b, t] or None: the token's
+    number).  Returns the two results, dense; k may be None (then q's result
+    alone)."""
+    device = _device(q)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return qk_norm_rope(q, k, q_weight=q_weight, k_weight=k_weight, q_table=q_table,
+                                k_table=k_table, q_positions=q_positions,
+                                k_positions=k_positions, eps=eps, interleaved=interleaved)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    packed, _ = _qk_pack(q, k, None, None, q_out, k_out, q_weight, k_weight, None, None, q_table,
+                         k_table, q_positions, k_positions, eps, interleaved, (0, 0))
+    L = lib()
+    rc = L.qk_norm_rope_fwd(packed, _raw_stream(device))
+    if rc != 1:
+        _raise("qk_norm_rope_fwd", rc, L.qk_norm_rope_fwd_check, packed)
+    return q_out if k is None else (q_out, k_out)
+
+
+def qk_norm_rope_bwd(dq, dk, q, k=None, *, q_weight=None, k_weight=None, q_table=None,
+                     k_table=None, q_positions=None, k_positions=None, eps=1e-6,
+                     interleaved=False, stream=None):
+    """Gradients of qk_norm_rope at its inputs: dq, dk are those of its
+    results.  Returns (dq, dk, dq_weight, dk_weight) at q, k and the weights
+    (fp32; also for a weight of None, which counts as ones); k may be None
+    (its two gradients are then None)."""
+    device = _device(q)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return qk_norm_rope_bwd(dq, dk, q, k, q_weight=q_weight, k_weight=k_weight,
+                                    q_table=q_table, k_table=k_table, q_positions=q_positions,
+                                    k_positions=k_positions, eps=eps, interleaved=interleaved)
+    d = q.shape[-1]
+    dq_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dk_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    dw = torch.empty((1 if k is None else 2, d), dtype=torch.float32, device=q.device)
+    dqw, dkw = dw[0], None if k is None else dw[1]
+    args = (q, k, dq, dk, dq_out, dk_out, q_weight, k_weight, dqw, dkw, q_table, k_table,
+            q_positions, k_positions, eps, interleaved)
+    L = lib()
+    packed, _ = _qk_pack(*args, (0, 0))
+    need = L.qk_norm_rope_bwd_workspace_bytes(packed)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    packed = packed[:-16] + struct.pack("@qq", ws.data_ptr(), need)
+    rc = L.qk_norm_rope_bwd(packed, _raw_stream(device))
+    if rc != 1:
+        _raise("qk_norm_rope_bwd", rc, L.qk_norm_rope_bwd_check, packed)
+    return dq_out, dk_out, dqw, dkw
+
+
+def rope_table(n, rot, *, base=10000.0, first=0, device=None):
+    """Table of qk_norm_rope for n positions from `first` on: fp32 [n, rot],
+    cosines then sines of position * base^(-2 i / rot), the angles formed in
+    64 bits."""
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    a = (torch.arange(n, dtype=torch.float64) + first)[:, None] * base ** (-2.0 * i / rot)
+    return torch.cat([a.cos(), a.sin()], 1).float().to(device)
+
+
+def rope_table_2d(h, w, rot, *, base=10000.0, device=None):
+    """Table for the pixels of an h x w map in NHWC order (rot a multiple of
+    4): the first half of the angles from the pixel's row, the second from its
+    column, each as rope_table's of rot / 2."""
+    i = torch.arange(rot // 4, dtype=torch.float64)
+    f = base ** (-4.0 * i / rot)
+    r = torch.arange(h, dtype=torch.float64)[:, None, None] * f
+    c = torch.arange(w, dtype=torch.float64)[None, :, None] * f
+    a = torch.cat([r.expand(h, w, -1), c.expand(h, w, -1)], 2).reshape(h * w, rot // 2)
+    return torch.cat([a.cos(), a.sin()], 1).float().to(device)

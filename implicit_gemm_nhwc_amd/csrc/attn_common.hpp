@@ -1,0 +1,213 @@
+// Pieces shared by the attention kernels: argument block, tile staging, the
+// MFMA operand layouts and the mask words.
+//
+// All of them work on blocks of 32 rows x 32 keys through
+// v_mfma_f32_32x32x16 (bf16 / fp16): lane l supplies row (A) or column (B)
+// l % 32 with 8 consecutive k at 8 * (l / 32); the result has column l % 32
+// and, in register i, row 8 * (i / 4) + 4 * (l / 32) + i % 4.  A result
+// therefore becomes the B operand of a following product without leaving its
+// lane when that product numbers its k axis by the result's rows: k slot
+// (half h, j) of a step of 16 is row 8 * (j / 4) + 4 * h + j % 4.  The other
+// operand follows that numbering through transposing LDS reads
+// (ds_read_b64_tr_b16: each lane gets 4 consecutive rows of one column).
+#pragma once
+
+#include "igemm_kernels.hpp"
+
+namespace igc {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct AttnArgs {
+    const uint8_t *q, *k, *v, *o, *dout;
+    uint8_t *out, *dq, *dk, *dv;
+    float* lse;            // [B][Hq][Tq]
+    const float* delta;    // backward: [B][Hk][rows]
+    const int32_t* lens;
+    const uint8_t* mask;
+    float *part, *stat;    // partial results of split launches
+    uint32_t* bound;       // backward, fp16: bound of |ds| per (batch, key head), float bits
+    // strides in bytes
+    int64_t q_b, q_t, q_h, k_b, k_t, k_h, v_b, v_t, v_h, o_b, o_t, o_h;
+    int64_t do_b, do_t, do_h, dq_b, dq_t, dq_h, dk_b, dk_t, dk_h, dv_b, dv_t, dv_h;
+    int64_t mask_b;
+    int B, Tq, Tk, Hq, Hk, G, D;
+    int rows;       // Tq * G: the queries that share one key head
+    int row_tiles;  // workgroups along the rows
+    int key_tiles;  // backward: workgroups along the keys
+    int nsplit;     // workgroups that share a tile's keys (backward dk / dv: its rows)
+    int split;      // keys (rows) per split, a multiple of the key (row) tile
+    float c;        // scale * log2(e): p = 2^(c s - c m)
+    float scale;
+    uint32_t g_mul; // row / G = mulhi(row, g_mul) >> g_shift, g_mul = 0 for G = 1
+    int g_shift;
+};
+
+// row / G by the host's multiplier (exact for row < 2^31).
+__device__ __forceinline__ int div_g(const AttnArgs& a, int row) {
+    return a.g_mul ? (int)(__umulhi((uint32_t)row, a.g_mul) >> a.g_shift) : row;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t attn_rsrc(const void* base) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, 0x7fffffff,
+                                             0x00020000);
+}
+// A buffer offset past the range: loads return zero, stores are dropped.
+constexpr unsigned kOut = 0x80000000u;
+
+// LDS tiles hold rows of DP elements (DP = D rounded up to 32), the 16-byte
+// chunk c of row r at c ^ lds_swz(r).  Two patterns read them: whole chunks
+// of 16 consecutive rows (ds_read_b128), and 64 adjacent bytes of 4
+// consecutive rows (the transposing read).  The low two chunk bits turn with
+// r / 4, and the bits above with what of r % 4 the row pitch does not spread
+// over the 256 bytes of banks by itself, so that both patterns reach
+// different banks.
+template <int DP>
+__device__ __forceinline__ int lds_swz(int r) {
+    const int lo = (r >> 2) & 3;
+    if constexpr (DP == 128) return ((r & 3) << 2) | lo;
+    if constexpr (DP == 64) return (((r >> 1) & 1) << 2) | lo;
+    return lo;   // 32: pitch 64; 96: pitch 192
+}
+
+// Byte offset of chunk c of row r.
+template <int DP>
+__device__ __forceinline__ int tile_off(int r, int c) {
+    return r * (DP * 2) + ((c ^ lds_swz<DP>(r)) << 4);
+}
+
+// Operand of 8 consecutive k of one row (chunk c of row r): plain read.
+template <int DP>
+__device__ __forceinline__ i32x4 frag_row(const uint8_t* lds, int r, int c) {
+    return *reinterpret_cast<const i32x4*>(lds + tile_off<DP>(r, c));
+}
+
+__device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
+    typedef __attribute__((address_space(3))) s16x4* lp;
+    typedef __attribute__((address_space(3))) const uint8_t* bp;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(bp)p));
+}
+
+// Operand whose row / column is column 32 * db + l % 32 of the tile and whose
+// k slots are the tile's rows r0 + 8 * (j / 4) + 4 * h + j % 4.  The 16 lanes
+// of a transposing read address 4 rows x 32 bytes: lane i row i / 4, bytes
+// 8 * (i % 4); `lane` terms are folded into tr_off, computed once:
+//   row 4 * h + (l % 16) / 4, chunk 4 * db + 2 * ((l / 16) % 2) + (l % 4) / 2.
+template <int DP>
+__device__ __forceinline__ i32x4 frag_col(const uint8_t* lds, int r0, int db, int lane) {
+    const int r = r0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
+    const int c = 4 * db + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const int b = (lane & 1) * 8;
+    const u32x2 x = read_tr(lds + tile_off<DP>(r, c) + b);
+    const u32x2 y = read_tr(lds + tile_off<DP>(r + 8, c) + b);
+    return i32x4{(int)x[0], (int)x[1], (int)y[0], (int)y[1]};
+}
+
+// Bit j of the result: key j0 + j is valid.  mb is the mask byte of key
+// j0 + lane (any nonzero value without a mask); keys at or past `end` are not.
+__device__ __forceinline__ uint64_t mask_word(uint32_t mb, int left) {
+    const uint64_t w = __ballot(mb != 0);
+    return left >= 64 ? w : left <= 0 ? 0 : w & (~0ull >> (64 - left));
+}
+
+// Mask byte of key j0 + lane for mask_word; reads only keys before `end`.
+__device__ __forceinline__ uint32_t mask_byte(const uint8_t* row, int j0, int end, int lane) {
+    if (!row) return 1;
+    return j0 + lane < end ? row[j0 + lane] : 0;
+}
+
+// Direct loads of a tile of ROWS rows into LDS by NW waves: each wave writes
+// 1 KB pieces (64 lanes x 16 bytes in LDS order), so a lane's LDS place fixes
+// its row and, through the swizzle, the chunk it has to fetch.  Lanes whose
+// chunk is past D or whose row is not to be read get an offset out of range,
+// which stores zeros.
+template <int DP, int ROWS, int NW>
+struct TileStage {
+    static constexpr int PIECES = ROWS * DP * 2 / 1024;
+    static constexpr int PER = (PIECES + NW - 1) / NW;
+    static constexpr bool EVEN = PIECES % NW == 0;
+    int row[PER], chunk[PER];
+
+    __device__ __forceinline__ void init(int wave, int lane, int D) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int p = ((i * NW + wave) * 1024 + lane * 16);
+            row[i] = p / (DP * 2);
+            const int c = ((p % (DP * 2)) >> 4) ^ lds_swz<DP>(row[i]);
+            chunk[i] = c * 8 < D ? c * 16 : -1;
+        }
+    }
+    // rows of `pitch` bytes from base; bit r of `valid` says row r is read
+    __device__ __forceinline__ void issue(const uint8_t* base, unsigned pitch, uint64_t valid,
+                                          uint8_t* lds, int wave) const {
+        const __amdgpu_buffer_rsrc_t rs = attn_rsrc(base);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (!EVEN && i * NW + wave >= PIECES) break;
+            const bool ok = chunk[i] >= 0 && ((valid >> row[i]) & 1);
+            const unsigned off = ok ? (unsigned)row[i] * pitch + (unsigned)chunk[i] : kOut;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rs, (__attribute__((address_space(3))) void*)(lds + (i * NW + wave) * 1024), 16,
+                off, 0, 0, 0);
+        }
+    }
+};
+
+// P (or ds) of 16 result registers as the two B operands of 16 rows each.
+template <int DT>
+__device__ __forceinline__ void pack_frag(const float* p, i32x4* f) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            f[g][j] = (int)pack_out2(p[8 * g + 2 * j], p[8 * g + 2 * j + 1], DT);
+}
+
+// Maximum and sum over a lane and the one 32 away.
+__device__ __forceinline__ void both_halves(float x, float* lo, float* hi) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t r0 = r[0], r1 = r[1];   // a bit cast of r[1] itself would read r[0]
+    *lo = __builtin_bit_cast(float, r0);
+    *hi = __builtin_bit_cast(float, r1);
+}
+__device__ __forceinline__ float max_halves(float x) {
+    float a, b;
+    both_halves(x, &a, &b);
+    return fmaxf(a, b);
+}
+__device__ __forceinline__ float sum_halves(float x) {
+    float a, b;
+    both_halves(x, &a, &b);
+    return a + b;
+}
+
+// Store of a result block whose columns are tensor rows and whose rows are
+// 32 values of the head axis: register 4 g + i of half h is value
+// 8 g + 4 h + i.  After exchanging halves each lane holds 8 adjacent values:
+// half h takes the groups g = h and 2 + h.  dst is the lane's row (NULL: no
+// store), d0 the block's first value, values at or past D are not stored.
+template <int DT>
+__device__ __forceinline__ void store_block(uint8_t* dst, const f32x16& v, float f, int d0, int D,
+                                            int half) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_out2(v[2 * i] * f, v[2 * i + 1] * f, DT);
+#pragma unroll
+    for (int gg = 0; gg < 2; ++gg) {
+        // groups 2 gg (words 4 gg, 4 gg + 1) and 2 gg + 1 (words 4 gg + 2, + 3)
+        const auto a = __builtin_amdgcn_permlane32_swap(w[4 * gg], w[4 * gg + 2], false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(w[4 * gg + 1], w[4 * gg + 3], false, false);
+        const int d = d0 + 16 * gg + 8 * half;
+        if (dst && d < D)
+            *reinterpret_cast<u32x4*>(dst + d * 2) = u32x4{a[0], b[0], a[1], b[1]};
+    }
+}
+
+}  // namespace igc

@@ -1,0 +1,445 @@
+// Cross attention, forward.
+//
+// Rows are the Tq * G queries that share one key head (G query heads a key
+// head), so grouped heads read their keys once.  Each wave keeps QB blocks of
+// 32 rows: scores come as S^T = K Q^T (keys down the registers, one row a
+// lane), which makes the softmax statistics of a row a sum over one lane's
+// registers plus one exchange between the wave's halves, and lets P^T go into
+// O^T += V^T P^T as the B operand without leaving its lane.
+#pragma once
+
+#include "attn_common.hpp"
+
+namespace igc {
+
+// fp16 holds probabilities down to 2^-14 with full precision: they are
+// scaled by 2^7 (the sum l with them, so the factor leaves in O / l).  With
+// the statistics' slack of 2^8 below they stay under 2^15.  bf16 has fp32's
+// range and needs none.
+template <int DT>
+__device__ __forceinline__ constexpr float p_shift() {
+    return DT == DT_FP16 ? 7.0f : 0.0f;
+}
+// The running maximum follows the true one only when a row exceeds it by
+// 2^kSlack: O and l are then rescaled, which most tiles so skip.  The
+// maximum only guards the range, so the result does not depend on it beyond
+// rounding.
+constexpr float kSlack = 8.0f;
+
+// Softmax step of one block of 32 rows over KB blocks of 32 keys: scores s
+// become probabilities, m (scaled by c, in powers of two) and l follow, and
+// acc is rescaled where a maximum moved.  `word` has a bit per key.
+template <int DT, int KB, int DB>
+__device__ __forceinline__ void softmax_step(f32x16 (&s)[KB], uint64_t word, bool full, float c,
+                                             float& m, float& l, f32x16 (&acc)[DB], int half) {
+    if (!full) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            const uint32_t w = (uint32_t)(word >> (32 * kb)) >> (4 * half);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (!((w >> (8 * (i / 4) + i % 4)) & 1)) s[kb][i] = -__builtin_inff();
+        }
+    }
+    float t = -__builtin_inff();
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) t = fmaxf(fmaxf(s[kb][i], s[kb][i + 1]), t);
+    t = max_halves(t) * c;
+    if (__any(t > m + kSlack)) {   // also the first tile with a valid key: m = -inf
+        const float mn = fmaxf(m, t);
+        // rows still without a valid key: 2^(-inf - 0) keeps everything 0
+        const float f = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[d][i] *= f;
+    }
+    const float ms = (m == -__builtin_inff() ? 0.0f : m) - p_shift<DT>();
+    float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], c, -ms));
+            s[kb][i] = p;
+            sum[i & 3] += p;
+        }
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+// Row `row` of the packed queries: byte offset of its (token, head) from the
+// batch and first head of the group.
+__device__ __forceinline__ int64_t packed_off(const AttnArgs& a, int row, int64_t st, int64_t sh) {
+    const int tok = div_g(a, row);
+    return (int64_t)tok * st + (int64_t)(row - tok * a.G) * sh;
+}
+
+// Results of one block of 32 rows (row of this lane: `row`): the final
+// output, or the partial result of one split.
+template <int DT, int DB>
+__device__ __forceinline__ void fwd_finish(const AttnArgs& a, int b, int hk, int sp, int row,
+                                           f32x16 (&acc)[DB], float m, float l, int half) {
+    l = sum_halves(l);
+    const bool live = row < a.rows;
+    if (a.nsplit > 1) {
+        const int64_t bh = (int64_t)b * a.Hk + hk;
+        const int64_t at = ((int64_t)sp * a.B * a.Hk + bh) * a.rows + row;
+        if (live) {
+            float* o = a.part + at * a.D;
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int d = 32 * db + 8 * g + 4 * half;
+                    if (d < a.D)
+                        *reinterpret_cast<f32x4*>(o + d) =
+                            f32x4{acc[db][4 * g], acc[db][4 * g + 1], acc[db][4 * g + 2],
+                                  acc[db][4 * g + 3]};
+                }
+            if (half == 0) {
+                a.stat[at * 2] = m;
+                a.stat[at * 2 + 1] = l;
+            }
+        }
+        return;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays NaN
+    uint8_t* dst = live ? a.out + (int64_t)b * a.o_b + (int64_t)hk * a.G * a.o_h +
+                              packed_off(a, row, a.o_t, a.o_h)
+                        : nullptr;
+#pragma unroll
+    for (int db = 0; db < DB; ++db) store_block<DT>(dst, acc[db], inv, 32 * db, a.D, half);
+    if (a.lse && live && half == 0) {
+        const int tok = div_g(a, row);
+        const int64_t h = (int64_t)b * a.Hq + hk * a.G + (row - tok * a.G);
+        // l carries 2^p_shift
+        a.lse[h * a.Tq + tok] =
+            l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l) - p_shift<DT>()) * kLn2;
+    }
+}
+
+// The wave's query block as B operands: rows past the last are zero, as are
+// values past D.
+template <int DP>
+__device__ __forceinline__ void load_rows(const AttnArgs& a, const uint8_t* base, int64_t st,
+                                          int64_t sh, int row, int half, i32x4 (&f)[DP / 16]) {
+    const bool live = row < a.rows;
+    const uint8_t* p = base + (live ? packed_off(a, row, st, sh) : 0) + 16 * half;
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s)
+        f[s] = live && 16 * s + 8 * half < a.D ? *reinterpret_cast<const i32x4*>(p + 32 * s)
+                                               : i32x4{0, 0, 0, 0};
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: NW waves of QB blocks of 32 rows walk the keys in tiles of 64,
+// double buffered in LDS through direct loads, one barrier a tile.
+template <int DT, int DP, int QB, int NW>
+__global__ __launch_bounds__(NW * 64, QB == 1 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
+    constexpr int KT = 64, KB = 2, DB = DP / 32, KS = DP / 16;
+    constexpr int TILE = KT * DP * 2;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    lds_poison<NW * 64>(lds, 4 * TILE);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int half = lane >> 5;
+
+    int idx = xcd_remap(blockIdx.x, gridDim.x);
+    const int rt = idx % a.row_tiles;
+    idx /= a.row_tiles;
+    const int sp = idx % a.nsplit;
+    idx /= a.nsplit;
+    const int hk = idx % a.Hk, b = idx / a.Hk;
+
+    const int len = a.lens ? max(0, min(a.lens[b], a.Tk)) : a.Tk;
+    const int j_begin = sp * a.split, j_end = min(len, j_begin + a.split);
+
+    int row[QB];
+    i32x4 qf[QB][KS];
+    f32x16 acc[QB][DB];
+    float m[QB], l[QB];
+    const uint8_t* qbase = a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h;
+#pragma unroll
+    for (int r = 0; r < QB; ++r) {
+        row[r] = (rt * NW + wave) * (32 * QB) + 32 * r + (lane & 31);
+        load_rows<DP>(a, qbase, a.q_t, a.q_h, row[r], half, qf[r]);
+        m[r] = -__builtin_inff();
+        l[r] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[r][d][i] = 0.0f;
+    }
+
+    const uint8_t* kbase = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h;
+    const uint8_t* vbase = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h;
+    const uint8_t* mrow = a.mask ? a.mask + (int64_t)b * a.mask_b : nullptr;
+    TileStage<DP, KT, NW> st;
+    st.init(wave, lane, a.D);
+    const unsigned kp = (unsigned)a.k_t, vp = (unsigned)a.v_t;
+
+    if (j_begin < j_end) {
+        uint64_t word = mask_word(mask_byte(mrow, j_begin, j_end, lane), j_end - j_begin);
+        st.issue(kbase + (int64_t)j_begin * a.k_t, kp, word, lds, wave);
+        st.issue(vbase + (int64_t)j_begin * a.v_t, vp, word, lds + TILE, wave);
+        uint32_t mb = mask_byte(mrow, j_begin + KT, j_end, lane);
+        int buf = 0;
+        for (int j = j_begin; j < j_end; j += KT) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            const uint8_t* kl = lds + buf * 2 * TILE;
+            const uint8_t* vl = kl + TILE;
+            const uint64_t next = mask_word(mb, j_end - (j + KT));
+            if (j + KT < j_end) {
+                uint8_t* nl = lds + (buf ^ 1) * 2 * TILE;
+                st.issue(kbase + (int64_t)(j + KT) * a.k_t, kp, next, nl, wave);
+                st.issue(vbase + (int64_t)(j + KT) * a.v_t, vp, next, nl + TILE, wave);
+                mb = mask_byte(mrow, j + 2 * KT, j_end, lane);
+            }
+            if (word != 0) {
+                f32x16 s[QB][KB];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+                    for (int r = 0; r < QB; ++r)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) s[r][kb][i] = 0.0f;
+#pragma unroll
+                    for (int x = 0; x < KS; ++x) {
+                        const i32x4 kf = frag_row<DP>(kl, 32 * kb + (lane & 31), 2 * x + half);
+#pragma unroll
+                        for (int r = 0; r < QB; ++r)
+                            s[r][kb] = mfma32<DT>(&kf, &qf[r][x], s[r][kb]);
+                    }
+                }
+                i32x4 pf[QB][KB][2];
+#pragma unroll
+                for (int r = 0; r < QB; ++r) {
+                    softmax_step<DT, KB, DB>(s[r], word, word == ~0ull, a.c, m[r], l[r], acc[r],
+                                             half);
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        float p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) p[i] = s[r][kb][i];
+                        pack_frag<DT>(p, pf[r][kb]);
+                    }
+                }
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+#pragma unroll
+                        for (int d = 0; d < DB; ++d) {
+                            const i32x4 vf = frag_col<DP>(vl, 32 * kb + 16 * g, d, lane);
+#pragma unroll
+                            for (int r = 0; r < QB; ++r)
+                                acc[r][d] = mfma32<DT>(&vf, &pf[r][kb][g], acc[r][d]);
+                        }
+            }
+            word = next;
+            buf ^= 1;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < QB; ++r)
+        fwd_finish<DT, DB>(a, b, hk, sp, row[r], acc[r], m[r], l[r], half);
+}
+
+// ---------------------------------------------------------------------------
+// At most 32 rows (single tokens): the waves of a workgroup take blocks of 32
+// keys in turn, each through its own two LDS buffers without barriers, so the
+// key and value bytes stream with two blocks a wave in flight; the waves'
+// results are joined through LDS at the end.
+template <int DT, int DP, int NW>
+__global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
+    constexpr int KT = 32, DB = DP / 32, KS = DP / 16;
+    constexpr int TILE = KT * DP * 2;
+    constexpr int STAGE = 2 * TILE;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    lds_poison<NW * 64>(lds, NW * 2 * STAGE + NW * 64 * 4);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int half = lane >> 5;
+    uint8_t* mine = lds + wave * 2 * STAGE;
+    float* st_m = reinterpret_cast<float*>(lds + NW * 2 * STAGE);   // [NW][32] m, then l
+    float* st_l = st_m + NW * 32;
+
+    int idx = xcd_remap(blockIdx.x, gridDim.x);
+    const int sp = idx % a.nsplit;
+    idx /= a.nsplit;
+    const int hk = idx % a.Hk, b = idx / a.Hk;
+    const int len = a.lens ? max(0, min(a.lens[b], a.Tk)) : a.Tk;
+    const int j_begin = sp * a.split + wave * KT, j_end = min(len, sp * a.split + a.split);
+
+    const int row = lane & 31;
+    i32x4 qf[KS];
+    load_rows<DP>(a, a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h, a.q_t, a.q_h, row, half,
+                  qf);
+    f32x16 acc[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+    float m = -__builtin_inff(), l = 0.0f;
+
+    const uint8_t* kbase = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h;
+    const uint8_t* vbase = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h;
+    const uint8_t* mrow = a.mask ? a.mask + (int64_t)b * a.mask_b : nullptr;
+    TileStage<DP, KT, 1> st;
+    st.init(0, lane, a.D);
+    constexpr int LOADS = 2 * TileStage<DP, KT, 1>::PIECES;
+    const unsigned kp = (unsigned)a.k_t, vp = (unsigned)a.v_t;
+    constexpr int STEP = NW * KT;
+
+    auto word_at = [&](uint32_t mb, int j) -> uint32_t {
+        return (uint32_t)(mask_word(mb, j_end - j) & 0xffffffffu);
+    };
+    if (j_begin < j_end) {
+        uint32_t w0 = word_at(mask_byte(mrow, j_begin, j_end, lane), j_begin), w1 = 0;
+        st.issue(kbase + (int64_t)j_begin * a.k_t, kp, w0, mine, 0);
+        st.issue(vbase + (int64_t)j_begin * a.v_t, vp, w0, mine + TILE, 0);
+        uint32_t mb = mask_byte(mrow, j_begin + STEP, j_end, lane);
+        int buf = 0;
+        for (int j = j_begin; j < j_end; j += STEP) {
+            if (j + STEP < j_end) {
+                w1 = word_at(mb, j + STEP);
+                uint8_t* nl = mine + (buf ^ 1) * STAGE;
+                // the reads of this buffer two blocks ago have returned: the
+                // products that used them are in program order before
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                st.issue(kbase + (int64_t)(j + STEP) * a.k_t, kp, w1, nl, 0);
+                st.issue(vbase + (int64_t)(j + STEP) * a.v_t, vp, w1, nl + TILE, 0);
+                mb = mask_byte(mrow, j + 2 * STEP, j_end, lane);
+                // all but the block just requested (the mask byte is younger)
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+            } else {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
+            const uint8_t* kl = mine + buf * STAGE;
+            const uint8_t* vl = kl + TILE;
+            if (w0 != 0) {
+                f32x16 s[1];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[0][i] = 0.0f;
+#pragma unroll
+                for (int x = 0; x < KS; ++x) {
+                    const i32x4 kf = frag_row<DP>(kl, lane & 31, 2 * x + half);
+                    s[0] = mfma32<DT>(&kf, &qf[x], s[0]);
+                }
+                softmax_step<DT, 1, DB>(s, w0, w0 == ~0u, a.c, m, l, acc, half);
+                i32x4 pf[2];
+                float p[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[i] = s[0][i];
+                pack_frag<DT>(p, pf);
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) {
+                        const i32x4 vf = frag_col<DP>(vl, 16 * g, d, lane);
+                        acc[d] = mfma32<DT>(&vf, &pf[g], acc[d]);
+                    }
+            }
+            w0 = w1;
+            buf ^= 1;
+        }
+    }
+    // join: wave w's rows as floats [rows][DP] over its own first buffer
+    l = sum_halves(l);
+    float* po = reinterpret_cast<float*>(mine);
+    if (row < a.rows) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4*>(po + row * DP + 32 * d + 8 * g + 4 * half) =
+                    f32x4{acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]};
+        if (half == 0) {
+            st_m[wave * 32 + row] = m;
+            st_l[wave * 32 + row] = l;
+        }
+    }
+    __syncthreads();
+    // four values a thread
+    const int per = a.D / 4;
+    for (int e = threadIdx.x; e < a.rows * per; e += NW * 64) {
+        const int r = e / per, d = (e - r * per) * 4;
+        float mm = -__builtin_inff();
+#pragma unroll
+        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, st_m[w * 32 + r]);
+        const float ms = mm == -__builtin_inff() ? 0.0f : mm;
+        float ll = 0.0f;
+        f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float f = __builtin_amdgcn_exp2f(st_m[w * 32 + r] - ms);
+            ll = __builtin_fmaf(st_l[w * 32 + r], f, ll);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(
+                reinterpret_cast<const float*>(lds + w * 2 * STAGE) + r * DP + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
+        }
+        const int64_t bh = (int64_t)b * a.Hk + hk;
+        if (a.nsplit > 1) {
+            const int64_t at = ((int64_t)sp * a.B * a.Hk + bh) * a.rows + r;
+            *reinterpret_cast<f32x4*>(a.part + at * a.D + d) = o;
+            if (d == 0) {
+                a.stat[at * 2] = mm;
+                a.stat[at * 2 + 1] = ll;
+            }
+            continue;
+        }
+        const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
+        const int tok = div_g(a, r);
+        uint8_t* dst = a.out + (int64_t)b * a.o_b + (int64_t)hk * a.G * a.o_h +
+                       packed_off(a, r, a.o_t, a.o_h) + d * 2;
+        *reinterpret_cast<u32x2*>(dst) =
+            u32x2{pack_out2(o[0] * inv, o[1] * inv, DT), pack_out2(o[2] * inv, o[3] * inv, DT)};
+        if (a.lse && d == 0)
+            a.lse[((int64_t)b * a.Hq + hk * a.G + (r - tok * a.G)) * a.Tq + tok] =
+                ll == 0.0f ? -__builtin_inff()
+                           : (mm + __builtin_amdgcn_logf(ll) - p_shift<DT>()) * kLn2;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Join of split launches, splits in order: one thread a row and 4 values.
+template <int DT>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+    const int per = a.D / 4;
+    const int64_t n = (int64_t)a.B * a.Hk * a.rows;
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= n * per) return;
+    const int64_t at = e / per;
+    const int d = (int)(e - at * per) * 4;
+    float mm = -__builtin_inff();
+    for (int s = 0; s < a.nsplit; ++s) mm = fmaxf(mm, a.stat[(s * n + at) * 2]);
+    const float ms = mm == -__builtin_inff() ? 0.0f : mm;
+    float ll = 0.0f;
+    f32x4 o = {0, 0, 0, 0};
+    for (int s = 0; s < a.nsplit; ++s) {
+        const float f = __builtin_amdgcn_exp2f(a.stat[(s * n + at) * 2] - ms);
+        ll = __builtin_fmaf(a.stat[(s * n + at) * 2 + 1], f, ll);
+        const f32x4 x = *reinterpret_cast<const f32x4*>(a.part + (s * n + at) * a.D + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
+    }
+    const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
+    const int64_t bh = at / a.rows;
+    const int r = (int)(at - bh * a.rows);
+    const int b = (int)(bh / a.Hk), hk = (int)(bh - (int64_t)b * a.Hk);
+    const int tok = div_g(a, r);
+    uint8_t* dst = a.out + (int64_t)b * a.o_b + (int64_t)hk * a.G * a.o_h +
+                   packed_off(a, r, a.o_t, a.o_h) + d * 2;
+    *reinterpret_cast<u32x2*>(dst) =
+        u32x2{pack_out2(o[0] * inv, o[1] * inv, DT), pack_out2(o[2] * inv, o[3] * inv, DT)};
+    if (a.lse && d == 0)
+        a.lse[((int64_t)b * a.Hq + hk * a.G + (r - tok * a.G)) * a.Tq + tok] =
+            ll == 0.0f ? -__builtin_inff()
+                       : (mm + __builtin_amdgcn_logf(ll) - p_shift<DT>()) * kLn2;
+}
+
+}  // namespace igc

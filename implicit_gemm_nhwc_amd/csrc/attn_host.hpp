@@ -1,0 +1,36 @@
+// Host-side pieces of the attention operators shared by their translation
+// units: launch plans and per-type launchers.
+#pragma once
+
+#include "attn_common.hpp"
+#include "igemm_host.hpp"
+#include "qk_norm.hpp"
+
+namespace igc {
+
+// Plan of one forward launch (fwd_plan in igemm_attn.hip).
+struct AttnPlan {
+    bool token;       // at most 32 rows a key head: attn_token_kernel
+    int qb;           // 32-row blocks a wave
+    int row_tiles, nsplit, split;
+    int64_t part_floats, stat_floats;   // workspace of split launches
+};
+
+constexpr int kAttnWaves = 4;     // waves a workgroup
+constexpr int kKeyTile = 64;      // keys a tile of the forward kernel
+constexpr int kTokenStep = 128;   // keys a round of the single-token kernel's waves
+
+// D rounded up to the tile widths the kernels are built for.
+inline int padded_dim(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 96 ? 96 : 128; }
+
+template <int DT>
+hipError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, hipStream_t stream);
+
+// Lanes a row of the norm kernels: chunks of 8 values, rounded up to a power
+// of two, at least 4.
+inline int qk_lanes(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : 16; }
+
+template <int DT>
+hipError_t launch_qk_norm(const QkArgs& a, int mode, bool backward, hipStream_t stream);
+
+}  // namespace igc

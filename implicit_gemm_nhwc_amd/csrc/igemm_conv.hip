@@ -12,6 +12,7 @@
 #include <string.h>
 #include <vector>
 
+#include "igemm_attn.h"
 #include "igemm_conv.h"
 #include "igemm_host.hpp"
 #include "igemm_aux_kernels.hpp"
@@ -1539,6 +1540,8 @@ const char* conv2d_reason_string(int32_t reason) {
         case IGC_DECLINE_WORKSPACE: return "workspace";
         case IGC_DECLINE_SIZE_LIMIT: return "size_limit";
         case IGC_DECLINE_EPILOGUE: return "epilogue";
+        case IGC_DECLINE_HEAD_DIM: return "head_dim";
+        case IGC_DECLINE_SCALE: return "scale";
         default: return "unknown";
     }
 }
