@@ -171,11 +171,12 @@ def _load(path):
     L.conv2d_fwd_general_workspace_bytes.argtypes = [i64p, i32, i64p, i64p, prm, i32]
     L.conv2d_fwd_general_workspace_bytes.restype = sz
     buf = ctypes.c_char_p   # the packed argument structs of include/igemm_attn.h
-    for name in ("cross_attn_fwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd"):
+    for name in ("cross_attn_fwd", "cross_attn_bwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd"):
         getattr(L, name).argtypes, getattr(L, name).restype = [buf, vp], i32
         check = getattr(L, name + "_check")
         check.argtypes, check.restype = [buf], i32
-    for name in ("cross_attn_fwd_workspace_bytes", "qk_norm_rope_bwd_workspace_bytes"):
+    for name in ("cross_attn_fwd_workspace_bytes", "cross_attn_bwd_workspace_bytes",
+                 "qk_norm_rope_bwd_workspace_bytes"):
         getattr(L, name).argtypes, getattr(L, name).restype = [buf], sz
     _libs[path] = L
     return L
@@ -830,6 +831,8 @@ def conv2d_general(input, filter, *, filter_is_fcrs, stride=1, dilation=1, pad_b
 
 # -------------------------------------------------- attention operators
 from .attention import (  # noqa: E402,F401
-    cross_attention, cross_attn_fwd, cross_attn_fwd_check, cross_attn_fwd_workspace_bytes,
+    cross_attention, cross_attention_bwd, cross_attn_bwd, cross_attn_bwd_check,
+    cross_attn_bwd_workspace_bytes, cross_attn_fwd, cross_attn_fwd_check,
+    cross_attn_fwd_workspace_bytes,
     qk_norm_rope, qk_norm_rope_bwd, qk_norm_rope_bwd_check, qk_norm_rope_fwd,
     qk_norm_rope_fwd_check, rope_table, rope_table_2d)

@@ -25,6 +25,7 @@ UNITS = [("igemm_conv", "igemm_conv.hip", []), ("igemm_attn", "igemm_attn.hip", 
 for _dt in ("BF16", "FP16"):
     _d = f"-DIGC_DT=igc::DT_{_dt}"
     UNITS += [(f"launch_attn_fwd_{_dt.lower()}", "launch_attn_fwd.hip", [_d]),
+              (f"launch_attn_bwd_{_dt.lower()}", "launch_attn_bwd.hip", [_d]),
               (f"launch_qk_norm_{_dt.lower()}", "launch_qk_norm.hip", [_d])]
 for _dt in ("BF16", "FP16", "FP8"):
     _d = f"-DIGC_DT=igc::DT_{_dt}"

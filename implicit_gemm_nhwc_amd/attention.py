@@ -12,11 +12,12 @@ multiples of 16 bytes; an NHWC map [N, H, W, heads * D] is
 map.view(N, H * W, heads, D).
 
   cross_attn_fwd, cross_attn_fwd_check, cross_attn_fwd_workspace_bytes,
+  cross_attn_bwd, cross_attn_bwd_check, cross_attn_bwd_workspace_bytes,
   qk_norm_rope_fwd, qk_norm_rope_fwd_check,
   qk_norm_rope_bwd, qk_norm_rope_bwd_check, qk_norm_rope_bwd_workspace_bytes
 mirror the C entries (1 handled, 0 declined, < 0 HIP error; outputs and
-workspace given); cross_attention, qk_norm_rope and qk_norm_rope_bwd allocate
-their outputs and raise on failure; rope_table and rope_table_2d make the
+workspace given); cross_attention, cross_attention_bwd, qk_norm_rope and
+qk_norm_rope_bwd allocate their outputs and raise on failure; rope_table and rope_table_2d make the
 rotation's tables.
 """
 import math
@@ -28,6 +29,7 @@ from . import (DTYPE_CODES, REASONS, Declined, InvalidArgument, _ptr, lib)
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1}
 _ATTN = struct.Struct("@26qdqqq")
+_VIEWS = struct.Struct("@16q")   # dout, dq, dk, dv
 _PART = struct.Struct("@21q")
 _QK_TAIL = struct.Struct("@4qdqq")
 _NO_VIEW = (0, 0, 0, 0)
@@ -219,6 +221,76 @@ def cross_attention(q, k, v, *, scale=None, kv_lens=None, key_mask=None, return_
     if rc != 1:
         _raise("cross_attn_fwd", rc, L.cross_attn_fwd_check, packed)
     return (out, lse) if return_lse else out
+
+
+def _grad_views(q, k, v, dout, dq, dk, dv, device):
+    views = _view("dout", dout, q.dtype, device)
+    if dout.shape != q.shape:
+        raise InvalidArgument(f"dout must have q's shape {tuple(q.shape)}")
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is None:
+            views += _NO_VIEW
+            continue
+        views += _view(name, t, q.dtype, device)
+        if t.shape != like.shape:
+            raise InvalidArgument(f"{name} must have {name[1]}'s shape {tuple(like.shape)}")
+    return _VIEWS.pack(*views)
+
+
+def cross_attn_bwd(dout, q, k, v, out, lse, dq, dk, dv, *, kv_lens=None, key_mask=None,
+                   scale=None, workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Enqueue the gradients into dq, dk, dv (dq, or dk and dv, may be None:
+    not wanted).  1 handled, 0 declined, < 0 HIP error."""
+    head, device = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
+    packed = _ATTN.pack(*head, *_work(workspace, workspace_bytes, device)) + _grad_views(
+        q, k, v, dout, dq, dk, dv, device)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return lib().cross_attn_bwd(packed, _raw_stream(device))
+    return lib().cross_attn_bwd(packed, _raw_stream(device))
+
+
+def cross_attn_bwd_check(dout, q, k, v, out, lse, dq, dk, dv, *, kv_lens=None, key_mask=None,
+                         scale=None, workspace=None, workspace_bytes=0) -> int:
+    """Host-only gate of cross_attn_bwd: 0 or a decline reason code."""
+    head, device = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
+    return lib().cross_attn_bwd_check(
+        _ATTN.pack(*head, *_work(workspace, workspace_bytes, device))
+        + _grad_views(q, k, v, dout, dq, dk, dv, device))
+
+
+def cross_attn_bwd_workspace_bytes(q_shape, k_shape, dtype) -> int:
+    """Workspace of a call of these shapes (0 when it would be declined)."""
+    b, tq, hq, d = q_shape
+    _, tk, hk, _ = k_shape
+    return lib().cross_attn_bwd_workspace_bytes(
+        _ATTN.pack(b, tq, tk, hq, hk, d, *(0,) * 20, 1.0, DTYPE_CODES.get(dtype, -1), 0, 0)
+        + bytes(_VIEWS.size))
+
+
+def cross_attention_bwd(dout, q, k, v, out, lse, *, scale=None, kv_lens=None, key_mask=None,
+                        stream=None):
+    """Gradients (dq, dk, dv), dense, of cross_attention at q, k and v from
+    dout, with its out and lse (return_lse) and the same scale, kv_lens and
+    key_mask.  dk and dv sum over the query heads that share a key head."""
+    device = _device(q)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return cross_attention_bwd(dout, q, k, v, out, lse, scale=scale, kv_lens=kv_lens,
+                                       key_mask=key_mask)
+    head, _ = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
+    dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
+    views = _grad_views(q, k, v, dout, dq, dk, dv, device)
+    L = lib()
+    packed = _ATTN.pack(*head, 0, 0) + views
+    need = L.cross_attn_bwd_workspace_bytes(packed)
+    if need:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        packed = _ATTN.pack(*head, ws.data_ptr(), need) + views
+    rc = L.cross_attn_bwd(packed, _raw_stream(device))
+    if rc != 1:
+        _raise("cross_attn_bwd", rc, L.cross_attn_bwd_check, packed)
+    return dq, dk, dv
 
 
 # ------------------------------------------- norm of queries and keys, rotation

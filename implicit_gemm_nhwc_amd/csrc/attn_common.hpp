@@ -28,17 +28,19 @@ struct AttnArgs {
     const uint8_t *q, *k, *v, *o, *dout;
     uint8_t *out, *dq, *dk, *dv;
     float* lse;            // [B][Hq][Tq]
-    const float* delta;    // backward: [B][Hk][rows]
     const int32_t* lens;
     const uint8_t* mask;
-    float *part, *stat;    // partial results of split launches
-    uint32_t* bound;       // backward, fp16: bound of |ds| per (batch, key head), float bits
+    float* part;           // partial results of split launches
+    float* stat;           // their (m, l); backward: [2][B][Hk][rows_pad] lse in powers of two, Delta
+    uint32_t* bound;       // backward, fp16: [B][Hk][bound_n] squared maxima of do and v, float bits
     // strides in bytes
     int64_t q_b, q_t, q_h, k_b, k_t, k_h, v_b, v_t, v_h, o_b, o_t, o_h;
     int64_t do_b, do_t, do_h, dq_b, dq_t, dq_h, dk_b, dk_t, dk_h, dv_b, dv_t, dv_h;
     int64_t mask_b;
     int B, Tq, Tk, Hq, Hk, G, D;
     int rows;       // Tq * G: the queries that share one key head
+    int rows_pad;   // backward: rows rounded up to whole row tiles
+    int bound_n;    // backward: workgroups a (batch, key head) of the row pass
     int row_tiles;  // workgroups along the rows
     int key_tiles;  // backward: workgroups along the keys
     int nsplit;     // workgroups that share a tile's keys (backward dk / dv: its rows)
@@ -167,6 +169,21 @@ __device__ __forceinline__ void pack_frag(const float* p, i32x4* f) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             f[g][j] = (int)pack_out2(p[8 * g + 2 * j], p[8 * g + 2 * j + 1], DT);
+}
+
+// 8 stored values as floats and back (one rounding).
+template <int DT>
+__device__ __forceinline__ void unpack8(const u32x4& u, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = out_to_f32((uint16_t)(u[i] & 0xffff), DT);
+        f[2 * i + 1] = out_to_f32((uint16_t)(u[i] >> 16), DT);
+    }
+}
+template <int DT>
+__device__ __forceinline__ u32x4 pack8(const float* f) {
+    return u32x4{pack_out2(f[0], f[1], DT), pack_out2(f[2], f[3], DT), pack_out2(f[4], f[5], DT),
+                 pack_out2(f[6], f[7], DT)};
 }
 
 // Maximum and sum over a lane and the one 32 away.

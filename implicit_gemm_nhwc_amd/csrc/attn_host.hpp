@@ -16,7 +16,16 @@ struct AttnPlan {
     int64_t part_floats, stat_floats;   // workspace of split launches
 };
 
+// Plan of a backward pass (bwd_plan in igemm_attn.hip).
+struct AttnGradPlan {
+    int rows_pad, bound_n;
+    int key_tiles, kv_nsplit, kv_split;   // dk dv: key tiles, splits of the rows
+    int row_tiles, q_nsplit, q_split;     // dq: row tiles, splits of the keys
+    int64_t stat_floats, bound_words, part_floats;   // workspace
+};
+
 constexpr int kAttnWaves = 4;     // waves a workgroup
+constexpr int kRowTile = 64;      // rows a tile of the dk dv kernel; padding of row statistics
 constexpr int kKeyTile = 64;      // keys a tile of the forward kernel
 constexpr int kTokenStep = 128;   // keys a round of the single-token kernel's waves
 
@@ -25,6 +34,8 @@ inline int padded_dim(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 96 ? 96
 
 template <int DT>
 hipError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, hipStream_t stream);
+template <int DT>
+hipError_t launch_attn_bwd(const AttnArgs& a, const AttnGradPlan& p, hipStream_t stream);
 
 // Lanes a row of the norm kernels: chunks of 8 values, rounded up to a power
 // of two, at least 4.

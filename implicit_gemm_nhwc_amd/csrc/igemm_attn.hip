@@ -1,7 +1,7 @@
 // C-ABI entry points of the attention operators (declarations and contracts
 // in include/igemm_attn.h): the host gates, the launch plans and the
 // workspaces.  Every step of the computation runs in the kernels of
-// attn_fwd.hpp and qk_norm.hpp.
+// attn_fwd.hpp, attn_bwd.hpp and qk_norm.hpp.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -226,6 +226,94 @@ AttnArgs attn_args(const igc_cross_attn* p, const AttnTensors& t) {
     return a;
 }
 
+// Plan of a backward pass from the shapes alone (checked before).
+AttnGradPlan bwd_plan(const igc_cross_attn* p) {
+    AttnGradPlan x{};
+    const int64_t bh = p->batch * p->kv_heads;
+    const int64_t rows = p->kv_heads ? p->q_len * (p->q_heads / p->kv_heads) : 0;
+    const int64_t row64 = ceil_div(rows, kRowTile), key64 = ceil_div(p->kv_len, kKeyTile);
+    if (bh == 0) return x;
+    x.rows_pad = (int)(row64 * kRowTile);
+    // row pass: four workgroups a CU, of 16 rows at least
+    int64_t n = ceil_div(4 * kNumCUs, bh);
+    if (n > x.rows_pad / 16) n = x.rows_pad / 16;
+    if (n > 256) n = 256;
+    x.bound_n = (int)(n < 1 ? 1 : n);
+    // both passes: two workgroups a CU, splits of four tiles at least
+    auto split = [](int64_t groups, int64_t tiles, int64_t unit, int* nsplit, int* len) {
+        int64_t n = groups > 0 ? 2 * kNumCUs / groups : 1;
+        if (n > tiles / 4) n = tiles / 4;
+        if (n < 1) n = 1;
+        const int64_t per = ceil_div(tiles > 0 ? tiles : 1, n);
+        *nsplit = (int)ceil_div(tiles > 0 ? tiles : 1, per);
+        *len = (int)(per * unit < kLim31 ? per * unit : kLim31 - 1);
+    };
+    x.key_tiles = (int)ceil_div(p->kv_len, kAttnWaves * 32);
+    split(bh * x.key_tiles, row64, kRowTile, &x.kv_nsplit, &x.kv_split);
+    x.row_tiles = (int)ceil_div(rows, kAttnWaves * 32);
+    split(bh * x.row_tiles, key64, kKeyTile, &x.q_nsplit, &x.q_split);
+    x.stat_floats = 2 * bh * x.rows_pad;
+    x.bound_words = p->dtype == IGC_DTYPE_FP16 ? 2 * bh * x.bound_n : 0;
+    int64_t f = x.kv_nsplit > 1 ? 2 * x.kv_nsplit * bh * p->kv_len * p->head_dim : 0;
+    const int64_t g = x.q_nsplit > 1 ? x.q_nsplit * bh * rows * p->head_dim : 0;
+    x.part_floats = f > g ? f : g;
+    return x;
+}
+
+size_t bwd_ws(const AttnGradPlan& x) {
+    return (size_t)(x.part_floats + x.stat_floats + x.bound_words) * sizeof(float);
+}
+
+struct GradTensors {
+    AttnTensors f;
+    Tensor g, dq, dk, dv;
+};
+
+int32_t check_bwd(const igc_cross_attn_grad* p, GradTensors* t, AttnGradPlan* plan) {
+    if (!p) return IGC_DECLINE_NULL_POINTER;
+    const igc_cross_attn* f = &p->fwd;
+    int32_t r;
+    if ((r = check_attn_shape(f))) return r;
+    if ((r = check_attn_views(f, &t->f, false))) return r;
+    const int64_t d = f->head_dim;
+    const bool rows = f->batch && f->q_len && f->q_heads;
+    if (rows && !f->lse) return IGC_DECLINE_NULL_POINTER;
+    if ((r = check_view(p->dout, f->batch, f->q_len, f->q_heads, d, false, &t->g))) return r;
+    t->dq = t->dk = t->dv = Tensor{nullptr, 0, 0, 0, 0};
+    if (p->dq.data &&
+        (r = check_view(p->dq, f->batch, f->q_len, f->q_heads, d, true, &t->dq)))
+        return r;
+    if (f->batch && f->kv_len && f->kv_heads && !p->dk.data != !p->dv.data)
+        return IGC_DECLINE_NULL_POINTER;
+    if (p->dk.data) {
+        if ((r = check_view(p->dk, f->batch, f->kv_len, f->kv_heads, d, true, &t->dk))) return r;
+        if ((r = check_view(p->dv, f->batch, f->kv_len, f->kv_heads, d, true, &t->dv))) return r;
+    }
+    const int64_t g = f->kv_heads ? f->q_heads / f->kv_heads : 1;
+    for (const Tensor* x : {&t->f.q, &t->g})
+        if (kRowTile * x->t + g * x->h >= kLim31) return IGC_DECLINE_SIZE_LIMIT;
+    *plan = bwd_plan(f);
+    const int64_t bh = f->batch * f->kv_heads;
+    if (bh * plan->key_tiles > kMaxGrid / (plan->kv_nsplit > 0 ? plan->kv_nsplit : 1) ||
+        bh * plan->row_tiles > kMaxGrid / (plan->q_nsplit > 0 ? plan->q_nsplit : 1) ||
+        bh > kMaxGrid / (plan->bound_n > 0 ? plan->bound_n : 1))
+        return IGC_DECLINE_SIZE_LIMIT;
+    const size_t ws = bwd_ws(*plan);
+    auto meets = [&](const void* w, size_t n) {
+        return meets_inputs(f, t->f, w, n) || meet(w, n, t->f.o.p, t->f.o.bytes) ||
+               meet(w, n, t->g.p, t->g.bytes) || meet(w, n, f->lse, lse_bytes(f));
+    };
+    for (const Tensor* x : {&t->dq, &t->dk, &t->dv})
+        if (meets(x->p, x->bytes) || (f->workspace && meet(f->workspace, ws, x->p, x->bytes)))
+            return IGC_DECLINE_OVERLAP;
+    if (f->workspace && ws) {
+        if (!aligned(f->workspace, 16)) return IGC_DECLINE_ALIGNMENT;
+        if (f->workspace_bytes < ws) return IGC_DECLINE_WORKSPACE;
+        if (meets(f->workspace, ws)) return IGC_DECLINE_OVERLAP;
+    }
+    return IGC_OK;
+}
+
 // ------------------------------------------------- norm and rotation
 int32_t check_qk_shape(const igc_qk_norm* p) {
     if (!p) return IGC_DECLINE_NULL_POINTER;
@@ -407,6 +495,57 @@ int32_t run_qk(const igc_qk_norm* p, bool backward, void* stream) {
 }  // namespace
 
 extern "C" {
+
+int32_t cross_attn_bwd_check(const igc_cross_attn_grad* args) {
+    GradTensors t;
+    AttnGradPlan plan;
+    return check_bwd(args, &t, &plan);
+}
+
+size_t cross_attn_bwd_workspace_bytes(const igc_cross_attn_grad* args) {
+    if (!args || check_attn_shape(&args->fwd) != IGC_OK) return 0;
+    return bwd_ws(bwd_plan(&args->fwd));
+}
+
+int32_t cross_attn_bwd(const igc_cross_attn_grad* args, void* stream) {
+    GradTensors t;
+    AttnGradPlan plan;
+    if (check_bwd(args, &t, &plan) != IGC_OK) return 0;
+    const igc_cross_attn* f = &args->fwd;
+    if (f->batch == 0 || f->kv_heads == 0) return 1;
+    const hipStream_t st = (hipStream_t)stream;
+    AttnArgs a = attn_args(f, t.f);
+    a.o = (const uint8_t*)t.f.o.p;
+    a.dout = (const uint8_t*)t.g.p;
+    a.do_b = t.g.b; a.do_t = t.g.t; a.do_h = t.g.h;
+    a.dq = (uint8_t*)const_cast<void*>(t.dq.p);
+    a.dq_b = t.dq.b; a.dq_t = t.dq.t; a.dq_h = t.dq.h;
+    a.dk = (uint8_t*)const_cast<void*>(t.dk.p);
+    a.dk_b = t.dk.b; a.dk_t = t.dk.t; a.dk_h = t.dk.h;
+    a.dv = (uint8_t*)const_cast<void*>(t.dv.p);
+    a.dv_b = t.dv.b; a.dv_t = t.dv.t; a.dv_h = t.dv.h;
+    a.rows_pad = plan.rows_pad;
+    a.bound_n = plan.bound_n;
+    void* own = nullptr;
+    if (const size_t ws = bwd_ws(plan)) {
+        void* w = f->workspace;
+        if (!w) {
+            const hipError_t e = hipMallocAsync(&own, ws, st);
+            if (e != hipSuccess) return -(int32_t)e;
+            w = own;
+        }
+        a.part = (float*)w;
+        a.stat = a.part + plan.part_floats;
+        a.bound = (uint32_t*)(a.stat + plan.stat_floats);
+    }
+    hipError_t e = f->dtype == IGC_DTYPE_BF16 ? launch_attn_bwd<DT_BF16>(a, plan, st)
+                                              : launch_attn_bwd<DT_FP16>(a, plan, st);
+    if (own) {
+        const hipError_t x = hipFreeAsync(own, st);
+        if (e == hipSuccess) e = x;
+    }
+    return e == hipSuccess ? 1 : -(int32_t)e;
+}
 
 int32_t qk_norm_rope_fwd_check(const igc_qk_norm* args) {
     QkTensors t[2];

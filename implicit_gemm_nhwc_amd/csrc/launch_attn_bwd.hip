@@ -1,0 +1,83 @@
+// Launchers of the cross-attention backward kernels, one element type per
+// translation unit (IGC_DT).
+#include "attn_bwd.hpp"
+#include "attn_host.hpp"
+
+#ifndef IGC_DT
+#error "IGC_DT must name the element type of this translation unit"
+#endif
+
+namespace igc {
+namespace {
+
+template <int DT, int DP>
+hipError_t launch_kv(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
+    auto kern = attn_bwd_kv_kernel<DT, DP, kAttnWaves>;
+    constexpr size_t lds = 2 * (2 * (size_t)kRowTile * DP * 2 + 2 * kRowTile * 4);
+    static LdsAttr attr;
+    hipError_t e = ensure_lds(attr, (const void*)kern, lds);
+    if (e != hipSuccess) return e;
+    a.key_tiles = p.key_tiles;
+    a.nsplit = p.kv_nsplit;
+    a.split = p.kv_split;
+    const int64_t bh = (int64_t)a.B * a.Hk;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(bh * a.nsplit * a.key_tiles)), dim3(kAttnWaves * 64),
+                       lds, stream, a);
+    e = hipGetLastError();
+    if (e != hipSuccess || a.nsplit <= 1) return e;
+    hipLaunchKernelGGL(attn_bwd_join_kernel<DT>,
+                       dim3((unsigned)((bh * a.Tk * (a.D / 4) + 255) / 256), 2), dim3(256), 0,
+                       stream, a, 1);
+    return hipGetLastError();
+}
+
+template <int DT, int DP>
+hipError_t launch_q(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
+    auto kern = attn_bwd_q_kernel<DT, DP, kAttnWaves>;
+    constexpr size_t lds = 4 * (size_t)kKeyTile * DP * 2;
+    static LdsAttr attr;
+    hipError_t e = ensure_lds(attr, (const void*)kern, lds);
+    if (e != hipSuccess) return e;
+    a.row_tiles = p.row_tiles;
+    a.nsplit = p.q_nsplit;
+    a.split = p.q_split;
+    const int64_t bh = (int64_t)a.B * a.Hk;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(bh * a.nsplit * a.row_tiles)), dim3(kAttnWaves * 64),
+                       lds, stream, a);
+    e = hipGetLastError();
+    if (e != hipSuccess || a.nsplit <= 1) return e;
+    hipLaunchKernelGGL(attn_bwd_join_kernel<DT>,
+                       dim3((unsigned)((bh * a.rows * (a.D / 4) + 255) / 256), 1), dim3(256), 0,
+                       stream, a, 0);
+    return hipGetLastError();
+}
+
+template <int DT, int DP>
+hipError_t launch_dp(const AttnArgs& a, const AttnGradPlan& p, hipStream_t stream) {
+    hipError_t e = hipSuccess;
+    if (a.rows > 0) {
+        hipLaunchKernelGGL(attn_bwd_rows_kernel<DT>,
+                           dim3((unsigned)((int64_t)a.B * a.Hk * a.bound_n)), dim3(256), 0, stream,
+                           a);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && a.Tk > 0 && a.dk) e = launch_kv<DT, DP>(a, p, stream);
+    if (e == hipSuccess && a.rows > 0 && a.dq) e = launch_q<DT, DP>(a, p, stream);
+    return e;
+}
+
+}  // namespace
+
+template <int DT>
+hipError_t launch_attn_bwd(const AttnArgs& a, const AttnGradPlan& p, hipStream_t stream) {
+    switch (padded_dim(a.D)) {
+        case 32: return launch_dp<DT, 32>(a, p, stream);
+        case 64: return launch_dp<DT, 64>(a, p, stream);
+        case 96: return launch_dp<DT, 96>(a, p, stream);
+        default: return launch_dp<DT, 128>(a, p, stream);
+    }
+}
+
+template hipError_t launch_attn_bwd<IGC_DT>(const AttnArgs&, const AttnGradPlan&, hipStream_t);
+
+}  // namespace igc

@@ -46,21 +46,6 @@ enum { ROT_HALVES = 0, ROT_HALVES_ANY = 1, ROT_PAIRS = 2 };
 constexpr int kQkHeads = 4;
 constexpr int kQkThreads = 256;
 
-// 8 stored values as floats and back (one rounding).
-template <int DT>
-__device__ __forceinline__ void unpack8(const u32x4& u, float* f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = out_to_f32((uint16_t)(u[i] & 0xffff), DT);
-        f[2 * i + 1] = out_to_f32((uint16_t)(u[i] >> 16), DT);
-    }
-}
-template <int DT>
-__device__ __forceinline__ u32x4 pack8(const float* f) {
-    return u32x4{pack_out2(f[0], f[1], DT), pack_out2(f[2], f[3], DT), pack_out2(f[4], f[5], DT),
-                 pack_out2(f[6], f[7], DT)};
-}
-
 template <int LPR>
 __device__ __forceinline__ float sum_row(float v) {
 #pragma unroll

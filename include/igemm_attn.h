@@ -97,6 +97,39 @@ int32_t cross_attn_fwd_check(const igc_cross_attn* args);
 size_t cross_attn_fwd_workspace_bytes(const igc_cross_attn* args);
 
 /*
+ * Gradients of cross attention from dout, the gradient at out, with out and
+ * lse as cross_attn_fwd left them:
+ *   Delta = dout . out,  dp_j = dout . v_j,  ds_j = p_j (dp_j - Delta)
+ *   dq = scale sum_j ds_j k_j,  dk_j = scale sum ds_j q,  dv_j = sum p_j dout
+ * the last two summed over the query tokens and over the query heads that
+ * share a key head.  Gradients of keys that are not valid are 0.  k and v
+ * that several batch entries share through stride 0 still get one dk and dv
+ * an entry.  dq.data may be NULL, or dk.data and dv.data both (not wanted).
+ *   fwd    the forward's arguments, out and lse now inputs, and the
+ *          workspace of this call
+ * ds and p are rounded to the element type before their products, which
+ * accumulate in fp32 (for fp16 scaled by powers of two that keep them in
+ * range).  Sums are taken in a fixed order.  Limits as the forward; besides,
+ * 64 token strides and one stride over a group's heads, of q and of dout,
+ * together below 2^31 bytes.  dq, dk and dv may interleave in one buffer,
+ * provided no element belongs to two of them.
+ */
+typedef struct igc_cross_attn_grad {
+    igc_cross_attn fwd;
+    igc_attn_view dout, dq, dk, dv;
+} igc_cross_attn_grad;
+
+int32_t cross_attn_bwd(const igc_cross_attn_grad* args, void* stream);
+
+/* Host-only gate of cross_attn_bwd (pointers compared, never dereferenced). */
+int32_t cross_attn_bwd_check(const igc_cross_attn_grad* args);
+
+/* Workspace of cross_attn_bwd: row statistics, and partial sums where few
+ * keys or rows are split over workgroups (0 for arguments that would be
+ * declined; pointers play no part). */
+size_t cross_attn_bwd_workspace_bytes(const igc_cross_attn_grad* args);
+
+/*
  * Norm of queries and keys per head with the position rotation in the same
  * pass.  Every head's D values x of every token, with w = weight (or 1):
  *   r = 1 / sqrt(mean(x^2) + eps),   n_d = x_d * r * w_d
