@@ -20,18 +20,16 @@ workspace given); cross_attention, cross_attention_bwd, qk_norm_rope and
 qk_norm_rope_bwd allocate their outputs and raise on failure; rope_table and rope_table_2d make the
 rotation's tables.
 """
-import math
 import struct
 
 import torch
 
-from . import (DTYPE_CODES, REASONS, Declined, InvalidArgument, _ptr, lib)
+from . import DTYPE_CODES, REASONS, Declined, InvalidArgument, lib
 
-_TYPES = {torch.bfloat16: 0, torch.float16: 1}
 _ATTN = struct.Struct("@26qdqqq")
 _VIEWS = struct.Struct("@16q")   # dout, dq, dk, dv
-_PART = struct.Struct("@21q")
-_QK_TAIL = struct.Struct("@4qdqq")
+_QK = struct.Struct("@42q4qdqq")   # two parts of 21 fields
+_NO_PART = (0,) * 21
 _NO_VIEW = (0, 0, 0, 0)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -40,12 +38,12 @@ def _view(name, t, dtype, device):
     """(pointer, batch, token, head stride) of a [batch, token, head, D] tensor."""
     if not isinstance(t, torch.Tensor):
         raise InvalidArgument(f"{name} must be a tensor")
-    if t.dim() != 4:
-        raise InvalidArgument(f"{name} must be [batch, token, head, D] (got {tuple(t.shape)})")
     if t.dtype != dtype:
         raise InvalidArgument(f"{name} dtype {t.dtype} differs from {dtype}")
     if t.get_device() != device:
         raise InvalidArgument(f"{name} is on {t.device}, the other tensors on GPU {device}")
+    if t.dim() != 4:
+        raise InvalidArgument(f"{name} must be [batch, token, head, D] (got {tuple(t.shape)})")
     sb, st, sh, sd = t.stride()
     if sd != 1 and t.shape[3] > 1:
         raise InvalidArgument(f"{name}: the D values of a head must be adjacent")
@@ -117,34 +115,26 @@ def _raise(name, rc, check, packed):
 
 
 # --------------------------------------------------------- cross attention
-def _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale):
-    """The call's head of igc_cross_attn: sizes, views, side arrays, scale and
+def _attn_head(q, k, v, kv_lens, key_mask, scale):
+    """Sizes and input views of igc_cross_attn, its side arrays with scale and
     type, and the GPU."""
     device = _device(q)
     dtype = q.dtype
-    if dtype not in _TYPES and dtype not in DTYPE_CODES:
+    if dtype not in DTYPE_CODES:
         raise InvalidArgument(f"q dtype {dtype} is not bf16 or fp16")
-    qv = _view("q", q, dtype, device)
-    kv = _view("k", k, dtype, device)
-    vv = _view("v", v, dtype, device)
+    views = _view("q", q, dtype, device) + _view("k", k, dtype, device) + _view(
+        "v", v, dtype, device)
     b, tq, hq, d = q.shape
-    kb, tk, hk, kd = k.shape
-    if kb != b or kd != d or v.shape != k.shape:
-        raise InvalidArgument(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} "
+    ks = k.shape
+    kb, tk, hk, kd = ks
+    if kb != b or kd != d or v.shape != ks:
+        raise InvalidArgument(f"q {tuple(q.shape)}, k {tuple(ks)} and v {tuple(v.shape)} "
                               "do not belong together")
-    if out is None:
-        ov = _NO_VIEW
-    else:
-        ov = _view("out", out, dtype, device)
-        if out.shape != q.shape:
-            raise InvalidArgument(f"out must have q's shape {tuple(q.shape)}")
-    lp = _small("lse", lse, torch.float32, device)
-    if lse is not None and lse.shape != (b, hq, tq):
-        raise InvalidArgument(f"lse must be {(b, hq, tq)} (got {tuple(lse.shape)})")
-    np_ = _small("kv_lens", kv_lens, torch.int32, device)
-    if kv_lens is not None and kv_lens.shape != (b,):
-        raise InvalidArgument(f"kv_lens must be {(b,)} (got {tuple(kv_lens.shape)})")
-    mp = ms = 0
+    np_ = mp = ms = 0
+    if kv_lens is not None:
+        np_ = _small("kv_lens", kv_lens, torch.int32, device)
+        if kv_lens.shape != (b,):
+            raise InvalidArgument(f"kv_lens must be {(b,)} (got {tuple(kv_lens.shape)})")
     if key_mask is not None:
         if key_mask.dtype not in (torch.uint8, torch.bool):
             raise InvalidArgument(f"key_mask must be uint8 or bool (got {key_mask.dtype})")
@@ -157,16 +147,34 @@ def _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale):
             raise InvalidArgument("key_mask: the keys of a batch entry must be adjacent")
         mp = key_mask.data_ptr()
     if scale is None:
-        scale = 1.0 / math.sqrt(d) if d else 1.0
-    code = _TYPES.get(dtype, DTYPE_CODES[dtype] if dtype in DTYPE_CODES else -1)
-    return (b, tq, tk, hq, hk, d, *qv, *kv, *vv, *ov, lp, np_, mp, ms, float(scale), code), device
+        scale = d ** -0.5 if d else 1.0
+    return ((b, tq, tk, hq, hk, d) + views,
+            (np_, mp, ms, float(scale), DTYPE_CODES[dtype]), device)
+
+
+def _attn_args(q, k, v, out, lse, kv_lens, key_mask, scale):
+    """_attn_head with the caller's out and lse: all but the workspace."""
+    head, tail, device = _attn_head(q, k, v, kv_lens, key_mask, scale)
+    ov = _view("out", out, q.dtype, device)
+    if out.shape != q.shape:
+        raise InvalidArgument(f"out must have q's shape {tuple(q.shape)}")
+    lp = _small("lse", lse, torch.float32, device)
+    if lse is not None and lse.shape != (head[0], head[3], head[1]):
+        raise InvalidArgument(f"lse must be {(head[0], head[3], head[1])} "
+                              f"(got {tuple(lse.shape)})")
+    return head + ov + (lp,) + tail, device
+
+
+def _like(t):
+    """A new dense tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def cross_attn_fwd(q, k, v, out, *, lse=None, kv_lens=None, key_mask=None, scale=None,
                    workspace=None, workspace_bytes=0, stream=None) -> int:
     """Enqueue cross attention into out (and lse).  1 handled, 0 declined, < 0
     HIP error."""
-    head, device = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
+    head, device = _attn_args(q, k, v, out, lse, kv_lens, key_mask, scale)
     ws = _work(workspace, workspace_bytes, device)
     if _elsewhere(device, stream):
         with _on(device, stream):
@@ -177,7 +185,7 @@ def cross_attn_fwd(q, k, v, out, *, lse=None, kv_lens=None, key_mask=None, scale
 def cross_attn_fwd_check(q, k, v, out, *, lse=None, kv_lens=None, key_mask=None, scale=None,
                          workspace=None, workspace_bytes=0) -> int:
     """Host-only gate of cross_attn_fwd: 0 or a decline reason code."""
-    head, device = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
+    head, device = _attn_args(q, k, v, out, lse, kv_lens, key_mask, scale)
     return lib().cross_attn_fwd_check(_ATTN.pack(*head, *_work(workspace, workspace_bytes, device)))
 
 
@@ -203,20 +211,20 @@ def cross_attention(q, k, v, *, scale=None, kv_lens=None, key_mask=None, return_
         with _on(device, stream):
             return cross_attention(q, k, v, scale=scale, kv_lens=kv_lens, key_mask=key_mask,
                                    return_lse=return_lse)
-    if q.dim() != 4:
-        raise InvalidArgument(f"q must be [batch, token, head, D] (got {tuple(q.shape)})")
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    head, tail, _ = _attn_head(q, k, v, kv_lens, key_mask, scale)
+    b, tq, _, hq, _, d = head[:6]
+    out = _like(q)
     lse = None
     if return_lse:
-        lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
-                          device=q.device)
-    head, _ = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
+        lse = torch.empty((b, hq, tq), dtype=torch.float32, device=q.device)
+    args = head + (out.data_ptr(), tq * hq * d, hq * d, d,
+                   0 if lse is None else lse.data_ptr()) + tail
     L = lib()
-    packed = _ATTN.pack(*head, 0, 0)
+    packed = _ATTN.pack(*args, 0, 0)
     need = L.cross_attn_fwd_workspace_bytes(packed)
     if need:
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        packed = _ATTN.pack(*head, ws.data_ptr(), need)
+        packed = _ATTN.pack(*args, ws.data_ptr(), need)
     rc = L.cross_attn_fwd(packed, _raw_stream(device))
     if rc != 1:
         _raise("cross_attn_fwd", rc, L.cross_attn_fwd_check, packed)
@@ -241,7 +249,7 @@ def cross_attn_bwd(dout, q, k, v, out, lse, dq, dk, dv, *, kv_lens=None, key_mas
                    scale=None, workspace=None, workspace_bytes=0, stream=None) -> int:
     """Enqueue the gradients into dq, dk, dv (dq, or dk and dv, may be None:
     not wanted).  1 handled, 0 declined, < 0 HIP error."""
-    head, device = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
+    head, device = _attn_args(q, k, v, out, lse, kv_lens, key_mask, scale)
     packed = _ATTN.pack(*head, *_work(workspace, workspace_bytes, device)) + _grad_views(
         q, k, v, dout, dq, dk, dv, device)
     if _elsewhere(device, stream):
@@ -253,7 +261,7 @@ def cross_attn_bwd(dout, q, k, v, out, lse, dq, dk, dv, *, kv_lens=None, key_mas
 def cross_attn_bwd_check(dout, q, k, v, out, lse, dq, dk, dv, *, kv_lens=None, key_mask=None,
                          scale=None, workspace=None, workspace_bytes=0) -> int:
     """Host-only gate of cross_attn_bwd: 0 or a decline reason code."""
-    head, device = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
+    head, device = _attn_args(q, k, v, out, lse, kv_lens, key_mask, scale)
     return lib().cross_attn_bwd_check(
         _ATTN.pack(*head, *_work(workspace, workspace_bytes, device))
         + _grad_views(q, k, v, dout, dq, dk, dv, device))
@@ -278,8 +286,8 @@ def cross_attention_bwd(dout, q, k, v, out, lse, *, scale=None, kv_lens=None, ke
         with _on(device, stream):
             return cross_attention_bwd(dout, q, k, v, out, lse, scale=scale, kv_lens=kv_lens,
                                        key_mask=key_mask)
-    head, _ = _attn_shapes(q, k, v, out, lse, kv_lens, key_mask, scale)
-    dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
+    head, _ = _attn_args(q, k, v, out, lse, kv_lens, key_mask, scale)
+    dq, dk, dv = _like(q), _like(k), _like(v)
     views = _grad_views(q, k, v, dout, dq, dk, dv, device)
     L = lib()
     packed = _ATTN.pack(*head, 0, 0) + views
@@ -294,35 +302,21 @@ def cross_attention_bwd(dout, q, k, v, out, lse, *, scale=None, kv_lens=None, ke
 
 
 # ------------------------------------------- norm of queries and keys, rotation
-def _table(name, t, device):
-    if t is None:
-        return 0, 0, 0
-    if t.dim() != 2:
-        raise InvalidArgument(f"{name} must be [rows, rotated values] (got {tuple(t.shape)})")
-    return _small(name, t, torch.float32, device), t.shape[0], t.shape[1]
-
-
-def _part(n, x, grad, out, weight, dweight, table, positions, dtype, device, d):
-    """One igc_qk_part, packed."""
-    if x is None:
-        return _PART.pack(*(0,) * 17, 0, 0, 0, 0)
-    b, t, h, dd = x.shape
+def _part(n, x, weight, table, positions, dtype, device, d, rot):
+    """Sizes and input view of an igc_qk_part, and what follows its views but
+    for the weight gradient."""
     xv = _view(n, x, dtype, device)
+    b, t, h, dd = x.shape
     if dd != d:
         raise InvalidArgument(f"{n} has heads of {dd}, not {d}")
-    gv, ov = _NO_VIEW, _NO_VIEW
-    if grad is not None:
-        gv = _view("d" + n, grad, dtype, device)
-        if grad.shape != x.shape:
-            raise InvalidArgument(f"d{n} must have {n}'s shape {tuple(x.shape)}")
-    if out is not None:
-        ov = _view(n + " output", out, dtype, device)
-        if out.shape != x.shape:
-            raise InvalidArgument(f"{n}'s output must have its shape {tuple(x.shape)}")
-    for name, w in ((n + "_weight", weight), (n + "_weight gradient", dweight)):
-        if w is not None and w.shape != (d,):
-            raise InvalidArgument(f"{name} must be {(d,)} (got {tuple(w.shape)})")
-    pp = ps = 0
+    wp = tp = rows = pp = ps = 0
+    if weight is not None:
+        wp = _small(n + "_weight", weight, torch.float32, device)
+        if weight.shape != (d,):
+            raise InvalidArgument(f"{n}_weight must be {(d,)} (got {tuple(weight.shape)})")
+    if table is not None:
+        tp = _small(n + "_table", table, torch.float32, device)
+        rows = table.shape[0]
     if positions is not None:
         if positions.dtype != torch.int32:
             raise InvalidArgument(f"{n}_positions must be int32 (got {positions.dtype})")
@@ -335,14 +329,32 @@ def _part(n, x, grad, out, weight, dweight, table, positions, dtype, device, d):
         if inner != 1 and t > 1:
             raise InvalidArgument(f"{n}_positions: the tokens of a batch entry must be adjacent")
         pp = positions.data_ptr()
-    tp, rows, _ = _table(n + "_table", table, device)
-    return _PART.pack(b, t, h, *xv, *gv, *ov, _small(n + "_weight", weight, torch.float32, device),
-                      _small(n + "_weight gradient", dweight, torch.float32, device), tp, rows,
-                      pp, ps)
+    return (b, t, h) + xv, wp, (tp, rows, pp, ps)
 
 
-def _qk_pack(q, k, dq, dk, q_out, k_out, q_weight, k_weight, dq_weight, dk_weight, q_table,
-             k_table, q_positions, k_positions, eps, interleaved, ws):
+def _rotated(x, table, name):
+    """Values that the table turns (0 without one), None for an absent x."""
+    if x is None:
+        return None
+    if table is None:
+        return 0
+    if table.dim() != 2:
+        raise InvalidArgument(f"{name} must be [rows, rotated values] (got "
+                              f"{tuple(table.shape)})")
+    return table.shape[1]
+
+
+def _same_shape(name, t, x, dtype, device):
+    v = _view(name, t, dtype, device)
+    if t.shape != x.shape:
+        raise InvalidArgument(f"{name} must have its input's shape {tuple(x.shape)}")
+    return v
+
+
+def _qk_pack(q, k, grads, outs, dweights, q_weight, k_weight, q_table, k_table, q_positions,
+             k_positions, eps, interleaved, ws=(0, 0)):
+    """igc_qk_norm, packed.  grads and dweights: pairs or None; outs: a pair
+    of tensors to check, or of views of new ones."""
     first = q if q is not None else k
     device = _device(first, "q" if q is not None else "k")
     dtype = first.dtype
@@ -352,16 +364,37 @@ def _qk_pack(q, k, dq, dk, q_out, k_out, q_weight, k_weight, dq_weight, dk_weigh
         raise InvalidArgument(f"tensors must be [batch, token, head, D] (got "
                               f"{tuple(first.shape)})")
     d = first.shape[3]
-    rots = {t.shape[1] for x, t in ((q, q_table), (k, k_table))
-            if x is not None and t is not None and t.dim() == 2}
-    if len(rots) > 1 or (rots and any(x is not None and t is None
-                                      for x, t in ((q, q_table), (k, k_table)))):
+    rot, rot_k = _rotated(q, q_table, "q_table"), _rotated(k, k_table, "k_table")
+    if rot is None:
+        rot = rot_k
+    elif rot_k is not None and rot_k != rot:
         raise InvalidArgument("q_table and k_table must rotate the same number of values")
-    rot = rots.pop() if rots else 0
-    return (_part("q", q, dq, q_out, q_weight, dq_weight, q_table, q_positions, dtype, device, d)
-            + _part("k", k, dk, k_out, k_weight, dk_weight, k_table, k_positions, dtype, device, d)
-            + _QK_TAIL.pack(d, rot, 1 if interleaved else 0, DTYPE_CODES[dtype], float(eps),
-                            *ws)), device
+    flat = ()
+    for i, (n, x, w, tab, pos) in enumerate((("q", q, q_weight, q_table, q_positions),
+                                             ("k", k, k_weight, k_table, k_positions))):
+        if x is None:
+            flat += _NO_PART
+            continue
+        head, wp, tail = _part(n, x, w, tab, pos, dtype, device, d, rot)
+        g = _NO_VIEW if grads is None else _same_shape("d" + n, grads[i], x, dtype, device)
+        o = outs[i]
+        if not isinstance(o, tuple):
+            o = _same_shape(n + " output", o, x, dtype, device)
+        dw = 0
+        if dweights is not None and dweights[i] is not None:
+            dw = dweights[i]
+            if isinstance(dw, torch.Tensor):
+                if dw.shape != (d,):
+                    raise InvalidArgument(f"the gradient of {n}_weight must be {(d,)}")
+                dw = _small(n + "_weight gradient", dw, torch.float32, device)
+        flat += head + g + o + (wp, dw) + tail
+    return _QK.pack(*flat, d, rot, 1 if interleaved else 0, DTYPE_CODES[dtype], eps, *ws), device
+
+
+def _dense(t, shape):
+    """View of a new dense tensor."""
+    _, n, h, d = shape
+    return t.data_ptr(), n * h * d, h * d, d
 
 
 def qk_norm_rope_fwd(q, k, q_out, k_out, *, q_weight=None, k_weight=None, q_table=None,
@@ -370,9 +403,8 @@ def qk_norm_rope_fwd(q, k, q_out, k_out, *, q_weight=None, k_weight=None, q_tabl
     """Enqueue the norm and rotation of q and k (either may be None) into
     q_out, k_out (q and k themselves: in place).  1 handled, 0 declined, < 0
     HIP error."""
-    packed, device = _qk_pack(q, k, None, None, q_out, k_out, q_weight, k_weight, None, None,
-                              q_table, k_table, q_positions, k_positions, eps, interleaved,
-                              (0, 0))
+    packed, device = _qk_pack(q, k, None, (q_out, k_out), None, q_weight, k_weight, q_table,
+                              k_table, q_positions, k_positions, eps, interleaved)
     if _elsewhere(device, stream):
         with _on(device, stream):
             return lib().qk_norm_rope_fwd(packed, _raw_stream(device))
@@ -383,9 +415,9 @@ def qk_norm_rope_fwd_check(q, k, q_out, k_out, *, q_weight=None, k_weight=None, 
                            k_table=None, q_positions=None, k_positions=None, eps=1e-6,
                            interleaved=False) -> int:
     """Host-only gate of qk_norm_rope_fwd: 0 or a decline reason code."""
-    packed, _ = _qk_pack(q, k, None, None, q_out, k_out, q_weight, k_weight, None, None, q_table,
-                         k_table, q_positions, k_positions, eps, interleaved, (0, 0))
-    return lib().qk_norm_rope_fwd_check(packed)
+    return lib().qk_norm_rope_fwd_check(
+        _qk_pack(q, k, None, (q_out, k_out), None, q_weight, k_weight, q_table, k_table,
+                 q_positions, k_positions, eps, interleaved)[0])
 
 
 def qk_norm_rope_bwd_check(dq, dk, q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
@@ -394,10 +426,10 @@ def qk_norm_rope_bwd_check(dq, dk, q, k, dq_out, dk_out, *, q_weight=None, k_wei
                            workspace=None, workspace_bytes=0) -> int:
     """Host-only gate of qk_norm_rope_bwd: 0 or a decline reason code."""
     device = _device(q if q is not None else k)
-    packed, _ = _qk_pack(q, k, dq, dk, dq_out, dk_out, q_weight, k_weight, dq_weight, dk_weight,
-                         q_table, k_table, q_positions, k_positions, eps, interleaved,
-                         _work(workspace, workspace_bytes, device))
-    return lib().qk_norm_rope_bwd_check(packed)
+    return lib().qk_norm_rope_bwd_check(
+        _qk_pack(q, k, (dq, dk), (dq_out, dk_out), (dq_weight, dk_weight), q_weight, k_weight,
+                 q_table, k_table, q_positions, k_positions, eps, interleaved,
+                 _work(workspace, workspace_bytes, device))[0])
 
 
 def qk_norm_rope(q, k=None, *, q_weight=None, k_weight=None, q_table=None, k_table=None,
@@ -414,10 +446,16 @@ def qk_norm_rope(q, k=None, *, q_weight=None, k_weight=None, q_table=None, k_tab
             return qk_norm_rope(q, k, q_weight=q_weight, k_weight=k_weight, q_table=q_table,
                                 k_table=k_table, q_positions=q_positions,
                                 k_positions=k_positions, eps=eps, interleaved=interleaved)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    packed, _ = _qk_pack(q, k, None, None, q_out, k_out, q_weight, k_weight, None, None, q_table,
-                         k_table, q_positions, k_positions, eps, interleaved, (0, 0))
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise InvalidArgument("q and k must be [batch, token, head, D]")
+    q_out = _like(q)
+    if k is None:
+        k_out, outs = None, (_dense(q_out, q.shape), None)
+    else:
+        k_out = _like(k)
+        outs = (_dense(q_out, q.shape), _dense(k_out, k.shape))
+    packed, _ = _qk_pack(q, k, None, outs, None, q_weight, k_weight, q_table, k_table,
+                         q_positions, k_positions, eps, interleaved)
     L = lib()
     rc = L.qk_norm_rope_fwd(packed, _raw_stream(device))
     if rc != 1:
@@ -438,18 +476,26 @@ def qk_norm_rope_bwd(dq, dk, q, k=None, *, q_weight=None, k_weight=None, q_table
             return qk_norm_rope_bwd(dq, dk, q, k, q_weight=q_weight, k_weight=k_weight,
                                     q_table=q_table, k_table=k_table, q_positions=q_positions,
                                     k_positions=k_positions, eps=eps, interleaved=interleaved)
-    d = q.shape[-1]
-    dq_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    dw = torch.empty((1 if k is None else 2, d), dtype=torch.float32, device=q.device)
-    dqw, dkw = dw[0], None if k is None else dw[1]
-    args = (q, k, dq, dk, dq_out, dk_out, q_weight, k_weight, dqw, dkw, q_table, k_table,
-            q_positions, k_positions, eps, interleaved)
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise InvalidArgument("q and k must be [batch, token, head, D]")
+    d = q.shape[3]
+    dw = torch.empty((2, d), dtype=torch.float32, device=q.device)
+    dqw, dkw = dw.unbind(0)
+    dq_out = _like(q)
+    if k is None:
+        dk_out = dkw = None
+        outs, dws = (_dense(dq_out, q.shape), None), (dw.data_ptr(), None)
+    else:
+        dk_out = _like(k)
+        outs = (_dense(dq_out, q.shape), _dense(dk_out, k.shape))
+        dws = (dw.data_ptr(), dw.data_ptr() + 4 * d)
+    packed, _ = _qk_pack(q, k, (dq, dk), outs, dws, q_weight, k_weight, q_table, k_table,
+                         q_positions, k_positions, eps, interleaved)
     L = lib()
-    packed, _ = _qk_pack(*args, (0, 0))
     need = L.qk_norm_rope_bwd_workspace_bytes(packed)
-    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    packed = packed[:-16] + struct.pack("@qq", ws.data_ptr(), need)
+    if need:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        packed = packed[:-16] + struct.pack("@qq", ws.data_ptr(), need)
     rc = L.qk_norm_rope_bwd(packed, _raw_stream(device))
     if rc != 1:
         _raise("qk_norm_rope_bwd", rc, L.qk_norm_rope_bwd_check, packed)

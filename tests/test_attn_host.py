@@ -162,8 +162,8 @@ def _norm(q=None, k=None, d=64, rot=64, inter=0, dtype=0, eps=1e-6, ws=0, ws_byt
                  g_b=100 * h * 64, g_t=h * 64, g_h=64, o=base + (2 << 28), o_b=100 * h * 64,
                  o_t=h * 64, o_h=64, w=0, dw=0, table=T, rows=128, pos=0, pos_b=0)
         f.update(over or {})
-        return A._PART.pack(*f.values())
-    return part(Q, 8, q) + part(K, 4, k) + A._QK_TAIL.pack(d, rot, inter, dtype, eps, ws, ws_bytes)
+        return list(f.values())
+    return A._QK.pack(*part(Q, 8, q), *part(K, 4, k), d, rot, inter, dtype, eps, ws, ws_bytes)
 
 
 def test_norm_good_calls():
@@ -231,7 +231,7 @@ def test_norm_gradient_refusals(kw, reason):
 def test_structs_are_the_headers():
     # 8-byte fields throughout: the packed sizes are those of the C structs
     assert A._ATTN.size == 8 * 30 and A._VIEWS.size == 8 * 16
-    assert A._PART.size == 8 * 21 and A._QK_TAIL.size == 8 * 7
+    assert A._QK.size == 8 * (2 * 21 + 7)
     assert struct.calcsize("P") == 8
 
 
