@@ -457,6 +457,7 @@ __global__ __launch_bounds__(256) void attn_bwd_join_kernel(AttnArgs a, int keys
     const int d = (int)(e - at * per) * 4;
     const float* src = a.part + (blockIdx.y ? a.nsplit * n * a.D : 0) + at * a.D + d;
     f32x4 o = {0, 0, 0, 0};
+#pragma unroll 4
     for (int s = 0; s < a.nsplit; ++s) o += *reinterpret_cast<const f32x4*>(src + s * n * a.D);
     const int64_t bh = at / count;
     const int r = (int)(at - bh * count);

@@ -406,26 +406,43 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Join of split launches, splits in order: one thread a row and 4 values.
+// Join of split launches.  A workgroup takes one packed row: groups of
+// kJoinLanes lanes (4 values a lane) sum every 8th split, and the 8 sums are
+// added in order through LDS.
+constexpr int kJoinLanes = 32;
 template <int DT>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-    const int per = a.D / 4;
+    __shared__ f32x4 part[8][kJoinLanes];
+    __shared__ float sum[8];
     const int64_t n = (int64_t)a.B * a.Hk * a.rows;
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (e >= n * per) return;
-    const int64_t at = e / per;
-    const int d = (int)(e - at * per) * 4;
+    const int64_t at = blockIdx.x;
+    const int g = threadIdx.x / kJoinLanes, d = (threadIdx.x % kJoinLanes) * 4;
+    // the maximum over the splits, by every group of 32 lanes
     float mm = -__builtin_inff();
-    for (int s = 0; s < a.nsplit; ++s) mm = fmaxf(mm, a.stat[(s * n + at) * 2]);
+    for (int s = threadIdx.x % kJoinLanes; s < a.nsplit; s += kJoinLanes)
+        mm = fmaxf(mm, a.stat[(s * n + at) * 2]);
+#pragma unroll
+    for (int o = 1; o < kJoinLanes; o <<= 1) mm = fmaxf(mm, __shfl_xor(mm, o, 64));
     const float ms = mm == -__builtin_inff() ? 0.0f : mm;
     float ll = 0.0f;
     f32x4 o = {0, 0, 0, 0};
-    for (int s = 0; s < a.nsplit; ++s) {
+    for (int s = g; s < a.nsplit; s += 8) {
         const float f = __builtin_amdgcn_exp2f(a.stat[(s * n + at) * 2] - ms);
         ll = __builtin_fmaf(a.stat[(s * n + at) * 2 + 1], f, ll);
-        const f32x4 x = *reinterpret_cast<const f32x4*>(a.part + (s * n + at) * a.D + d);
+        if (d < a.D) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(a.part + (s * n + at) * a.D + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
+            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
+        }
+    }
+    part[g][threadIdx.x % kJoinLanes] = o;
+    if (d == 0) sum[g] = ll;
+    __syncthreads();
+    if (g != 0 || d >= a.D) return;
+    ll = sum[0];
+    for (int i = 1; i < 8; ++i) {
+        ll += sum[i];
+        o += part[i][threadIdx.x];
     }
     const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
     const int64_t bh = at / a.rows;

@@ -41,9 +41,8 @@ hipError_t launch_dp(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
     else if (p.qb == 2) e = launch_rows<DT, DP, 2>(a, stream);
     else e = launch_rows<DT, DP, 1>(a, stream);
     if (e != hipSuccess || a.nsplit <= 1) return e;
-    const int64_t n = (int64_t)a.B * a.Hk * a.rows * (a.D / 4);
-    hipLaunchKernelGGL(attn_join_kernel<DT>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0,
-                       stream, a);
+    const int64_t n = (int64_t)a.B * a.Hk * a.rows;
+    hipLaunchKernelGGL(attn_join_kernel<DT>, dim3((unsigned)n), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

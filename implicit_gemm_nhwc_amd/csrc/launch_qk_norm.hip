@@ -41,7 +41,7 @@ hipError_t launch_qk_norm(const QkArgs& a, int mode, bool backward, hipStream_t 
     else if (lanes == 8) e = launch_mode<DT, 8>(a, mode, backward, stream);
     else e = launch_mode<DT, 16>(a, mode, backward, stream);
     if (e != hipSuccess || !backward || !(a.part[0].dw || a.part[1].dw)) return e;
-    hipLaunchKernelGGL(qk_norm_dw_kernel<DT>, dim3((unsigned)((a.D + 15) / 16), 2), dim3(256), 0,
+    hipLaunchKernelGGL(qk_norm_dw_kernel<DT>, dim3((unsigned)((a.D + 15) / 16), 2), dim3(1024), 0,
                        stream, a, lanes * 8);
     return hipGetLastError();
 }

@@ -61,6 +61,34 @@ struct Turn {
     __device__ __forceinline__ void load(const float* table, int64_t row, bool ok, int R, int c) {
         const float* t = table + row * R;
         const int h = R >> 1;
+        // a chunk that turns as a whole: 16-byte loads (4-byte aligned)
+        typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
+        if constexpr (MODE != ROT_HALVES_ANY) {
+            if (ok && 8 * c + 8 <= R) {
+                if constexpr (MODE == ROT_PAIRS) {
+                    const f32x4a x = *reinterpret_cast<const f32x4a*>(t + 4 * c);
+                    const f32x4a y = *reinterpret_cast<const f32x4a*>(t + h + 4 * c);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        cs[j] = x[j >> 1];
+                        sn[j] = y[j >> 1];
+                    }
+                } else {
+                    const int i = 8 * c < h ? 8 * c : 8 * c - h;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const f32x4a x = *reinterpret_cast<const f32x4a*>(t + i + 4 * k);
+                        const f32x4a y = *reinterpret_cast<const f32x4a*>(t + h + i + 4 * k);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            cs[4 * k + j] = x[j];
+                            sn[4 * k + j] = y[j];
+                        }
+                    }
+                }
+                return;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int e = 8 * c + j;
@@ -251,27 +279,27 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_bwd_kernel(QkArgs a) {
 }
 
 // Sum of the workgroups' partial weight gradients in a fixed order: a
-// workgroup takes 16 values of one part, 16 lanes each over every 16th
-// partial.
+// workgroup takes 16 values of one part, 64 groups of 16 lanes every 64th
+// partial, and the groups' sums are added as a tree.
 template <int DT>
-__global__ __launch_bounds__(256) void qk_norm_dw_kernel(QkArgs a, int width) {
-    __shared__ float sum[16][17];
+__global__ __launch_bounds__(1024) void qk_norm_dw_kernel(QkArgs a, int width) {
+    __shared__ float sum[64][17];
     const int part = blockIdx.y;
     const QkPart& p = a.part[part];
     if (!p.dw) return;
-    const int d = blockIdx.x * 16 + (threadIdx.x & 15), g = threadIdx.x >> 4;
+    const int x = threadIdx.x & 15, g = threadIdx.x >> 4, d = blockIdx.x * 16 + x;
     const float* src = a.partial + (int64_t)(part ? a.part[0].blocks : 0) * width;
     float s = 0.0f;
-    if (d < width)
-        for (int i = g; i < p.blocks; i += 16) s += src[(int64_t)i * width + d];
-    sum[g][threadIdx.x & 15] = s;
-    __syncthreads();
-    if (g == 0 && d < a.D) {
-        s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s += sum[i][threadIdx.x];
-        p.dw[d] = s;
+    if (d < width) {
+#pragma unroll 8
+        for (int i = g; i < p.blocks; i += 64) s += src[(int64_t)i * width + d];
     }
+    sum[g][x] = s;
+    for (int n = 32; n; n >>= 1) {
+        __syncthreads();
+        if (g < n) sum[g][x] += sum[g + n][x];
+    }
+    if (g == 0 && d < a.D) p.dw[d] = sum[0][x];
 }
 
 }  // namespace igc
