@@ -27,26 +27,29 @@ namespace igc {
 // |do| (|v| + |o|) <= 2 max|do| max|v| (o is a mean of v rows), so with the
 // head's maxima the largest power that keeps it under 2^15 is known before
 // the first product.  bf16 has fp32's exponent range and takes 1.
+__device__ __forceinline__ float range_scale(float s) {
+    if (!(s > 0.0f) || !(s < 3e38f)) return 1.0f;
+    int e;
+    frexpf(s, &e);   // s < 2^e
+    return ldexpf(1.0f, min(max(14 - e, -100), 100));
+}
+
 template <int DT>
 __device__ __forceinline__ float ds_scale(const AttnArgs& a, int64_t bh, int lane) {
     if constexpr (DT != DT_FP16) return 1.0f;
     const float* p = reinterpret_cast<const float*>(a.bound) + bh * a.bound_n * 2;
     float g = 0.0f, v = 0.0f;
-    for (int i = lane; i < a.bound_n; i += 64) {
-        g = fmaxf(g, p[2 * i]);
-        v = fmaxf(v, p[2 * i + 1]);
+    for (int i = 0; i < a.bound_n; i += 64) {
+        const int x = min(i + lane, a.bound_n - 1);
+        g = fmaxf(g, p[2 * x]);
+        v = fmaxf(v, p[2 * x + 1]);
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) {
         g = fmaxf(g, __shfl_xor(g, o, 64));
         v = fmaxf(v, __shfl_xor(v, o, 64));
     }
-    const float s = 2.0f * sqrtf(g) * sqrtf(v);
-    if (!(s > 0.0f) || !(s < 3e38f)) return 1.0f;
-    int e;
-    frexpf(s, &e);   // s < 2^e
-    e = min(max(14 - e, -100), 100);
-    return ldexpf(1.0f, e);
+    return range_scale(2.0f * sqrtf(g) * sqrtf(v));
 }
 
 // Delta and lse of the packed rows [bh][rows_pad], and for fp16 the squared
@@ -68,8 +71,9 @@ __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnArgs a) {
         float s = 0.0f, n = 0.0f;
         if (live && on) {
             float x[8], g[8];
-            unpack8<DT>(*reinterpret_cast<const u32x4*>(ob + packed_off(a, r, a.o_t, a.o_h)), x);
-            unpack8<DT>(*reinterpret_cast<const u32x4*>(gb + packed_off(a, r, a.do_t, a.do_h)), g);
+            const int tok = div_g(a, r), h = r - tok * a.G;
+            unpack8<DT>(*reinterpret_cast<const u32x4*>(ob + tok * a.o_t + h * a.o_h), x);
+            unpack8<DT>(*reinterpret_cast<const u32x4*>(gb + tok * a.do_t + h * a.do_h), g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 s = __builtin_fmaf(x[j], g[j], s);
@@ -136,28 +140,11 @@ __device__ __forceinline__ void issue_packed(const TileStage<DP, ROWS, NW>& st, 
     for (int i = 0; i < TileStage<DP, ROWS, NW>::PER; ++i) {
         if (!TileStage<DP, ROWS, NW>::EVEN && i * NW + wave >= TileStage<DP, ROWS, NW>::PIECES)
             break;
-        const int r = r0 + st.row[i];
-        const int tok = div_g(a, r);
-        const bool ok = st.chunk[i] >= 0 && r < a.rows;
-        const unsigned off = ok ? (unsigned)(tok - t0) * (unsigned)pt +
-                                      (unsigned)(r - tok * a.G) * (unsigned)ph +
-                                      (unsigned)st.chunk[i]
-                                : kOut;
+        const unsigned at = packed_off(a, r0 + st.row[i], t0, pt, ph) + (unsigned)st.chunk[i];
+        const unsigned off = st.chunk[i] >= 0 ? at : kOut;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rs, (__attribute__((address_space(3))) void*)(lds + (i * NW + wave) * 1024), 16, off,
             0, 0, 0);
-    }
-}
-
-// Store of fp32 partial sums: lane's row `o` (or null), block of 32 values.
-__device__ __forceinline__ void store_part(float* o, const f32x16& v, float f, int d0, int D,
-                                           int half) {
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int d = d0 + 8 * g + 4 * half;
-        if (o && d < D)
-            *reinterpret_cast<f32x4*>(o + d) =
-                f32x4{v[4 * g] * f, v[4 * g + 1] * f, v[4 * g + 2] * f, v[4 * g + 3] * f};
     }
 }
 
@@ -184,26 +171,21 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_bwd_kv_kernel(A
     const int bh = idx / a.nsplit;
     const int hk = bh % a.Hk, b = bh / a.Hk;
     const int len = a.lens ? max(0, min(a.lens[b], a.Tk)) : a.Tk;
-    const int key = (kt * NW + wave) * 32 + (lane & 31);
+    const int key0 = (kt * NW + wave) * 32, kr = lane & 31;
     const uint8_t* mrow = a.mask ? a.mask + (int64_t)b * a.mask_b : nullptr;
-    const bool valid = key < len && (!mrow || mrow[key]);
+    const bool valid = mask_byte(mrow, key0, len, kr) != 0 && key0 + kr < len;
     // the whole workgroup's keys may be out of range: nothing to sum then
     const int r_begin = sp * a.split;
     const int r_end = kt * NW * 32 < len ? min(a.rows, r_begin + a.split) : r_begin;
+    const bool idle = !__any(valid);   // this wave then only stages
 
     i32x4 kf[KS], vf[KS];
     f32x16 dk[DB], dv[DB];
     {
-        const uint8_t* kp = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h +
-                            (valid ? (int64_t)key * a.k_t : 0) + 16 * half;
-        const uint8_t* vp = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h +
-                            (valid ? (int64_t)key * a.v_t : 0) + 16 * half;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const bool on = valid && 16 * s + 8 * half < a.D;
-            kf[s] = on ? *reinterpret_cast<const i32x4*>(kp + 32 * s) : i32x4{0, 0, 0, 0};
-            vf[s] = on ? *reinterpret_cast<const i32x4*>(vp + 32 * s) : i32x4{0, 0, 0, 0};
-        }
+        const uint8_t* kp = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h + (int64_t)key0 * a.k_t;
+        const uint8_t* vp = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h + (int64_t)key0 * a.v_t;
+        load_rows<DP>(attn_rsrc(kp), valid ? (unsigned)kr * (unsigned)a.k_t : kOut, a.D, half, kf);
+        load_rows<DP>(attn_rsrc(vp), valid ? (unsigned)kr * (unsigned)a.v_t : kOut, a.D, half, vf);
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -223,11 +205,11 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_bwd_kv_kernel(A
     auto issue = [&](int r0, uint8_t* to) {
         issue_packed(st, a, qbase, a.q_t, a.q_h, r0, to, wave);
         issue_packed(st, a, gbase, a.do_t, a.do_h, r0, to + TILE, wave);
-        if (wave < 2) {   // 64 floats each: lse, Delta
-            const float* src = (wave ? delta : lse2) + r0;
+        for (int x = wave; x < 2; x += NW) {   // 64 floats each: lse, Delta
+            const float* src = (x ? delta : lse2) + r0;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 attn_rsrc(src),
-                (__attribute__((address_space(3))) void*)(to + 2 * TILE + wave * QT * 4), 4,
+                (__attribute__((address_space(3))) void*)(to + 2 * TILE + x * QT * 4), 4,
                 lane * 4, 0, 0, 0);
         }
     };
@@ -241,6 +223,7 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_bwd_kv_kernel(A
             const uint8_t* gl = ql + TILE;
             const float* ls = reinterpret_cast<const float*>(ql + 2 * TILE);
             if (r0 + QT < r_end) issue(r0 + QT, lds + (buf ^ 1) * STAGE);
+            if (!idle)
 #pragma unroll
             for (int rb = 0; rb < QT / 32; ++rb) {
                 f32x16 s, dp;
@@ -295,32 +278,36 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_bwd_kv_kernel(A
         }
     }
     const float fk = a.scale / f, fv = DT == DT_FP16 ? 0.00006103515625f : 1.0f;
-    if (!valid) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.0f;
-    }
-    const bool live = key < a.Tk;
+        for (int i = 0; i < 16; ++i) {
+            dk[d][i] = valid ? dk[d][i] : 0.0f;
+            dv[d][i] = valid ? dv[d][i] : 0.0f;
+        }
+    const bool live = key0 + kr < a.Tk;
     if (a.nsplit > 1) {
         const int64_t n = (int64_t)a.B * a.Hk * a.Tk * a.D;
-        float* o = live ? a.part + sp * n + ((int64_t)bh * a.Tk + key) * a.D : nullptr;
-        float* o2 = live ? o + a.nsplit * n : nullptr;
+        float* o = a.part + sp * n + ((int64_t)bh * a.Tk + key0) * a.D;
+        const __amdgpu_buffer_rsrc_t k1 = attn_rsrc(o), v1 = attn_rsrc(o + a.nsplit * n);
+        const unsigned off = live ? (unsigned)(kr * a.D) * 4 : kOut;
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
-            store_part(o, dk[d], fk, 32 * d, a.D, half);
-            store_part(o2, dv[d], fv, 32 * d, a.D, half);
+            store_part(k1, off, dk[d], fk, 32 * d, a.D, half);
+            store_part(v1, off, dv[d], fv, 32 * d, a.D, half);
         }
         return;
     }
-    uint8_t* ko = live ? a.dk + (int64_t)b * a.dk_b + (int64_t)hk * a.dk_h + (int64_t)key * a.dk_t
-                       : nullptr;
-    uint8_t* vo = live ? a.dv + (int64_t)b * a.dv_b + (int64_t)hk * a.dv_h + (int64_t)key * a.dv_t
-                       : nullptr;
+    const __amdgpu_buffer_rsrc_t ko = attn_rsrc(a.dk + (int64_t)b * a.dk_b +
+                                                (int64_t)hk * a.dk_h + (int64_t)key0 * a.dk_t);
+    const __amdgpu_buffer_rsrc_t vo = attn_rsrc(a.dv + (int64_t)b * a.dv_b +
+                                                (int64_t)hk * a.dv_h + (int64_t)key0 * a.dv_t);
+    const unsigned koff = live ? (unsigned)kr * (unsigned)a.dk_t : kOut;
+    const unsigned voff = live ? (unsigned)kr * (unsigned)a.dv_t : kOut;
 #pragma unroll
     for (int d = 0; d < DB; ++d) {
-        store_block<DT>(ko, dk[d], fk, 32 * d, a.D, half);
-        store_block<DT>(vo, dv[d], fv, 32 * d, a.D, half);
+        store_block<DT>(ko, koff, dk[d], fk, 32 * d, a.D, half);
+        store_block<DT>(vo, voff, dv[d], fv, 32 * d, a.D, half);
     }
 }
 
@@ -345,15 +332,21 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_bwd_q_kernel(AttnArgs a) {
     const int len = a.lens ? max(0, min(a.lens[b], a.Tk)) : a.Tk;
     const int j_begin = sp * a.split, j_end = min(len, j_begin + a.split);
 
-    const int row = (rt * NW + wave) * 32 + (lane & 31);
+    const int row0 = (rt * NW + wave) * 32, row = row0 + (lane & 31), t0 = div_g(a, row0);
     i32x4 qf[KS], gf[KS];
-    load_rows<DP>(a, a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h, a.q_t, a.q_h, row, half,
-                  qf);
-    load_rows<DP>(a, a.dout + (int64_t)b * a.do_b + (int64_t)hk * a.G * a.do_h, a.do_t, a.do_h,
-                  row, half, gf);
+    load_rows<DP>(attn_rsrc(a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h +
+                            (int64_t)t0 * a.q_t),
+                  packed_off(a, row, t0, a.q_t, a.q_h), a.D, half, qf);
+    load_rows<DP>(attn_rsrc(a.dout + (int64_t)b * a.do_b + (int64_t)hk * a.G * a.do_h +
+                            (int64_t)t0 * a.do_t),
+                  packed_off(a, row, t0, a.do_t, a.do_h), a.D, half, gf);
     const bool live = row < a.rows;
-    const float L = live ? a.stat[(int64_t)bh * a.rows_pad + row] : __builtin_inff();
-    const float De = live ? a.stat[((int64_t)a.B * a.Hk + bh) * a.rows_pad + row] : 0.0f;
+    // padding rows have statistics, rows past the padding read as 0: their
+    // results are not stored
+    const unsigned soff = row < a.rows_pad ? (unsigned)(lane & 31) * 4 : kOut;
+    const float L = load4(attn_rsrc(a.stat + (int64_t)bh * a.rows_pad + row0), soff);
+    const float De =
+        load4(attn_rsrc(a.stat + ((int64_t)a.B * a.Hk + bh) * a.rows_pad + row0), soff);
     const float f = ds_scale<DT>(a, bh, lane);
     f32x16 dq[DB];
 #pragma unroll
@@ -431,16 +424,18 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_bwd_q_kernel(AttnArgs a) {
     const float fq = a.scale / f;
     if (a.nsplit > 1) {
         const int64_t n = (int64_t)a.B * a.Hk * a.rows * a.D;
-        float* o = live ? a.part + sp * n + ((int64_t)bh * a.rows + row) * a.D : nullptr;
+        const __amdgpu_buffer_rsrc_t rs =
+            attn_rsrc(a.part + sp * n + ((int64_t)bh * a.rows + row0) * a.D);
+        const unsigned off = live ? (unsigned)((lane & 31) * a.D) * 4 : kOut;
 #pragma unroll
-        for (int d = 0; d < DB; ++d) store_part(o, dq[d], fq, 32 * d, a.D, half);
+        for (int d = 0; d < DB; ++d) store_part(rs, off, dq[d], fq, 32 * d, a.D, half);
         return;
     }
-    uint8_t* dst = live ? a.dq + (int64_t)b * a.dq_b + (int64_t)hk * a.G * a.dq_h +
-                              packed_off(a, row, a.dq_t, a.dq_h)
-                        : nullptr;
+    const __amdgpu_buffer_rsrc_t rs = attn_rsrc(a.dq + (int64_t)b * a.dq_b +
+                                                (int64_t)hk * a.G * a.dq_h + (int64_t)t0 * a.dq_t);
+    const unsigned off = packed_off(a, row, t0, a.dq_t, a.dq_h);
 #pragma unroll
-    for (int d = 0; d < DB; ++d) store_block<DT>(dst, dq[d], fq, 32 * d, a.D, half);
+    for (int d = 0; d < DB; ++d) store_block<DT>(rs, off, dq[d], fq, 32 * d, a.D, half);
 }
 
 // ---------------------------------------------------------------------------
@@ -463,9 +458,10 @@ __global__ __launch_bounds__(256) void attn_bwd_join_kernel(AttnArgs a, int keys
     const int r = (int)(at - bh * count);
     const int b = (int)(bh / a.Hk), hk = (int)(bh - (int64_t)b * a.Hk);
     uint8_t* dst;
+    const int tok = div_g(a, r);
     if (!keys)
-        dst = a.dq + (int64_t)b * a.dq_b + (int64_t)hk * a.G * a.dq_h +
-              packed_off(a, r, a.dq_t, a.dq_h);
+        dst = a.dq + (int64_t)b * a.dq_b + (int64_t)hk * a.G * a.dq_h + (int64_t)tok * a.dq_t +
+              packed_off(a, r, tok, a.dq_t, a.dq_h);
     else if (blockIdx.y == 0)
         dst = a.dk + (int64_t)b * a.dk_b + (int64_t)hk * a.dk_h + (int64_t)r * a.dk_t;
     else

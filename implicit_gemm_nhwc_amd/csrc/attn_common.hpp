@@ -53,7 +53,8 @@ struct AttnArgs {
 
 // row / G by the host's multiplier (exact for row < 2^31).
 __device__ __forceinline__ int div_g(const AttnArgs& a, int row) {
-    return a.g_mul ? (int)(__umulhi((uint32_t)row, a.g_mul) >> a.g_shift) : row;
+    const int q = (int)(__umulhi((uint32_t)row, a.g_mul) >> a.g_shift);
+    return a.g_mul ? q : row;
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t attn_rsrc(const void* base) {
@@ -61,7 +62,45 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t attn_rsrc(const void* base) {
                                              0x00020000);
 }
 // A buffer offset past the range: loads return zero, stores are dropped.
+// Every masked access of these kernels goes this way, by selecting the
+// offset, and none by a branch on the lane: the kernels fill the register
+// file, and where a value is moved to an accumulation register at the join of
+// such a branch the compiler was seen to put the copy before the execution
+// mask is restored, which loses the other lanes' values.
 constexpr unsigned kOut = 0x80000000u;
+
+__device__ __forceinline__ u32x4 load16(const __amdgpu_buffer_rsrc_t& rs, unsigned off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+}
+__device__ __forceinline__ float load4(const __amdgpu_buffer_rsrc_t& rs, unsigned off) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
+}
+__device__ __forceinline__ void store16(const __amdgpu_buffer_rsrc_t& rs, unsigned off, u32x4 v) {
+    typedef decltype(__builtin_amdgcn_raw_buffer_load_b128(rs, 0, 0, 0)) V;
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(V, v), rs, off, 0, 0);
+}
+__device__ __forceinline__ void store4(const __amdgpu_buffer_rsrc_t& rs, unsigned off, float v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rs, off, 0, 0);
+}
+
+// Row `row` of the packed queries: byte offset of its (token, head) from
+// token t0 and the first head of the group; rows past the last get kOut.
+__device__ __forceinline__ unsigned packed_off(const AttnArgs& a, int row, int t0, int64_t st,
+                                               int64_t sh) {
+    const int tok = div_g(a, row);
+    const unsigned off = (unsigned)(tok - t0) * (unsigned)st +
+                         (unsigned)(row - tok * a.G) * (unsigned)sh;
+    return row < a.rows ? off : kOut;
+}
+
+// lse entry of a packed row of key head hk, from lse_base.
+__device__ __forceinline__ unsigned lse_off(const AttnArgs& a, int row) {
+    const int tok = div_g(a, row);
+    return row < a.rows ? (unsigned)((row - tok * a.G) * a.Tq + tok) * 4 : kOut;
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t lse_base(const AttnArgs& a, int b, int hk) {
+    return attn_rsrc(a.lse + ((int64_t)b * a.Hq + hk * a.G) * a.Tq);
+}
 
 // LDS tiles hold rows of DP elements (DP = D rounded up to 32), the 16-byte
 // chunk c of row r at c ^ lds_swz(r).  Two patterns read them: whole chunks
@@ -121,7 +160,8 @@ __device__ __forceinline__ uint64_t mask_word(uint32_t mb, int left) {
 // Mask byte of key j0 + lane for mask_word; reads only keys before `end`.
 __device__ __forceinline__ uint32_t mask_byte(const uint8_t* row, int j0, int end, int lane) {
     if (!row) return 1;
-    return j0 + lane < end ? row[j0 + lane] : 0;
+    return __builtin_amdgcn_raw_buffer_load_b8(attn_rsrc(row + j0),
+                                               lane < end - j0 ? (unsigned)lane : kOut, 0, 0);
 }
 
 // Direct loads of a tile of ROWS rows into LDS by NW waves: each wave writes
@@ -153,7 +193,8 @@ struct TileStage {
         for (int i = 0; i < PER; ++i) {
             if (!EVEN && i * NW + wave >= PIECES) break;
             const bool ok = chunk[i] >= 0 && ((valid >> row[i]) & 1);
-            const unsigned off = ok ? (unsigned)row[i] * pitch + (unsigned)chunk[i] : kOut;
+            const unsigned at = (unsigned)row[i] * pitch + (unsigned)chunk[i];
+            const unsigned off = ok ? at : kOut;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rs, (__attribute__((address_space(3))) void*)(lds + (i * NW + wave) * 1024), 16,
                 off, 0, 0, 0);
@@ -208,11 +249,11 @@ __device__ __forceinline__ float sum_halves(float x) {
 // Store of a result block whose columns are tensor rows and whose rows are
 // 32 values of the head axis: register 4 g + i of half h is value
 // 8 g + 4 h + i.  After exchanging halves each lane holds 8 adjacent values:
-// half h takes the groups g = h and 2 + h.  dst is the lane's row (NULL: no
+// half h takes the groups g = h and 2 + h.  off is the lane's row (kOut: no
 // store), d0 the block's first value, values at or past D are not stored.
 template <int DT>
-__device__ __forceinline__ void store_block(uint8_t* dst, const f32x16& v, float f, int d0, int D,
-                                            int half) {
+__device__ __forceinline__ void store_block(const __amdgpu_buffer_rsrc_t& rs, unsigned off,
+                                            const f32x16& v, float f, int d0, int D, int half) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = pack_out2(v[2 * i] * f, v[2 * i + 1] * f, DT);
@@ -222,8 +263,31 @@ __device__ __forceinline__ void store_block(uint8_t* dst, const f32x16& v, float
         const auto a = __builtin_amdgcn_permlane32_swap(w[4 * gg], w[4 * gg + 2], false, false);
         const auto b = __builtin_amdgcn_permlane32_swap(w[4 * gg + 1], w[4 * gg + 3], false, false);
         const int d = d0 + 16 * gg + 8 * half;
-        if (dst && d < D)
-            *reinterpret_cast<u32x4*>(dst + d * 2) = u32x4{a[0], b[0], a[1], b[1]};
+        store16(rs, d < D ? off + 2 * d : kOut, u32x4{a[0], b[0], a[1], b[1]});
+    }
+}
+
+// The same block as fp32 values (partial sums of split launches).
+__device__ __forceinline__ void store_part(const __amdgpu_buffer_rsrc_t& rs, unsigned off,
+                                           const f32x16& v, float f, int d0, int D, int half) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int d = d0 + 8 * g + 4 * half;
+        store16(rs, d < D ? off + 4 * d : kOut,
+                __builtin_bit_cast(u32x4, f32x4{v[4 * g] * f, v[4 * g + 1] * f, v[4 * g + 2] * f,
+                                                v[4 * g + 3] * f}));
+    }
+}
+
+// A block of 32 rows as operands, one row a lane: `off` the lane's row (kOut:
+// zeros); values past D are zero.
+template <int DP>
+__device__ __forceinline__ void load_rows(const __amdgpu_buffer_rsrc_t& rs, unsigned off, int D,
+                                          int half, i32x4 (&f)[DP / 16]) {
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) {
+        const int d = 16 * s + 8 * half;
+        f[s] = __builtin_bit_cast(i32x4, load16(rs, d < D ? off + 2 * d : kOut));
     }
 }
 

@@ -71,68 +71,36 @@ __device__ __forceinline__ void softmax_step(f32x16 (&s)[KB], uint64_t word, boo
     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
-// Row `row` of the packed queries: byte offset of its (token, head) from the
-// batch and first head of the group.
-__device__ __forceinline__ int64_t packed_off(const AttnArgs& a, int row, int64_t st, int64_t sh) {
-    const int tok = div_g(a, row);
-    return (int64_t)tok * st + (int64_t)(row - tok * a.G) * sh;
-}
-
-// Results of one block of 32 rows (row of this lane: `row`): the final
-// output, or the partial result of one split.
+// Results of a block of 32 rows from row0 (this lane's: row0 + lane % 32):
+// the final output, or the partial result of one split.
 template <int DT, int DB>
-__device__ __forceinline__ void fwd_finish(const AttnArgs& a, int b, int hk, int sp, int row,
-                                           f32x16 (&acc)[DB], float m, float l, int half) {
+__device__ __forceinline__ void fwd_finish(const AttnArgs& a, int b, int hk, int sp, int row0,
+                                           int lane, f32x16 (&acc)[DB], float m, float l) {
+    const int half = lane >> 5, r = lane & 31, row = row0 + r;
     l = sum_halves(l);
     const bool live = row < a.rows;
     if (a.nsplit > 1) {
         const int64_t bh = (int64_t)b * a.Hk + hk;
-        const int64_t at = ((int64_t)sp * a.B * a.Hk + bh) * a.rows + row;
-        if (live) {
-            float* o = a.part + at * a.D;
+        const int64_t at = ((int64_t)sp * a.B * a.Hk + bh) * a.rows + row0;
+        const __amdgpu_buffer_rsrc_t rs = attn_rsrc(a.part + at * a.D);
+        const unsigned off = live ? (unsigned)(r * a.D) * 4 : kOut;
 #pragma unroll
-            for (int db = 0; db < DB; ++db)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int d = 32 * db + 8 * g + 4 * half;
-                    if (d < a.D)
-                        *reinterpret_cast<f32x4*>(o + d) =
-                            f32x4{acc[db][4 * g], acc[db][4 * g + 1], acc[db][4 * g + 2],
-                                  acc[db][4 * g + 3]};
-                }
-            if (half == 0) {
-                a.stat[at * 2] = m;
-                a.stat[at * 2 + 1] = l;
-            }
-        }
+        for (int db = 0; db < DB; ++db) store_part(rs, off, acc[db], 1.0f, 32 * db, a.D, half);
+        store4(attn_rsrc(a.stat + at * 2), live ? (unsigned)(r * 2 + half) * 4 : kOut,
+               half ? l : m);
         return;
     }
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays NaN
-    uint8_t* dst = live ? a.out + (int64_t)b * a.o_b + (int64_t)hk * a.G * a.o_h +
-                              packed_off(a, row, a.o_t, a.o_h)
-                        : nullptr;
+    const int t0 = div_g(a, row0);
+    const __amdgpu_buffer_rsrc_t rs = attn_rsrc(a.out + (int64_t)b * a.o_b +
+                                                (int64_t)hk * a.G * a.o_h + (int64_t)t0 * a.o_t);
+    const unsigned off = packed_off(a, row, t0, a.o_t, a.o_h);
 #pragma unroll
-    for (int db = 0; db < DB; ++db) store_block<DT>(dst, acc[db], inv, 32 * db, a.D, half);
-    if (a.lse && live && half == 0) {
-        const int tok = div_g(a, row);
-        const int64_t h = (int64_t)b * a.Hq + hk * a.G + (row - tok * a.G);
-        // l carries 2^p_shift
-        a.lse[h * a.Tq + tok] =
-            l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l) - p_shift<DT>()) * kLn2;
-    }
-}
-
-// The wave's query block as B operands: rows past the last are zero, as are
-// values past D.
-template <int DP>
-__device__ __forceinline__ void load_rows(const AttnArgs& a, const uint8_t* base, int64_t st,
-                                          int64_t sh, int row, int half, i32x4 (&f)[DP / 16]) {
-    const bool live = row < a.rows;
-    const uint8_t* p = base + (live ? packed_off(a, row, st, sh) : 0) + 16 * half;
-#pragma unroll
-    for (int s = 0; s < DP / 16; ++s)
-        f[s] = live && 16 * s + 8 * half < a.D ? *reinterpret_cast<const i32x4*>(p + 32 * s)
-                                               : i32x4{0, 0, 0, 0};
+    for (int db = 0; db < DB; ++db) store_block<DT>(rs, off, acc[db], inv, 32 * db, a.D, half);
+    if (a.lse)   // l carries 2^p_shift
+        store4(lse_base(a, b, hk), half == 0 ? lse_off(a, row) : kOut,
+               l == 0.0f ? -__builtin_inff()
+                         : (m + __builtin_amdgcn_logf(l) - p_shift<DT>()) * kLn2);
 }
 
 // ---------------------------------------------------------------------------
@@ -157,15 +125,16 @@ __global__ __launch_bounds__(NW * 64, QB == 1 ? 2 : 1) void attn_fwd_kernel(Attn
     const int len = a.lens ? max(0, min(a.lens[b], a.Tk)) : a.Tk;
     const int j_begin = sp * a.split, j_end = min(len, j_begin + a.split);
 
-    int row[QB];
     i32x4 qf[QB][KS];
     f32x16 acc[QB][DB];
     float m[QB], l[QB];
-    const uint8_t* qbase = a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h;
+    const int row0 = (rt * NW + wave) * (32 * QB), t0 = div_g(a, row0);
+    const __amdgpu_buffer_rsrc_t qrs = attn_rsrc(
+        a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h + (int64_t)t0 * a.q_t);
 #pragma unroll
     for (int r = 0; r < QB; ++r) {
-        row[r] = (rt * NW + wave) * (32 * QB) + 32 * r + (lane & 31);
-        load_rows<DP>(a, qbase, a.q_t, a.q_h, row[r], half, qf[r]);
+        load_rows<DP>(qrs, packed_off(a, row0 + 32 * r + (lane & 31), t0, a.q_t, a.q_h), a.D, half,
+                      qf[r]);
         m[r] = -__builtin_inff();
         l[r] = 0.0f;
 #pragma unroll
@@ -246,7 +215,7 @@ __global__ __launch_bounds__(NW * 64, QB == 1 ? 2 : 1) void attn_fwd_kernel(Attn
     }
 #pragma unroll
     for (int r = 0; r < QB; ++r)
-        fwd_finish<DT, DB>(a, b, hk, sp, row[r], acc[r], m[r], l[r], half);
+        fwd_finish<DT, DB>(a, b, hk, sp, row0 + 32 * r, lane, acc[r], m[r], l[r]);
 }
 
 // ---------------------------------------------------------------------------
@@ -276,8 +245,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
 
     const int row = lane & 31;
     i32x4 qf[KS];
-    load_rows<DP>(a, a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h, a.q_t, a.q_h, row, half,
-                  qf);
+    load_rows<DP>(attn_rsrc(a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h),
+                  packed_off(a, row, 0, a.q_t, a.q_h), a.D, half, qf);
     f32x16 acc[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -393,11 +362,11 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
             continue;
         }
         const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
-        const int tok = div_g(a, r);
         uint8_t* dst = a.out + (int64_t)b * a.o_b + (int64_t)hk * a.G * a.o_h +
-                       packed_off(a, r, a.o_t, a.o_h) + d * 2;
+                       packed_off(a, r, 0, a.o_t, a.o_h) + d * 2;
         *reinterpret_cast<u32x2*>(dst) =
             u32x2{pack_out2(o[0] * inv, o[1] * inv, DT), pack_out2(o[2] * inv, o[3] * inv, DT)};
+        const int tok = div_g(a, r);
         if (a.lse && d == 0)
             a.lse[((int64_t)b * a.Hq + hk * a.G + (r - tok * a.G)) * a.Tq + tok] =
                 ll == 0.0f ? -__builtin_inff()
@@ -450,7 +419,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     const int b = (int)(bh / a.Hk), hk = (int)(bh - (int64_t)b * a.Hk);
     const int tok = div_g(a, r);
     uint8_t* dst = a.out + (int64_t)b * a.o_b + (int64_t)hk * a.G * a.o_h +
-                   packed_off(a, r, a.o_t, a.o_h) + d * 2;
+                   (int64_t)tok * a.o_t + packed_off(a, r, tok, a.o_t, a.o_h) + d * 2;
     *reinterpret_cast<u32x2*>(dst) =
         u32x2{pack_out2(o[0] * inv, o[1] * inv, DT), pack_out2(o[2] * inv, o[3] * inv, DT)};
     if (a.lse && d == 0)

@@ -11,6 +11,7 @@ namespace igc {
 // Plan of one forward launch (fwd_plan in igemm_attn.hip).
 struct AttnPlan {
     bool token;       // at most 32 rows a key head: attn_token_kernel
+    bool few_keys;    // at most kShortKeys keys: attn_short_fwd_kernel
     int qb;           // 32-row blocks a wave
     int row_tiles, nsplit, split;
     int64_t part_floats, stat_floats;   // workspace of split launches
@@ -18,13 +19,17 @@ struct AttnPlan {
 
 // Plan of a backward pass (bwd_plan in igemm_attn.hip).
 struct AttnGradPlan {
+    bool few_keys;        // at most kShortKeys keys: attn_short_rows_kernel instead of
+                          // the row pass and the dq kernel
     int rows_pad, bound_n;
+    int kv_waves;         // dk dv: waves a workgroup, 32 keys each
     int key_tiles, kv_nsplit, kv_split;   // dk dv: key tiles, splits of the rows
     int row_tiles, q_nsplit, q_split;     // dq: row tiles, splits of the keys
     int64_t stat_floats, bound_words, part_floats;   // workspace
 };
 
 constexpr int kAttnWaves = 4;     // waves a workgroup
+constexpr int kShortKeys = 128;   // keys that the few-keys kernels hold in LDS
 constexpr int kRowTile = 64;      // rows a tile of the dk dv kernel; padding of row statistics
 constexpr int kKeyTile = 64;      // keys a tile of the forward kernel
 constexpr int kTokenStep = 128;   // keys a round of the single-token kernel's waves

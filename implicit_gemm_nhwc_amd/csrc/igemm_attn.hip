@@ -1,7 +1,8 @@
 // C-ABI entry points of the attention operators (declarations and contracts
 // in include/igemm_attn.h): the host gates, the launch plans and the
 // workspaces.  Every step of the computation runs in the kernels of
-// attn_fwd.hpp, attn_bwd.hpp and qk_norm.hpp.
+// attn_fwd.hpp, attn_short.hpp, attn_bwd.hpp and
+// qk_norm.hpp.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -91,13 +92,21 @@ int32_t check_attn_shape(const igc_cross_attn* p) {
         p->kv_heads >= kLim31)
         return IGC_DECLINE_SIZE_LIMIT;
     const int64_t g = p->kv_heads ? p->q_heads / p->kv_heads : 1;
-    if (g * p->q_len >= kLim31 - 4096 || p->kv_len >= kLim31 - 4096 ||
+    if (g * p->q_len >= kLim31 / 4 || p->kv_len >= kLim31 - 4096 ||
         p->batch * p->q_heads >= kLim31)
         return IGC_DECLINE_SIZE_LIMIT;
     return IGC_OK;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Workgroups a key head of the few-keys kernels.
+int64_t short_tiles(int64_t bh, int64_t rows) {
+    const int64_t most = ceil_div(rows, 32 * kAttnWaves);
+    const int64_t want = bh > 0 ? ceil_div(4 * kNumCUs, bh) : 1;
+    const int64_t n = want < most ? want : most;
+    return n < 1 ? 1 : n;
+}
 
 // Plan of a forward launch from the shapes alone (checked before).
 AttnPlan fwd_plan(const igc_cross_attn* p) {
@@ -106,6 +115,15 @@ AttnPlan fwd_plan(const igc_cross_attn* p) {
     const int64_t rows = p->kv_heads ? p->q_len * (p->q_heads / p->kv_heads) : 0;
     x.token = rows <= 32;
     x.qb = 1;
+    x.nsplit = 1;
+    x.split = kLim31 - 1;
+    x.few_keys = !x.token && p->kv_len <= kShortKeys;
+    if (x.few_keys) {
+        // the waves walk the rows: workgroups for four a CU, each wave one
+        // block of 32 rows at least
+        x.row_tiles = (int)short_tiles(bh, rows);
+        return x;
+    }
     int64_t groups, step;
     if (x.token) {
         x.row_tiles = 1;
@@ -117,10 +135,13 @@ AttnPlan fwd_plan(const igc_cross_attn* p) {
         step = kKeyTile;
     }
     const int64_t steps = ceil_div(p->kv_len, step);
-    // workgroups for two a CU; a split has one round of the token kernel or
-    // four tiles of the other at least, below which its join costs more
+    // Workgroups for two a CU.  A round of the token kernel is one memory
+    // latency (about 1.5 us) and the join of split keys another launch: at 7
+    // rounds both ways take 11.4 us (32 key heads, 784 keys of 128), below
+    // the split loses, above every round given to another workgroup gains.
+    // The tile kernel keeps four tiles a split.
     const int64_t want = groups > 0 ? 2 * kNumCUs / groups : 1;
-    const int64_t most = x.token ? steps : steps / 4;
+    const int64_t most = !x.token ? steps / 4 : steps > 7 ? steps : 1;
     int64_t n = want < most ? want : most;
     if (n < 1) n = 1;
     const int64_t per = ceil_div(steps > 0 ? steps : 1, n);
@@ -141,6 +162,13 @@ struct AttnTensors {
     Tensor q, k, v, o;
 };
 
+// The kernels address a tile of packed rows (at most 65 tokens, all heads of
+// a group) in 32 bits.
+bool packed_fits(const igc_cross_attn* p, const Tensor& x) {
+    const int64_t g = p->kv_heads ? p->q_heads / p->kv_heads : 1;
+    return (kRowTile + 1) * x.t + g * x.h < kLim31;
+}
+
 int32_t check_attn_views(const igc_cross_attn* p, AttnTensors* t, bool write_out) {
     int32_t r;
     const int64_t d = p->head_dim;
@@ -151,6 +179,7 @@ int32_t check_attn_views(const igc_cross_attn* p, AttnTensors* t, bool write_out
     if ((r = check_view(p->v, any ? p->batch : 0, p->kv_len, p->kv_heads, d, false, &t->v)))
         return r;
     if ((r = check_view(p->out, p->batch, p->q_len, p->q_heads, d, write_out, &t->o))) return r;
+    if (!packed_fits(p, t->q) || !packed_fits(p, t->o)) return IGC_DECLINE_SIZE_LIMIT;
     if (p->kv_lens && !aligned(p->kv_lens, 4)) return IGC_DECLINE_ALIGNMENT;
     if (p->lse && !aligned(p->lse, 4)) return IGC_DECLINE_ALIGNMENT;
     if (p->key_mask && (p->key_mask_stride < 0 || p->key_mask_stride >= kBatchStrideLim))
@@ -248,10 +277,18 @@ AttnGradPlan bwd_plan(const igc_cross_attn* p) {
         *nsplit = (int)ceil_div(tiles > 0 ? tiles : 1, per);
         *len = (int)(per * unit < kLim31 ? per * unit : kLim31 - 1);
     };
-    x.key_tiles = (int)ceil_div(p->kv_len, kAttnWaves * 32);
+    const int64_t key32 = ceil_div(p->kv_len, 32);
+    x.kv_waves = (int)(key32 < 1 ? 1 : key32 < kAttnWaves ? key32 : kAttnWaves);
+    x.key_tiles = (int)ceil_div(key32, x.kv_waves);
     split(bh * x.key_tiles, row64, kRowTile, &x.kv_nsplit, &x.kv_split);
     x.row_tiles = (int)ceil_div(rows, kAttnWaves * 32);
     split(bh * x.row_tiles, key64, kKeyTile, &x.q_nsplit, &x.q_split);
+    x.few_keys = p->kv_len <= kShortKeys;
+    if (x.few_keys) {
+        x.row_tiles = (int)short_tiles(bh, x.rows_pad);
+        x.q_nsplit = 1;
+        x.bound_n = x.row_tiles * kAttnWaves;   // one a wave
+    }
     x.stat_floats = 2 * bh * x.rows_pad;
     x.bound_words = p->dtype == IGC_DTYPE_FP16 ? 2 * bh * x.bound_n : 0;
     int64_t f = x.kv_nsplit > 1 ? 2 * x.kv_nsplit * bh * p->kv_len * p->head_dim : 0;
@@ -289,9 +326,8 @@ int32_t check_bwd(const igc_cross_attn_grad* p, GradTensors* t, AttnGradPlan* pl
         if ((r = check_view(p->dk, f->batch, f->kv_len, f->kv_heads, d, true, &t->dk))) return r;
         if ((r = check_view(p->dv, f->batch, f->kv_len, f->kv_heads, d, true, &t->dv))) return r;
     }
-    const int64_t g = f->kv_heads ? f->q_heads / f->kv_heads : 1;
-    for (const Tensor* x : {&t->f.q, &t->g})
-        if (kRowTile * x->t + g * x->h >= kLim31) return IGC_DECLINE_SIZE_LIMIT;
+    for (const Tensor* x : {&t->g, &t->dq})
+        if (!packed_fits(f, *x)) return IGC_DECLINE_SIZE_LIMIT;
     *plan = bwd_plan(f);
     const int64_t bh = f->batch * f->kv_heads;
     if (bh * plan->key_tiles > kMaxGrid / (plan->kv_nsplit > 0 ? plan->kv_nsplit : 1) ||

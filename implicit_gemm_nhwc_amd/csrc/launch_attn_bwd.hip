@@ -1,7 +1,7 @@
 // Launchers of the cross-attention backward kernels, one element type per
 // translation unit (IGC_DT).
-#include "attn_bwd.hpp"
 #include "attn_host.hpp"
+#include "attn_short.hpp"
 
 #ifndef IGC_DT
 #error "IGC_DT must name the element type of this translation unit"
@@ -10,9 +10,9 @@
 namespace igc {
 namespace {
 
-template <int DT, int DP>
+template <int DT, int DP, int NW>
 hipError_t launch_kv(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
-    auto kern = attn_bwd_kv_kernel<DT, DP, kAttnWaves>;
+    auto kern = attn_bwd_kv_kernel<DT, DP, NW>;
     constexpr size_t lds = 2 * (2 * (size_t)kRowTile * DP * 2 + 2 * kRowTile * 4);
     static LdsAttr attr;
     hipError_t e = ensure_lds(attr, (const void*)kern, lds);
@@ -21,8 +21,8 @@ hipError_t launch_kv(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
     a.nsplit = p.kv_nsplit;
     a.split = p.kv_split;
     const int64_t bh = (int64_t)a.B * a.Hk;
-    hipLaunchKernelGGL(kern, dim3((unsigned)(bh * a.nsplit * a.key_tiles)), dim3(kAttnWaves * 64),
-                       lds, stream, a);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(bh * a.nsplit * a.key_tiles)), dim3(NW * 64), lds,
+                       stream, a);
     e = hipGetLastError();
     if (e != hipSuccess || a.nsplit <= 1) return e;
     hipLaunchKernelGGL(attn_bwd_join_kernel<DT>,
@@ -53,16 +53,40 @@ hipError_t launch_q(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
 }
 
 template <int DT, int DP>
+hipError_t launch_short(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
+    auto kern = attn_short_rows_kernel<DT, DP, kAttnWaves>;
+    constexpr size_t lds = 2 * (size_t)kShortKeys * DP * 2;
+    static LdsAttr attr;
+    const hipError_t e = ensure_lds(attr, (const void*)kern, lds);
+    if (e != hipSuccess) return e;
+    a.row_tiles = p.row_tiles;
+    hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)a.B * a.Hk * a.row_tiles)),
+                       dim3(kAttnWaves * 64), lds, stream, a);
+    return hipGetLastError();
+}
+
+template <int DT, int DP>
 hipError_t launch_dp(const AttnArgs& a, const AttnGradPlan& p, hipStream_t stream) {
     hipError_t e = hipSuccess;
     if (a.rows > 0) {
-        hipLaunchKernelGGL(attn_bwd_rows_kernel<DT>,
-                           dim3((unsigned)((int64_t)a.B * a.Hk * a.bound_n)), dim3(256), 0, stream,
-                           a);
-        e = hipGetLastError();
+        if (p.few_keys) {
+            e = launch_short<DT, DP>(a, p, stream);
+        } else {
+            hipLaunchKernelGGL(attn_bwd_rows_kernel<DT>,
+                               dim3((unsigned)((int64_t)a.B * a.Hk * a.bound_n)), dim3(256), 0,
+                               stream, a);
+            e = hipGetLastError();
+        }
     }
-    if (e == hipSuccess && a.Tk > 0 && a.dk) e = launch_kv<DT, DP>(a, p, stream);
-    if (e == hipSuccess && a.rows > 0 && a.dq) e = launch_q<DT, DP>(a, p, stream);
+    if (e == hipSuccess && a.Tk > 0 && a.dk) {
+        switch (p.kv_waves) {
+            case 1: e = launch_kv<DT, DP, 1>(a, p, stream); break;
+            case 2: e = launch_kv<DT, DP, 2>(a, p, stream); break;
+            case 3: e = launch_kv<DT, DP, 3>(a, p, stream); break;
+            default: e = launch_kv<DT, DP, 4>(a, p, stream); break;
+        }
+    }
+    if (e == hipSuccess && a.rows > 0 && a.dq && !p.few_keys) e = launch_q<DT, DP>(a, p, stream);
     return e;
 }
 

@@ -1,7 +1,7 @@
 // Launchers of the cross-attention forward kernels, one element type per
 // translation unit (IGC_DT).
-#include "attn_fwd.hpp"
 #include "attn_host.hpp"
+#include "attn_short.hpp"
 
 #ifndef IGC_DT
 #error "IGC_DT must name the element type of this translation unit"
@@ -23,6 +23,18 @@ hipError_t launch_rows(const AttnArgs& a, hipStream_t stream) {
 }
 
 template <int DT, int DP>
+hipError_t launch_short(const AttnArgs& a, hipStream_t stream) {
+    auto kern = attn_short_fwd_kernel<DT, DP, kAttnWaves>;
+    constexpr size_t lds = 2 * (size_t)kShortKeys * DP * 2;
+    static LdsAttr attr;
+    const hipError_t e = ensure_lds(attr, (const void*)kern, lds);
+    if (e != hipSuccess) return e;
+    const unsigned grid = (unsigned)((int64_t)a.B * a.Hk * a.row_tiles);
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(kAttnWaves * 64), lds, stream, a);
+    return hipGetLastError();
+}
+
+template <int DT, int DP>
 hipError_t launch_token(const AttnArgs& a, hipStream_t stream) {
     auto kern = attn_token_kernel<DT, DP, kAttnWaves>;
     constexpr size_t lds = (size_t)kAttnWaves * 2 * 2 * 32 * DP * 2 + kAttnWaves * 64 * 4;
@@ -38,6 +50,7 @@ template <int DT, int DP>
 hipError_t launch_dp(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
     hipError_t e;
     if (p.token) e = launch_token<DT, DP>(a, stream);
+    else if (p.few_keys) e = launch_short<DT, DP>(a, stream);
     else if (p.qb == 2) e = launch_rows<DT, DP, 2>(a, stream);
     else e = launch_rows<DT, DP, 1>(a, stream);
     if (e != hipSuccess || a.nsplit <= 1) return e;

@@ -70,9 +70,10 @@ typedef struct igc_attn_view {
  * Few rows over many keys run as several workgroups per row block whose
  * partial results (fp32, in the workspace) a second launch joins in a fixed
  * order: results do not change from run to run.
- * Limits: kv_len, q_len * q_heads / kv_heads and batch * heads below 2^31,
- * token and head strides of q, k, v, out (and of the gradients) below 2^23
- * elements.
+ * Limits: kv_len and batch * heads below 2^31, q_len * q_heads / kv_heads
+ * below 2^29; token and head strides of q, k, v, out (and of the gradients)
+ * below 2^23 elements; of q and out (dout, dq) 65 token strides and the
+ * strides over the heads of a group together below 2^31 bytes.
  */
 typedef struct igc_cross_attn {
     int64_t batch, q_len, kv_len, q_heads, kv_heads, head_dim;
@@ -109,10 +110,9 @@ size_t cross_attn_fwd_workspace_bytes(const igc_cross_attn* args);
  *          workspace of this call
  * ds and p are rounded to the element type before their products, which
  * accumulate in fp32 (for fp16 scaled by powers of two that keep them in
- * range).  Sums are taken in a fixed order.  Limits as the forward; besides,
- * 64 token strides and one stride over a group's heads, of q and of dout,
- * together below 2^31 bytes.  dq, dk and dv may interleave in one buffer,
- * provided no element belongs to two of them.
+ * range).  Sums are taken in a fixed order.  Limits as the forward.  dq, dk
+ * and dv may interleave in one buffer, provided no element belongs to two of
+ * them.
  */
 typedef struct igc_cross_attn_grad {
     igc_cross_attn fwd;
