@@ -149,20 +149,35 @@ __device__ __forceinline__ void issue_packed(const TileStage<DP, ROWS, NW>& st, 
 }
 
 // ---------------------------------------------------------------------------
-// dk and dv: each wave owns 32 keys (k and v as B operands in registers) and
-// walks the rows in tiles of 64 (q and do in LDS).  S = Q K^T has rows down
-// the registers and a key a lane, so p and ds go into dv^T += do^T p and
-// dk^T += q^T ds as B operands without leaving their lane; do^T and q^T come
-// by transposing reads of the same tiles.
-template <int DT, int DP, int NW>
-__global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_bwd_kv_kernel(AttnArgs a) {
-    constexpr int DB = DP / 32, KS = DP / 16, QT = kRowTile;
-    constexpr int TILE = QT * DP * 2;
-    constexpr int STAGE = 2 * TILE + 2 * QT * 4;   // q, do, lse, Delta
-    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-    lds_poison<NW * 64>(lds, 2 * STAGE);
+// dk and dv: each wave owns 32 keys and walks the rows in tiles of QT (q and
+// do in LDS).  S = Q K^T has rows down the registers and a key a lane, so p
+// and ds go into dv^T += do^T p and dk^T += q^T ds as B operands without
+// leaving their lane; do^T and q^T come by transposing reads of the same
+// tiles.  The keys' own operands (k and v) stay in registers, or in LDS
+// (KV_LDS) where the registers of two waves a SIMD do not hold them.  RG = 2:
+// two waves a key block take alternate blocks of 32 rows, and their sums are
+// added through LDS at the end.
+template <int DP, int NWK, int RG, int QT, bool KV_LDS>
+struct KvShape {
+    static constexpr int NW = NWK * RG;
+    static constexpr int TILE = QT * DP * 2;
+    static constexpr int STAGE = (2 * TILE + 2 * QT * 4 + 1023) / 1024 * 1024;  // q, do, lse, Delta
+    static constexpr int KEYS = KV_LDS ? 2 * NWK * 32 * DP * 2 : 0;             // k, v
+    static constexpr int SUM = RG > 1 ? NWK * 64 * DP * 2 : 0;                  // over all of it
+    static constexpr int LDS = KEYS + 2 * STAGE > SUM ? KEYS + 2 * STAGE : SUM;
+};
+
+template <int DT, int DP, int NWK, int RG, int QT, bool KV_LDS, int OCC>
+__global__ __launch_bounds__(NWK * RG * 64, OCC) void attn_bwd_kv_kernel(AttnArgs a) {
+    typedef KvShape<DP, NWK, RG, QT, KV_LDS> Sh;
+    constexpr int NW = Sh::NW, TILE = Sh::TILE, STAGE = Sh::STAGE;
+    constexpr int DB = DP / 32, KS = DP / 16;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds_all[];
+    lds_poison<NW * 64>(lds_all, Sh::LDS);
+    uint8_t* lds = lds_all + Sh::KEYS;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int half = lane >> 5;
+    const int wk = RG > 1 ? wave % NWK : wave, rg = RG > 1 ? wave / NWK : 0;
 
     int idx = xcd_remap(blockIdx.x, gridDim.x);
     const int kt = idx % a.key_tiles;
@@ -171,26 +186,39 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_bwd_kv_kernel(A
     const int bh = idx / a.nsplit;
     const int hk = bh % a.Hk, b = bh / a.Hk;
     const int len = a.lens ? max(0, min(a.lens[b], a.Tk)) : a.Tk;
-    const int key0 = (kt * NW + wave) * 32, kr = lane & 31;
+    const int key0 = (kt * NWK + wk) * 32, kr = lane & 31;
     const uint8_t* mrow = a.mask ? a.mask + (int64_t)b * a.mask_b : nullptr;
     const bool valid = mask_byte(mrow, key0, len, kr) != 0 && key0 + kr < len;
     // the whole workgroup's keys may be out of range: nothing to sum then
     const int r_begin = sp * a.split;
-    const int r_end = kt * NW * 32 < len ? min(a.rows, r_begin + a.split) : r_begin;
+    const int r_end = kt * NWK * 32 < len ? min(a.rows, r_begin + a.split) : r_begin;
     const bool idle = !__any(valid);   // this wave then only stages
 
     i32x4 kf[KS], vf[KS];
     f32x16 dk[DB], dv[DB];
-    {
-        const uint8_t* kp = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h + (int64_t)key0 * a.k_t;
-        const uint8_t* vp = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h + (int64_t)key0 * a.v_t;
-        load_rows<DP>(attn_rsrc(kp), valid ? (unsigned)kr * (unsigned)a.k_t : kOut, a.D, half, kf);
-        load_rows<DP>(attn_rsrc(vp), valid ? (unsigned)kr * (unsigned)a.v_t : kOut, a.D, half, vf);
+    const uint8_t* kp = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h;
+    const uint8_t* vp = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h;
+    if constexpr (KV_LDS) {
+        TileStage<DP, 32, NW> ks;
+        ks.init(wave, lane, a.D);
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.0f;
+        for (int w = 0; w < NWK; ++w) {
+            const int k0 = (kt * NWK + w) * 32;
+            const uint64_t word = mask_word(mask_byte(mrow, k0, len, lane), len - k0);
+            ks.issue(kp + (int64_t)k0 * a.k_t, (unsigned)a.k_t, word, lds_all + w * 64 * DP, wave);
+            ks.issue(vp + (int64_t)k0 * a.v_t, (unsigned)a.v_t, word,
+                     lds_all + (NWK + w) * 64 * DP, wave);
+        }
+    } else {
+        load_rows<DP>(attn_rsrc(kp + (int64_t)key0 * a.k_t),
+                      valid ? (unsigned)kr * (unsigned)a.k_t : kOut, a.D, half, kf);
+        load_rows<DP>(attn_rsrc(vp + (int64_t)key0 * a.v_t),
+                      valid ? (unsigned)kr * (unsigned)a.v_t : kOut, a.D, half, vf);
     }
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.0f;
     const float f = ds_scale<DT>(a, bh, lane);
     constexpr float PS = DT == DT_FP16 ? 14.0f : 0.0f;   // p carries 2^PS
     const float fp = DT == DT_FP16 ? f * 0.00006103515625f : f;
@@ -205,14 +233,16 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_bwd_kv_kernel(A
     auto issue = [&](int r0, uint8_t* to) {
         issue_packed(st, a, qbase, a.q_t, a.q_h, r0, to, wave);
         issue_packed(st, a, gbase, a.do_t, a.do_h, r0, to + TILE, wave);
-        for (int x = wave; x < 2; x += NW) {   // 64 floats each: lse, Delta
-            const float* src = (x ? delta : lse2) + r0;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                attn_rsrc(src),
-                (__attribute__((address_space(3))) void*)(to + 2 * TILE + x * QT * 4), 4,
-                lane * 4, 0, 0, 0);
-        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)   // QT floats each: lse, Delta
+            if (wave == x % NW)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    attn_rsrc((x ? delta : lse2) + r0),
+                    (__attribute__((address_space(3))) void*)(to + 2 * TILE + x * QT * 4), 4,
+                    lane < QT ? (unsigned)lane * 4 : kOut, 0, 0, 0);
     };
+    const uint8_t* kl = lds_all + wk * 64 * DP;
+    const uint8_t* vl = kl + NWK * 64 * DP;
     if (r_begin < r_end) {
         issue(r_begin, lds);
         int buf = 0;
@@ -225,7 +255,8 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_bwd_kv_kernel(A
             if (r0 + QT < r_end) issue(r0 + QT, lds + (buf ^ 1) * STAGE);
             if (!idle)
 #pragma unroll
-            for (int rb = 0; rb < QT / 32; ++rb) {
+            for (int rx = 0; rx < QT / 32 / RG; ++rx) {
+                const int rb = rx * RG + rg;
                 f32x16 s, dp;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -235,12 +266,14 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_bwd_kv_kernel(A
 #pragma unroll
                 for (int x = 0; x < KS; ++x) {
                     const i32x4 qf = frag_row<DP>(ql, 32 * rb + (lane & 31), 2 * x + half);
-                    s = mfma32<DT>(&qf, &kf[x], s);
+                    const i32x4 kx = KV_LDS ? frag_row<DP>(kl, lane & 31, 2 * x + half) : kf[x];
+                    s = mfma32<DT>(&qf, &kx, s);
                 }
 #pragma unroll
                 for (int x = 0; x < KS; ++x) {
                     const i32x4 gf = frag_row<DP>(gl, 32 * rb + (lane & 31), 2 * x + half);
-                    dp = mfma32<DT>(&gf, &vf[x], dp);
+                    const i32x4 vx = KV_LDS ? frag_row<DP>(vl, lane & 31, 2 * x + half) : vf[x];
+                    dp = mfma32<DT>(&gf, &vx, dp);
                 }
                 float p[16], ds[16];
 #pragma unroll
@@ -253,7 +286,8 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_bwd_kv_kernel(A
                     for (int i = 0; i < 4; ++i) {
                         const int e = 4 * g + i;
                         p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], a.c, PS - L[i]));
-                        ds[e] = p[e] * (dp[e] - De[i]) * fp;
+                        ds[e] = p[e] * (dp[e] - De[i]);
+                        if constexpr (DT == DT_FP16) ds[e] *= fp;
                     }
                 }
                 i32x4 pf[2], df[2];
@@ -276,6 +310,36 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_bwd_kv_kernel(A
             }
             buf ^= 1;
         }
+    }
+    if constexpr (RG > 1) {
+        // the second row group's sums through LDS, dk then dv, lane by lane
+        f32x4* x = reinterpret_cast<f32x4*>(lds_all) + (wk * 64 + lane);
+        constexpr int N = NWK * 64;   // f32x4 between a lane's
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            f32x16(&acc)[DB] = t ? dv : dk;
+            __syncthreads();
+            if (rg == 1) {
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        x[(4 * d + g) * N] = f32x4{acc[d][4 * g], acc[d][4 * g + 1],
+                                                   acc[d][4 * g + 2], acc[d][4 * g + 3]};
+            }
+            __syncthreads();
+            if (rg == 0) {
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const f32x4 y = x[(4 * d + g) * N];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[d][4 * g + i] += y[i];
+                    }
+            }
+        }
+        if (rg == 1) return;
     }
     const float fk = a.scale / f, fv = DT == DT_FP16 ? 0.00006103515625f : 1.0f;
 #pragma unroll

@@ -100,11 +100,14 @@ int32_t check_attn_shape(const igc_cross_attn* p) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Workgroups a key head of the few-keys kernels.
-int64_t short_tiles(int64_t bh, int64_t rows) {
-    const int64_t most = ceil_div(rows, 32 * kAttnWaves);
-    const int64_t want = bh > 0 ? ceil_div(4 * kNumCUs, bh) : 1;
-    const int64_t n = want < most ? want : most;
+// Workgroups a key head of the few-keys kernels, whose waves walk blocks of 32
+// rows: as many rounds as the card's `slots` workgroups need, spread evenly.
+int64_t short_tiles(int64_t bh, int64_t rows, int64_t slots) {
+    const int64_t blocks = ceil_div(rows, 32);
+    int64_t per = bh > 0 ? slots / bh : 1;   // workgroups a head that run at once
+    if (per < 1) per = 1;
+    const int64_t rounds = ceil_div(blocks, per * kAttnWaves);
+    const int64_t n = ceil_div(blocks, (rounds > 0 ? rounds : 1) * kAttnWaves);
     return n < 1 ? 1 : n;
 }
 
@@ -119,9 +122,7 @@ AttnPlan fwd_plan(const igc_cross_attn* p) {
     x.split = kLim31 - 1;
     x.few_keys = !x.token && p->kv_len <= kShortKeys;
     if (x.few_keys) {
-        // the waves walk the rows: workgroups for four a CU, each wave one
-        // block of 32 rows at least
-        x.row_tiles = (int)short_tiles(bh, rows);
+        x.row_tiles = (int)short_tiles(bh, rows, (p->head_dim <= 64 ? 3 : 2) * kNumCUs);
         return x;
     }
     int64_t groups, step;
@@ -268,9 +269,11 @@ AttnGradPlan bwd_plan(const igc_cross_attn* p) {
     if (n > x.rows_pad / 16) n = x.rows_pad / 16;
     if (n > 256) n = 256;
     x.bound_n = (int)(n < 1 ? 1 : n);
-    // both passes: two workgroups a CU, splits of four tiles at least
-    auto split = [](int64_t groups, int64_t tiles, int64_t unit, int* nsplit, int* len) {
-        int64_t n = groups > 0 ? 2 * kNumCUs / groups : 1;
+    // splits for one workgroup a CU (dk dv: eight waves) or two (dq: four),
+    // of four tiles at least
+    auto split = [](int64_t want, int64_t groups, int64_t tiles, int64_t unit, int* nsplit,
+                    int* len) {
+        int64_t n = groups > 0 ? want / groups : 1;
         if (n > tiles / 4) n = tiles / 4;
         if (n < 1) n = 1;
         const int64_t per = ceil_div(tiles > 0 ? tiles : 1, n);
@@ -280,12 +283,12 @@ AttnGradPlan bwd_plan(const igc_cross_attn* p) {
     const int64_t key32 = ceil_div(p->kv_len, 32);
     x.kv_waves = (int)(key32 < 1 ? 1 : key32 < kAttnWaves ? key32 : kAttnWaves);
     x.key_tiles = (int)ceil_div(key32, x.kv_waves);
-    split(bh * x.key_tiles, row64, kRowTile, &x.kv_nsplit, &x.kv_split);
+    split(kNumCUs, bh * x.key_tiles, row64, kRowTile, &x.kv_nsplit, &x.kv_split);
     x.row_tiles = (int)ceil_div(rows, kAttnWaves * 32);
-    split(bh * x.row_tiles, key64, kKeyTile, &x.q_nsplit, &x.q_split);
+    split(2 * kNumCUs, bh * x.row_tiles, key64, kKeyTile, &x.q_nsplit, &x.q_split);
     x.few_keys = p->kv_len <= kShortKeys;
     if (x.few_keys) {
-        x.row_tiles = (int)short_tiles(bh, x.rows_pad);
+        x.row_tiles = (int)short_tiles(bh, x.rows_pad, (p->head_dim <= 64 ? 2 : 1) * kNumCUs);
         x.q_nsplit = 1;
         x.bound_n = x.row_tiles * kAttnWaves;   // one a wave
     }

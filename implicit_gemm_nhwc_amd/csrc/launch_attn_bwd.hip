@@ -10,10 +10,11 @@
 namespace igc {
 namespace {
 
-template <int DT, int DP, int NW>
+template <int DT, int DP, int NWK, int RG, int QT, bool KV_LDS, int OCC>
 hipError_t launch_kv(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
-    auto kern = attn_bwd_kv_kernel<DT, DP, NW>;
-    constexpr size_t lds = 2 * (2 * (size_t)kRowTile * DP * 2 + 2 * kRowTile * 4);
+    auto kern = attn_bwd_kv_kernel<DT, DP, NWK, RG, QT, KV_LDS, OCC>;
+    constexpr size_t lds = KvShape<DP, NWK, RG, QT, KV_LDS>::LDS;
+    constexpr int NW = NWK * RG;
     static LdsAttr attr;
     hipError_t e = ensure_lds(attr, (const void*)kern, lds);
     if (e != hipSuccess) return e;
@@ -29,6 +30,16 @@ hipError_t launch_kv(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
                        dim3((unsigned)((bh * a.Tk * (a.D / 4) + 255) / 256), 2), dim3(256), 0,
                        stream, a, 1);
     return hipGetLastError();
+}
+
+// Two row groups a workgroup and two waves a SIMD.  Up to 64 values a head
+// the keys' operands stay in registers (32 x 77 keys of 64, 784 rows: 21.7 us,
+// from LDS 24.2); wider heads do not fit two waves that way and read them
+// from LDS (2 x 2048 keys of 128, 8192 rows: 282 us; in registers with one
+// wave a SIMD 375, spilling 467).
+template <int DT, int DP, int NWK>
+hipError_t launch_kv_dp(const AttnArgs& a, const AttnGradPlan& p, hipStream_t stream) {
+    return launch_kv<DT, DP, NWK, 2, kRowTile, (DP > 64), 2>(a, p, stream);
 }
 
 template <int DT, int DP>
@@ -80,10 +91,10 @@ hipError_t launch_dp(const AttnArgs& a, const AttnGradPlan& p, hipStream_t strea
     }
     if (e == hipSuccess && a.Tk > 0 && a.dk) {
         switch (p.kv_waves) {
-            case 1: e = launch_kv<DT, DP, 1>(a, p, stream); break;
-            case 2: e = launch_kv<DT, DP, 2>(a, p, stream); break;
-            case 3: e = launch_kv<DT, DP, 3>(a, p, stream); break;
-            default: e = launch_kv<DT, DP, 4>(a, p, stream); break;
+            case 1: e = launch_kv_dp<DT, DP, 1>(a, p, stream); break;
+            case 2: e = launch_kv_dp<DT, DP, 2>(a, p, stream); break;
+            case 3: e = launch_kv_dp<DT, DP, 3>(a, p, stream); break;
+            default: e = launch_kv_dp<DT, DP, 4>(a, p, stream); break;
         }
     }
     if (e == hipSuccess && a.rows > 0 && a.dq && !p.few_keys) e = launch_q<DT, DP>(a, p, stream);
