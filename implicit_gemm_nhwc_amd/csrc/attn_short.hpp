@@ -13,8 +13,13 @@
 
 namespace igc {
 
-// Keys and values of one head in LDS (two tiles of 64 each), and the words
-// of valid keys of the four blocks of 32.
+// LDS: two tiles of 64 keys, two of values, and for each key 0 or, where it
+// is not valid, -inf, with which the score products start.
+template <int DP>
+constexpr int short_lds() { return 2 * kShortKeys * DP * 2 + kShortKeys * 4; }
+
+// Keys and values of one head in LDS, and the words of valid keys of the four
+// blocks of 32.
 template <int DP, int NW>
 __device__ __forceinline__ void stage_short(const AttnArgs& a, int b, int hk, int wave, int lane,
                                             uint8_t* lds, uint32_t (&word)[4]) {
@@ -35,17 +40,23 @@ __device__ __forceinline__ void stage_short(const AttnArgs& a, int b, int hk, in
         st.issue(vbase + (int64_t)(64 * t) * a.v_t, (unsigned)a.v_t, w, lds + (2 + t) * TILE,
                  wave);
     }
+    if (wave == 0) {
+        float* bias = reinterpret_cast<float*>(lds + 4 * TILE);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t w = lane < 32 ? word[2 * t] : word[2 * t + 1];
+            bias[64 * t + lane] = (w >> (lane & 31)) & 1 ? 0.0f : -__builtin_inff();
+        }
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
 }
 
-// Products of the 32 keys of block kb in a staged tile with 32 rows.
+// Products of the 32 keys of block kb in a staged tile with 32 rows, added to
+// s.
 template <int DT, int DP>
 __device__ __forceinline__ f32x16 short_scores(const uint8_t* tile, int kb, int lane,
-                                               const i32x4 (&f)[DP / 16]) {
-    f32x16 s;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+                                               const i32x4 (&f)[DP / 16], f32x16 s) {
 #pragma unroll
     for (int x = 0; x < DP / 16; ++x) {
         const i32x4 kf =
@@ -55,11 +66,25 @@ __device__ __forceinline__ f32x16 short_scores(const uint8_t* tile, int kb, int 
     return s;
 }
 
+// -inf for the block's keys that are not valid, 0 for the others, in result
+// order.
+__device__ __forceinline__ f32x16 short_bias(const uint8_t* bias, int kb, int half) {
+    f32x16 s;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const f32x4 x =
+            *reinterpret_cast<const f32x4*>(bias + (32 * kb + 8 * g + 4 * half) * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[4 * g + i] = x[i];
+    }
+    return s;
+}
+
 template <int DT, int DP, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void attn_short_fwd_kernel(AttnArgs a) {
     constexpr int DB = DP / 32, KS = DP / 16, TILE = 64 * DP * 2;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-    lds_poison<NW * 64>(lds, 4 * TILE);
+    lds_poison<NW * 64>(lds, short_lds<DP>());
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int half = lane >> 5;
     int idx = xcd_remap(blockIdx.x, gridDim.x);
@@ -87,13 +112,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_short_fwd_kernel(AttnArgs a) 
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb)
             if (word[kb]) {
-                s[kb] = short_scores<DT, DP>(lds + (kb >> 1) * TILE, kb & 1, lane, qf);
-                if (word[kb] != ~0u) {
-                    const uint32_t w = word[kb] >> (4 * half);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!((w >> (8 * (i / 4) + i % 4)) & 1)) s[kb][i] = -__builtin_inff();
-                }
+                s[kb] = short_scores<DT, DP>(lds + (kb >> 1) * TILE, kb & 1, lane, qf,
+                                             short_bias(lds + 4 * TILE, kb, half));
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) m = fmaxf(fmaxf(s[kb][i], s[kb][i + 1]), m);
             }
@@ -142,7 +162,7 @@ template <int DT, int DP, int NW>
 __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_short_rows_kernel(AttnArgs a) {
     constexpr int DB = DP / 32, KS = DP / 16, TILE = 64 * DP * 2;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-    lds_poison<NW * 64>(lds, 4 * TILE);
+    lds_poison<NW * 64>(lds, short_lds<DP>());
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int half = lane >> 5;
     int idx = xcd_remap(blockIdx.x, gridDim.x);
@@ -183,17 +203,15 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_short_rows_kern
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb)
             if (word[kb]) {
-                s[kb] = short_scores<DT, DP>(lds + (kb >> 1) * TILE, kb & 1, lane, qf);
-                dp[kb] = short_scores<DT, DP>(lds + (2 + (kb >> 1)) * TILE, kb & 1, lane, gf);
-                const uint32_t w = word[kb] >> (4 * half);
+                f32x16 zero;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) zero[i] = 0.0f;
+                s[kb] = short_scores<DT, DP>(lds + (kb >> 1) * TILE, kb & 1, lane, qf,
+                                             short_bias(lds + 4 * TILE, kb, half));
+                dp[kb] = short_scores<DT, DP>(lds + (2 + (kb >> 1)) * TILE, kb & 1, lane, gf, zero);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     s[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], a.c, -L));
-                if (word[kb] != ~0u) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!((w >> (8 * (i / 4) + i % 4)) & 1)) s[kb][i] = 0.0f;
-                }
                 float t[2] = {0, 0};
 #pragma unroll
                 for (int i = 0; i < 16; ++i) t[i & 1] = __builtin_fmaf(s[kb][i], dp[kb][i], t[i & 1]);

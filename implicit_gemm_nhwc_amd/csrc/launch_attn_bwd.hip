@@ -66,7 +66,7 @@ hipError_t launch_q(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
 template <int DT, int DP>
 hipError_t launch_short(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
     auto kern = attn_short_rows_kernel<DT, DP, kAttnWaves>;
-    constexpr size_t lds = 2 * (size_t)kShortKeys * DP * 2;
+    constexpr size_t lds = short_lds<DP>();
     static LdsAttr attr;
     const hipError_t e = ensure_lds(attr, (const void*)kern, lds);
     if (e != hipSuccess) return e;

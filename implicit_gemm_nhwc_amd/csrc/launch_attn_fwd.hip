@@ -25,7 +25,7 @@ hipError_t launch_rows(const AttnArgs& a, hipStream_t stream) {
 template <int DT, int DP>
 hipError_t launch_short(const AttnArgs& a, hipStream_t stream) {
     auto kern = attn_short_fwd_kernel<DT, DP, kAttnWaves>;
-    constexpr size_t lds = 2 * (size_t)kShortKeys * DP * 2;
+    constexpr size_t lds = short_lds<DP>();
     static LdsAttr attr;
     const hipError_t e = ensure_lds(attr, (const void*)kern, lds);
     if (e != hipSuccess) return e;
