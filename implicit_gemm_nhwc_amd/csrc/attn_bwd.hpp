@@ -129,22 +129,26 @@ __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnArgs a) {
     }
 }
 
-// Direct loads of packed rows r0 .. r0 + ROWS - 1 (see TileStage).
+// Direct loads of packed rows r0 .. r0 + ROWS - 1 (see TileStage).  Where the
+// group's heads divide the tile every tile starts a token, and its rows lie at
+// the offsets formed once (st.init_packed); other groups' offsets are formed
+// for each tile.
 template <int DP, int ROWS, int NW>
 __device__ __forceinline__ void issue_packed(const TileStage<DP, ROWS, NW>& st, const AttnArgs& a,
-                                             const uint8_t* base, int64_t pt, int64_t ph, int r0,
-                                             uint8_t* lds, int wave) {
+                                             bool fixed, const uint8_t* base, int64_t pt,
+                                             int64_t ph, int r0, uint8_t* lds, int wave, int lane) {
     const int t0 = div_g(a, r0);
+    if (fixed) {
+        st.issue_first(base + (int64_t)t0 * pt, a.rows - r0, lds, wave);
+        return;
+    }
     const __amdgpu_buffer_rsrc_t rs = attn_rsrc(base + (int64_t)t0 * pt);
 #pragma unroll
     for (int i = 0; i < TileStage<DP, ROWS, NW>::PER; ++i) {
-        if (!TileStage<DP, ROWS, NW>::EVEN && i * NW + wave >= TileStage<DP, ROWS, NW>::PIECES)
-            break;
-        const unsigned at = packed_off(a, r0 + st.row[i], t0, pt, ph) + (unsigned)st.chunk[i];
-        const unsigned off = st.chunk[i] >= 0 ? at : kOut;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rs, (__attribute__((address_space(3))) void*)(lds + (i * NW + wave) * 1024), 16, off,
-            0, 0, 0);
+        TileStage<DP, ROWS, NW> s;
+        const unsigned c = s.place(i, wave, lane, a.D);
+        const unsigned at = packed_off(a, r0 + s.row[i], t0, pt, ph) + c;
+        st.load(rs, i, c == kOut ? kOut : at, lds, wave);
     }
 }
 
@@ -163,7 +167,7 @@ struct KvShape {
     static constexpr int TILE = QT * DP * 2;
     static constexpr int STAGE = (2 * TILE + 2 * QT * 4 + 1023) / 1024 * 1024;  // q, do, lse, Delta
     static constexpr int KEYS = KV_LDS ? 2 * NWK * 32 * DP * 2 : 0;             // k, v
-    static constexpr int SUM = RG > 1 ? NWK * 64 * DP * 2 : 0;                  // over all of it
+    static constexpr int SUM = RG / 2 * NWK * 64 * DP * 2;                      // over all of it
     static constexpr int LDS = KEYS + 2 * STAGE > SUM ? KEYS + 2 * STAGE : SUM;
 };
 
@@ -199,15 +203,15 @@ __global__ __launch_bounds__(NWK * RG * 64, OCC) void attn_bwd_kv_kernel(AttnArg
     const uint8_t* kp = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h;
     const uint8_t* vp = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h;
     if constexpr (KV_LDS) {
-        TileStage<DP, 32, NW> ks;
-        ks.init(wave, lane, a.D);
+        TileStage<DP, 32, NW> ks, vs;
+        ks.init(wave, lane, a.D, (unsigned)a.k_t);
+        vs.init(wave, lane, a.D, (unsigned)a.v_t);
 #pragma unroll
         for (int w = 0; w < NWK; ++w) {
             const int k0 = (kt * NWK + w) * 32;
-            const uint64_t word = mask_word(mask_byte(mrow, k0, len, lane), len - k0);
-            ks.issue(kp + (int64_t)k0 * a.k_t, (unsigned)a.k_t, word, lds_all + w * 64 * DP, wave);
-            ks.issue(vp + (int64_t)k0 * a.v_t, (unsigned)a.v_t, word,
-                     lds_all + (NWK + w) * 64 * DP, wave);
+            const uint32_t word = (uint32_t)mask_word(mask_byte(mrow, k0, len, lane), len - k0);
+            ks.issue(kp + (int64_t)k0 * a.k_t, word, lds_all + w * 64 * DP, wave);
+            vs.issue(vp + (int64_t)k0 * a.v_t, word, lds_all + (NWK + w) * 64 * DP, wave);
         }
     } else {
         load_rows<DP>(attn_rsrc(kp + (int64_t)key0 * a.k_t),
@@ -228,18 +232,20 @@ __global__ __launch_bounds__(NWK * RG * 64, OCC) void attn_bwd_kv_kernel(AttnArg
     const uint8_t* gbase = a.dout + (int64_t)b * a.do_b + (int64_t)hk * a.G * a.do_h;
     const float* lse2 = a.stat + (int64_t)bh * a.rows_pad;
     const float* delta = a.stat + ((int64_t)a.B * a.Hk + bh) * a.rows_pad;
-    TileStage<DP, QT, NW> st;
-    st.init(wave, lane, a.D);
+    TileStage<DP, QT, NW> qs, gs;
+    const bool fixed = QT % a.G == 0;
+    qs.init_packed(a, wave, lane, a.q_t, a.q_h);
+    gs.init_packed(a, wave, lane, a.do_t, a.do_h);
     auto issue = [&](int r0, uint8_t* to) {
-        issue_packed(st, a, qbase, a.q_t, a.q_h, r0, to, wave);
-        issue_packed(st, a, gbase, a.do_t, a.do_h, r0, to + TILE, wave);
+        issue_packed(qs, a, fixed, qbase, a.q_t, a.q_h, r0, to, wave, lane);
+        issue_packed(gs, a, fixed, gbase, a.do_t, a.do_h, r0, to + TILE, wave, lane);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)   // QT floats each: lse, Delta
+        for (int x = 0; x < QT / 32; ++x)   // QT floats each: lse, then Delta
             if (wave == x % NW)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    attn_rsrc((x ? delta : lse2) + r0),
-                    (__attribute__((address_space(3))) void*)(to + 2 * TILE + x * QT * 4), 4,
-                    lane < QT ? (unsigned)lane * 4 : kOut, 0, 0, 0);
+                    attn_rsrc((x < QT / 64 ? lse2 : delta - QT) + r0 + x * 64),
+                    (__attribute__((address_space(3))) void*)(to + 2 * TILE + x * 256), 4,
+                    lane * 4, 0, 0, 0);
     };
     const uint8_t* kl = lds_all + wk * 64 * DP;
     const uint8_t* vl = kl + NWK * 64 * DP;
@@ -312,34 +318,38 @@ __global__ __launch_bounds__(NWK * RG * 64, OCC) void attn_bwd_kv_kernel(AttnArg
         }
     }
     if constexpr (RG > 1) {
-        // the second row group's sums through LDS, dk then dv, lane by lane
-        f32x4* x = reinterpret_cast<f32x4*>(lds_all) + (wk * 64 + lane);
+        // the row groups' sums through LDS, dk then dv, lane by lane: the upper
+        // half of the groups adds to the lower, until one is left
         constexpr int N = NWK * 64;   // f32x4 between a lane's
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            f32x16(&acc)[DB] = t ? dv : dk;
-            __syncthreads();
-            if (rg == 1) {
+        for (int n = RG / 2; n; n /= 2)
 #pragma unroll
-                for (int d = 0; d < DB; ++d)
+            for (int t = 0; t < 2; ++t) {
+                f32x16(&acc)[DB] = t ? dv : dk;
+                f32x4* x = reinterpret_cast<f32x4*>(lds_all) + (rg % n) * (N * DP / 8) +
+                           (wk * 64 + lane);
+                __syncthreads();
+                if (rg >= n && rg < 2 * n) {
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        x[(4 * d + g) * N] = f32x4{acc[d][4 * g], acc[d][4 * g + 1],
-                                                   acc[d][4 * g + 2], acc[d][4 * g + 3]};
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            x[(4 * d + g) * N] = f32x4{acc[d][4 * g], acc[d][4 * g + 1],
+                                                       acc[d][4 * g + 2], acc[d][4 * g + 3]};
+                }
+                __syncthreads();
+                if (rg < n) {
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const f32x4 y = x[(4 * d + g) * N];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[d][4 * g + i] += y[i];
+                        }
+                }
             }
-            __syncthreads();
-            if (rg == 0) {
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const f32x4 y = x[(4 * d + g) * N];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[d][4 * g + i] += y[i];
-                    }
-            }
-        }
-        if (rg == 1) return;
+        if (rg >= 1) return;
     }
     const float fk = a.scale / f, fv = DT == DT_FP16 ? 0.00006103515625f : 1.0f;
 #pragma unroll
@@ -421,13 +431,13 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_bwd_q_kernel(AttnArgs a) {
     const uint8_t* kbase = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h;
     const uint8_t* vbase = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h;
     const uint8_t* mrow = a.mask ? a.mask + (int64_t)b * a.mask_b : nullptr;
-    TileStage<DP, KT, NW> st;
-    st.init(wave, lane, a.D);
-    const unsigned kp = (unsigned)a.k_t, vp = (unsigned)a.v_t;
+    TileStage<DP, KT, NW> ks, vs;
+    ks.init(wave, lane, a.D, (unsigned)a.k_t);
+    vs.init(wave, lane, a.D, (unsigned)a.v_t);
     if (j_begin < j_end) {
         uint64_t word = mask_word(mask_byte(mrow, j_begin, j_end, lane), j_end - j_begin);
-        st.issue(kbase + (int64_t)j_begin * a.k_t, kp, word, lds, wave);
-        st.issue(vbase + (int64_t)j_begin * a.v_t, vp, word, lds + TILE, wave);
+        ks.issue(kbase + (int64_t)j_begin * a.k_t, word, lds, wave);
+        vs.issue(vbase + (int64_t)j_begin * a.v_t, word, lds + TILE, wave);
         uint32_t mb = mask_byte(mrow, j_begin + KT, j_end, lane);
         int buf = 0;
         for (int j = j_begin; j < j_end; j += KT) {
@@ -438,8 +448,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_bwd_q_kernel(AttnArgs a) {
             const uint64_t next = mask_word(mb, j_end - (j + KT));
             if (j + KT < j_end) {
                 uint8_t* nl = lds + (buf ^ 1) * 2 * TILE;
-                st.issue(kbase + (int64_t)(j + KT) * a.k_t, kp, next, nl, wave);
-                st.issue(vbase + (int64_t)(j + KT) * a.v_t, vp, next, nl + TILE, wave);
+                ks.issue(kbase + (int64_t)(j + KT) * a.k_t, next, nl, wave);
+                vs.issue(vbase + (int64_t)(j + KT) * a.v_t, next, nl + TILE, wave);
                 mb = mask_byte(mrow, j + 2 * KT, j_end, lane);
             }
             if (word != 0) {

@@ -129,17 +129,20 @@ __device__ __forceinline__ i32x4 frag_row(const uint8_t* lds, int r, int c) {
     return *reinterpret_cast<const i32x4*>(lds + tile_off<DP>(r, c));
 }
 
-__device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
+// One transposing read.  The pointer is restrict only for its side effect:
+// inlining then leaves alias metadata on the read, without which the compiler
+// makes it wait for every direct load to LDS in flight, the next tile's among
+// them.  The kernels order those loads by their own waits and barriers.
+__device__ __forceinline__ u32x2 read_tr(const uint8_t* __restrict__ p) {
     typedef __attribute__((address_space(3))) s16x4* lp;
     typedef __attribute__((address_space(3))) const uint8_t* bp;
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(bp)p));
 }
 
 // Operand whose row / column is column 32 * db + l % 32 of the tile and whose
-// k slots are the tile's rows r0 + 8 * (j / 4) + 4 * h + j % 4.  The 16 lanes
-// of a transposing read address 4 rows x 32 bytes: lane i row i / 4, bytes
-// 8 * (i % 4); `lane` terms are folded into tr_off, computed once:
-//   row 4 * h + (l % 16) / 4, chunk 4 * db + 2 * ((l / 16) % 2) + (l % 4) / 2.
+// k slots are the tile's rows r0 + 8 * (j / 4) + 4 * h + j % 4, by transposing
+// reads: their 16 lanes address 4 rows x 32 bytes, lane i row i / 4, bytes
+// 8 * (i % 4).
 template <int DP>
 __device__ __forceinline__ i32x4 frag_col(const uint8_t* lds, int r0, int db, int lane) {
     const int r = r0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
@@ -168,37 +171,69 @@ __device__ __forceinline__ uint32_t mask_byte(const uint8_t* row, int j0, int en
 // 1 KB pieces (64 lanes x 16 bytes in LDS order), so a lane's LDS place fixes
 // its row and, through the swizzle, the chunk it has to fetch.  Lanes whose
 // chunk is past D or whose row is not to be read get an offset out of range,
-// which stores zeros.
+// which stores zeros.  The offsets are the same for every tile, formed once.
 template <int DP, int ROWS, int NW>
 struct TileStage {
     static constexpr int PIECES = ROWS * DP * 2 / 1024;
     static constexpr int PER = (PIECES + NW - 1) / NW;
     static constexpr bool EVEN = PIECES % NW == 0;
-    int row[PER], chunk[PER];
+    int row[PER];
+    unsigned off[PER];
 
-    __device__ __forceinline__ void init(int wave, int lane, int D) {
+    // first byte of the lane's chunk in its row, kOut for a chunk past D
+    __device__ __forceinline__ unsigned place(int i, int wave, int lane, int D) {
+        const int p = ((i * NW + wave) * 1024 + lane * 16);
+        row[i] = p / (DP * 2);
+        const int c = ((p % (DP * 2)) >> 4) ^ lds_swz<DP>(row[i]);
+        return c * 8 < D ? (unsigned)c * 16 : kOut;
+    }
+    // rows of `pitch` bytes
+    __device__ __forceinline__ void init(int wave, int lane, int D, unsigned pitch) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int p = ((i * NW + wave) * 1024 + lane * 16);
-            row[i] = p / (DP * 2);
-            const int c = ((p % (DP * 2)) >> 4) ^ lds_swz<DP>(row[i]);
-            chunk[i] = c * 8 < D ? c * 16 : -1;
+            const unsigned c = place(i, wave, lane, D);
+            off[i] = c == kOut ? kOut : c + (unsigned)row[i] * pitch;
         }
     }
-    // rows of `pitch` bytes from base; bit r of `valid` says row r is read
-    __device__ __forceinline__ void issue(const uint8_t* base, unsigned pitch, uint64_t valid,
-                                          uint8_t* lds, int wave) const {
-        const __amdgpu_buffer_rsrc_t rs = attn_rsrc(base);
+    // packed rows of a tile that starts with a group's first head
+    __device__ __forceinline__ void init_packed(const AttnArgs& a, int wave, int lane, int64_t pt,
+                                                int64_t ph) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            if (!EVEN && i * NW + wave >= PIECES) break;
-            const bool ok = chunk[i] >= 0 && ((valid >> row[i]) & 1);
-            const unsigned at = (unsigned)row[i] * pitch + (unsigned)chunk[i];
-            const unsigned off = ok ? at : kOut;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rs, (__attribute__((address_space(3))) void*)(lds + (i * NW + wave) * 1024), 16,
-                off, 0, 0, 0);
+            const unsigned c = place(i, wave, lane, a.D);
+            const int tok = div_g(a, row[i]);
+            const unsigned at = (unsigned)tok * (unsigned)pt +
+                                (unsigned)(row[i] - tok * a.G) * (unsigned)ph + c;
+            off[i] = c == kOut ? kOut : at;
         }
+    }
+    __device__ __forceinline__ void load(const __amdgpu_buffer_rsrc_t& rs, int i, unsigned at,
+                                         uint8_t* lds, int wave) const {
+        if (!EVEN && i * NW + wave >= PIECES) return;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rs, (__attribute__((address_space(3))) void*)(lds + (i * NW + wave) * 1024), 16, at, 0,
+            0, 0);
+    }
+    // bit r of `valid` says row r is read
+    __device__ __forceinline__ void issue(const uint8_t* base, uint64_t valid, uint8_t* lds,
+                                          int wave) const {
+        const __amdgpu_buffer_rsrc_t rs = attn_rsrc(base);
+        constexpr uint64_t all = ~0ull >> (64 - ROWS);
+        if (valid == all) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) load(rs, i, off[i], lds, wave);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                load(rs, i, (valid >> row[i]) & 1 ? off[i] : kOut, lds, wave);
+        }
+    }
+    // the first n rows
+    __device__ __forceinline__ void issue_first(const uint8_t* base, int n, uint8_t* lds,
+                                                int wave) const {
+        const __amdgpu_buffer_rsrc_t rs = attn_rsrc(base);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) load(rs, i, row[i] < n ? off[i] : kOut, lds, wave);
     }
 };
 

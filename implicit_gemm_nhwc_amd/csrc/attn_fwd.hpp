@@ -106,8 +106,14 @@ __device__ __forceinline__ void fwd_finish(const AttnArgs& a, int b, int hk, int
 // ---------------------------------------------------------------------------
 // Many rows: NW waves of QB blocks of 32 rows walk the keys in tiles of 64,
 // double buffered in LDS through direct loads, one barrier a tile.
+// Waves a SIMD that the registers of the kernel below are cut to (and its LDS
+// allows): one register more than 512 / waves costs a wave.
+constexpr int fwd_waves(int dp, int qb) {
+    return qb > 1 ? 1 : dp <= 64 ? 4 : dp <= 96 ? 3 : 2;
+}
+
 template <int DT, int DP, int QB, int NW>
-__global__ __launch_bounds__(NW * 64, QB == 1 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
+__global__ __launch_bounds__(NW * 64, fwd_waves(DP, QB)) void attn_fwd_kernel(AttnArgs a) {
     constexpr int KT = 64, KB = 2, DB = DP / 32, KS = DP / 16;
     constexpr int TILE = KT * DP * 2;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -146,14 +152,14 @@ __global__ __launch_bounds__(NW * 64, QB == 1 ? 2 : 1) void attn_fwd_kernel(Attn
     const uint8_t* kbase = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h;
     const uint8_t* vbase = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h;
     const uint8_t* mrow = a.mask ? a.mask + (int64_t)b * a.mask_b : nullptr;
-    TileStage<DP, KT, NW> st;
-    st.init(wave, lane, a.D);
-    const unsigned kp = (unsigned)a.k_t, vp = (unsigned)a.v_t;
+    TileStage<DP, KT, NW> ks, vs;
+    ks.init(wave, lane, a.D, (unsigned)a.k_t);
+    vs.init(wave, lane, a.D, (unsigned)a.v_t);
 
     if (j_begin < j_end) {
         uint64_t word = mask_word(mask_byte(mrow, j_begin, j_end, lane), j_end - j_begin);
-        st.issue(kbase + (int64_t)j_begin * a.k_t, kp, word, lds, wave);
-        st.issue(vbase + (int64_t)j_begin * a.v_t, vp, word, lds + TILE, wave);
+        ks.issue(kbase + (int64_t)j_begin * a.k_t, word, lds, wave);
+        vs.issue(vbase + (int64_t)j_begin * a.v_t, word, lds + TILE, wave);
         uint32_t mb = mask_byte(mrow, j_begin + KT, j_end, lane);
         int buf = 0;
         for (int j = j_begin; j < j_end; j += KT) {
@@ -164,8 +170,8 @@ __global__ __launch_bounds__(NW * 64, QB == 1 ? 2 : 1) void attn_fwd_kernel(Attn
             const uint64_t next = mask_word(mb, j_end - (j + KT));
             if (j + KT < j_end) {
                 uint8_t* nl = lds + (buf ^ 1) * 2 * TILE;
-                st.issue(kbase + (int64_t)(j + KT) * a.k_t, kp, next, nl, wave);
-                st.issue(vbase + (int64_t)(j + KT) * a.v_t, vp, next, nl + TILE, wave);
+                ks.issue(kbase + (int64_t)(j + KT) * a.k_t, next, nl, wave);
+                vs.issue(vbase + (int64_t)(j + KT) * a.v_t, next, nl + TILE, wave);
                 mb = mask_byte(mrow, j + 2 * KT, j_end, lane);
             }
             if (word != 0) {
@@ -257,10 +263,10 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
     const uint8_t* kbase = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h;
     const uint8_t* vbase = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h;
     const uint8_t* mrow = a.mask ? a.mask + (int64_t)b * a.mask_b : nullptr;
-    TileStage<DP, KT, 1> st;
-    st.init(0, lane, a.D);
+    TileStage<DP, KT, 1> ks, vs;
+    ks.init(0, lane, a.D, (unsigned)a.k_t);
+    vs.init(0, lane, a.D, (unsigned)a.v_t);
     constexpr int LOADS = 2 * TileStage<DP, KT, 1>::PIECES;
-    const unsigned kp = (unsigned)a.k_t, vp = (unsigned)a.v_t;
     constexpr int STEP = NW * KT;
 
     auto word_at = [&](uint32_t mb, int j) -> uint32_t {
@@ -268,8 +274,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
     };
     if (j_begin < j_end) {
         uint32_t w0 = word_at(mask_byte(mrow, j_begin, j_end, lane), j_begin), w1 = 0;
-        st.issue(kbase + (int64_t)j_begin * a.k_t, kp, w0, mine, 0);
-        st.issue(vbase + (int64_t)j_begin * a.v_t, vp, w0, mine + TILE, 0);
+        ks.issue(kbase + (int64_t)j_begin * a.k_t, w0, mine, 0);
+        vs.issue(vbase + (int64_t)j_begin * a.v_t, w0, mine + TILE, 0);
         uint32_t mb = mask_byte(mrow, j_begin + STEP, j_end, lane);
         int buf = 0;
         for (int j = j_begin; j < j_end; j += STEP) {
@@ -279,8 +285,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
                 // the reads of this buffer two blocks ago have returned: the
                 // products that used them are in program order before
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                st.issue(kbase + (int64_t)(j + STEP) * a.k_t, kp, w1, nl, 0);
-                st.issue(vbase + (int64_t)(j + STEP) * a.v_t, vp, w1, nl + TILE, 0);
+                ks.issue(kbase + (int64_t)(j + STEP) * a.k_t, w1, nl, 0);
+                vs.issue(vbase + (int64_t)(j + STEP) * a.v_t, w1, nl + TILE, 0);
                 mb = mask_byte(mrow, j + 2 * STEP, j_end, lane);
                 // all but the block just requested (the mask byte is younger)
                 asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");

@@ -28,17 +28,17 @@ __device__ __forceinline__ void stage_short(const AttnArgs& a, int b, int hk, in
     const uint8_t* kbase = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h;
     const uint8_t* vbase = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h;
     const uint8_t* mrow = a.mask ? a.mask + (int64_t)b * a.mask_b : nullptr;
-    TileStage<DP, 64, NW> st;
-    st.init(wave, lane, a.D);
+    TileStage<DP, 64, NW> ks, vs;
+    ks.init(wave, lane, a.D, (unsigned)a.k_t);
+    vs.init(wave, lane, a.D, (unsigned)a.v_t);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const uint64_t w = mask_word(mask_byte(mrow, 64 * t, len, lane), len - 64 * t);
         word[2 * t] = (uint32_t)w;
         word[2 * t + 1] = (uint32_t)(w >> 32);
         if (w == 0) continue;
-        st.issue(kbase + (int64_t)(64 * t) * a.k_t, (unsigned)a.k_t, w, lds + t * TILE, wave);
-        st.issue(vbase + (int64_t)(64 * t) * a.v_t, (unsigned)a.v_t, w, lds + (2 + t) * TILE,
-                 wave);
+        ks.issue(kbase + (int64_t)(64 * t) * a.k_t, w, lds + t * TILE, wave);
+        vs.issue(vbase + (int64_t)(64 * t) * a.v_t, w, lds + (2 + t) * TILE, wave);
     }
     if (wave == 0) {
         float* bias = reinterpret_cast<float*>(lds + 4 * TILE);
@@ -81,7 +81,7 @@ __device__ __forceinline__ f32x16 short_bias(const uint8_t* bias, int kb, int ha
 }
 
 template <int DT, int DP, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void attn_short_fwd_kernel(AttnArgs a) {
+__global__ __launch_bounds__(NW * 64, DP > 64 ? 2 : 3) void attn_short_fwd_kernel(AttnArgs a) {
     constexpr int DB = DP / 32, KS = DP / 16, TILE = 64 * DP * 2;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     lds_poison<NW * 64>(lds, short_lds<DP>());
@@ -139,8 +139,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_short_fwd_kernel(AttnArgs a) 
                 for (int g = 0; g < 2; ++g)
 #pragma unroll
                     for (int d = 0; d < DB; ++d) {
-                        const i32x4 vf = frag_col<DP>(lds + (2 + (kb >> 1)) * TILE,
-                                                      32 * (kb & 1) + 16 * g, d, lane);
+                        const i32x4 vf =
+                            frag_col<DP>(lds + (4 + kb) * (TILE / 2), 16 * g, d, lane);
                         acc[d] = mfma32<DT>(&vf, &pf[g], acc[d]);
                     }
             }
@@ -251,8 +251,7 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_short_rows_kern
                     for (int g = 0; g < 2; ++g)
 #pragma unroll
                         for (int d = 0; d < DB; ++d) {
-                            const i32x4 kt = frag_col<DP>(lds + (kb >> 1) * TILE,
-                                                          32 * (kb & 1) + 16 * g, d, lane);
+                            const i32x4 kt = frag_col<DP>(lds + kb * (TILE / 2), 16 * g, d, lane);
                             dq[d] = mfma32<DT>(&kt, &df[g], dq[d]);
                         }
                 }

@@ -39,7 +39,11 @@ hipError_t launch_kv(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
 // wave a SIMD 375, spilling 467).
 template <int DT, int DP, int NWK>
 hipError_t launch_kv_dp(const AttnArgs& a, const AttnGradPlan& p, hipStream_t stream) {
-    return launch_kv<DT, DP, NWK, 2, kRowTile, (DP > 64), 2>(a, p, stream);
+    #ifndef KV64
+#define KV64 2, 64, false, 2
+#endif
+    if constexpr (DP <= 64) return launch_kv<DT, DP, NWK, KV64>(a, p, stream);
+    else return launch_kv<DT, DP, NWK, 2, 64, true, 2>(a, p, stream);
 }
 
 template <int DT, int DP>
