@@ -183,7 +183,7 @@ __global__ __launch_bounds__(NWK * RG * 64, OCC) void attn_bwd_kv_kernel(AttnArg
     const int half = lane >> 5;
     const int wk = RG > 1 ? wave % NWK : wave, rg = RG > 1 ? wave / NWK : 0;
 
-    int idx = xcd_remap(blockIdx.x, gridDim.x);
+    int idx = launch_place(a);
     const int kt = idx % a.key_tiles;
     idx /= a.key_tiles;
     const int sp = idx % a.nsplit;
@@ -397,7 +397,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_bwd_q_kernel(AttnArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int half = lane >> 5;
 
-    int idx = xcd_remap(blockIdx.x, gridDim.x);
+    int idx = launch_place(a);
     const int rt = idx % a.row_tiles;
     idx /= a.row_tiles;
     const int sp = idx % a.nsplit;

@@ -93,6 +93,17 @@ __device__ __forceinline__ unsigned packed_off(const AttnArgs& a, int row, int t
     return row < a.rows ? off : kOut;
 }
 
+// This workgroup's place in the launch order.  Workgroups that share a key
+// head follow one another there, and where all heads cost the same each XCD
+// takes one run of them, so that its L2 holds few heads' keys (16384 rows x
+// 4096 keys of 128, 32 heads).  With ragged lengths a run of long heads would
+// leave the other XCDs idle: the hardware's round-robin order then deals
+// every head's workgroups to all of them (4 x 3136 x 1333 ragged: 115 -> 73 us, the
+// masked tiles' cheaper start included).
+__device__ __forceinline__ int launch_place(const AttnArgs& a) {
+    return a.lens || a.mask ? (int)blockIdx.x : xcd_remap(blockIdx.x, gridDim.x);
+}
+
 // lse entry of a packed row of key head hk, from lse_base.
 __device__ __forceinline__ unsigned lse_off(const AttnArgs& a, int row) {
     const int tok = div_g(a, row);

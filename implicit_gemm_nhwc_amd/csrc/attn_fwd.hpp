@@ -112,16 +112,20 @@ constexpr int fwd_waves(int dp, int qb) {
     return qb > 1 ? 1 : dp <= 64 ? 4 : dp <= 96 ? 3 : 2;
 }
 
-template <int DT, int DP, int QB, int NW>
+// MASK: a key mask is given, so that any tile may have keys that are not
+// valid; their score products then start from -inf (LDS), which costs eight
+// LDS reads a tile instead of three instructions a score.
+template <int DT, int DP, int QB, int NW, bool MASK>
 __global__ __launch_bounds__(NW * 64, fwd_waves(DP, QB)) void attn_fwd_kernel(AttnArgs a) {
     constexpr int KT = 64, KB = 2, DB = DP / 32, KS = DP / 16;
     constexpr int TILE = KT * DP * 2;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-    lds_poison<NW * 64>(lds, 4 * TILE);
+    lds_poison<NW * 64>(lds, 4 * TILE + 2 * KT * 4);
+    float* bias = reinterpret_cast<float*>(lds + 4 * TILE);   // [2][KT], MASK
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int half = lane >> 5;
 
-    int idx = xcd_remap(blockIdx.x, gridDim.x);
+    int idx = launch_place(a);
     const int rt = idx % a.row_tiles;
     idx /= a.row_tiles;
     const int sp = idx % a.nsplit;
@@ -161,6 +165,7 @@ __global__ __launch_bounds__(NW * 64, fwd_waves(DP, QB)) void attn_fwd_kernel(At
         ks.issue(kbase + (int64_t)j_begin * a.k_t, word, lds, wave);
         vs.issue(vbase + (int64_t)j_begin * a.v_t, word, lds + TILE, wave);
         uint32_t mb = mask_byte(mrow, j_begin + KT, j_end, lane);
+        if (MASK && wave == 0) bias[lane] = (word >> lane) & 1 ? 0.0f : -__builtin_inff();
         int buf = 0;
         for (int j = j_begin; j < j_end; j += KT) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -173,6 +178,8 @@ __global__ __launch_bounds__(NW * 64, fwd_waves(DP, QB)) void attn_fwd_kernel(At
                 ks.issue(kbase + (int64_t)(j + KT) * a.k_t, next, nl, wave);
                 vs.issue(vbase + (int64_t)(j + KT) * a.v_t, next, nl + TILE, wave);
                 mb = mask_byte(mrow, j + 2 * KT, j_end, lane);
+                if (MASK && wave == 0)
+                    bias[(buf ^ 1) * KT + lane] = (next >> lane) & 1 ? 0.0f : -__builtin_inff();
             }
             if (word != 0) {
                 f32x16 s[QB][KB];
@@ -181,7 +188,14 @@ __global__ __launch_bounds__(NW * 64, fwd_waves(DP, QB)) void attn_fwd_kernel(At
 #pragma unroll
                     for (int r = 0; r < QB; ++r)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) s[r][kb][i] = 0.0f;
+                        for (int g = 0; g < 4; ++g) {
+                            f32x4 x = {0, 0, 0, 0};
+                            if constexpr (MASK)
+                                x = *reinterpret_cast<const f32x4*>(bias + buf * KT + 32 * kb +
+                                                                    8 * g + 4 * half);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) s[r][kb][4 * g + i] = x[i];
+                        }
 #pragma unroll
                     for (int x = 0; x < KS; ++x) {
                         const i32x4 kf = frag_row<DP>(kl, 32 * kb + (lane & 31), 2 * x + half);
@@ -193,8 +207,8 @@ __global__ __launch_bounds__(NW * 64, fwd_waves(DP, QB)) void attn_fwd_kernel(At
                 i32x4 pf[QB][KB][2];
 #pragma unroll
                 for (int r = 0; r < QB; ++r) {
-                    softmax_step<DT, KB, DB>(s[r], word, word == ~0ull, a.c, m[r], l[r], acc[r],
-                                             half);
+                    softmax_step<DT, KB, DB>(s[r], word, MASK || word == ~0ull, a.c, m[r], l[r],
+                                             acc[r], half);
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb) {
                         float p[16];
@@ -242,7 +256,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
     float* st_m = reinterpret_cast<float*>(lds + NW * 2 * STAGE);   // [NW][32] m, then l
     float* st_l = st_m + NW * 32;
 
-    int idx = xcd_remap(blockIdx.x, gridDim.x);
+    int idx = launch_place(a);
     const int sp = idx % a.nsplit;
     idx /= a.nsplit;
     const int hk = idx % a.Hk, b = idx / a.Hk;

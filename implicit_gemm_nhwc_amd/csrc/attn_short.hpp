@@ -87,7 +87,7 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 2 : 3) void attn_short_fwd_kerne
     lds_poison<NW * 64>(lds, short_lds<DP>());
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int half = lane >> 5;
-    int idx = xcd_remap(blockIdx.x, gridDim.x);
+    int idx = launch_place(a);
     const int first = idx % a.row_tiles * NW + wave;
     idx /= a.row_tiles;
     const int hk = idx % a.Hk, b = idx / a.Hk;
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_short_rows_kern
     lds_poison<NW * 64>(lds, short_lds<DP>());
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int half = lane >> 5;
-    int idx = xcd_remap(blockIdx.x, gridDim.x);
+    int idx = launch_place(a);
     const int first = idx % a.row_tiles * NW + wave;
     const int bh = idx / a.row_tiles;
     const int hk = bh % a.Hk, b = bh / a.Hk;
