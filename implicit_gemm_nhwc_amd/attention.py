@@ -38,7 +38,7 @@ def _view(name, t, dtype, device):
     """(pointer, batch, token, head stride) of a [batch, token, head, D] tensor."""
     if not isinstance(t, torch.Tensor):
         raise InvalidArgument(f"{name} must be a tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise InvalidArgument(f"{name} dtype {t.dtype} differs from {dtype}")
     if t.get_device() != device:
         raise InvalidArgument(f"{name} is on {t.device}, the other tensors on GPU {device}")
@@ -54,13 +54,13 @@ def _small(name, t, dtype, device):
     """Pointer of a dense side tensor (or None)."""
     if t is None:
         return 0
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise InvalidArgument(f"{name} must be {dtype} (got {t.dtype})")
     if t.get_device() != device:
         raise InvalidArgument(f"{name} is on {t.device}, the other tensors on GPU {device}")
-    if not t.is_contiguous():
-        raise InvalidArgument(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise InvalidArgument(f"{name} must be contiguous")
 
 
 def _device(t, name="q"):
@@ -167,6 +167,8 @@ def _attn_args(q, k, v, out, lse, kv_lens, key_mask, scale):
 
 def _like(t):
     """A new dense tensor of t's shape and type."""
+    if t.is_contiguous():
+        return torch.empty_like(t)
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
@@ -302,93 +304,90 @@ def cross_attention_bwd(dout, q, k, v, out, lse, *, scale=None, kv_lens=None, ke
 
 
 # ------------------------------------------- norm of queries and keys, rotation
-def _part(n, x, weight, table, positions, dtype, device, d, rot):
-    """Sizes and input view of an igc_qk_part, and what follows its views but
-    for the weight gradient."""
+def _part(n, x, grad, out, dw, weight, table, positions, dtype, device, d):
+    """All fields of an igc_qk_part.  out: a tensor to check, or the view of a
+    new one; dw: a tensor to check, a pointer or 0."""
     xv = _view(n, x, dtype, device)
-    b, t, h, dd = x.shape
+    shape = x.shape
+    b, t, h, dd = shape
     if dd != d:
         raise InvalidArgument(f"{n} has heads of {dd}, not {d}")
-    wp = tp = rows = pp = ps = 0
+    g = _NO_VIEW
+    if grad is not None:
+        g = _view(n + "'s gradient", grad, dtype, device)
+        if grad.shape != shape:
+            raise InvalidArgument(f"d{n} must have {n}'s shape {tuple(shape)}")
+    if not isinstance(out, tuple):
+        o, out = out, _view(n + "'s output", out, dtype, device)
+        if o.shape != shape:
+            raise InvalidArgument(f"{n}'s output must have its shape {tuple(shape)}")
+    wp = 0
     if weight is not None:
-        wp = _small(n + "_weight", weight, torch.float32, device)
-        if weight.shape != (d,):
+        wp = _small("weight", weight, torch.float32, device)
+        if weight.dim() != 1 or len(weight) != d:
             raise InvalidArgument(f"{n}_weight must be {(d,)} (got {tuple(weight.shape)})")
-    if table is not None:
-        tp = _small(n + "_table", table, torch.float32, device)
-        rows = table.shape[0]
+    if isinstance(dw, torch.Tensor):
+        if dw.shape != (d,):
+            raise InvalidArgument(f"the gradient of {n}_weight must be {(d,)}")
+        dw = _small("weight gradient", dw, torch.float32, device)
+    pp = ps = 0
     if positions is not None:
-        if positions.dtype != torch.int32:
-            raise InvalidArgument(f"{n}_positions must be int32 (got {positions.dtype})")
+        if positions.dtype is not torch.int32 or positions.dim() != 2:
+            raise InvalidArgument(f"{n}_positions must be int32 [batch, token] (got "
+                                  f"{positions.dtype}, {tuple(positions.shape)})")
         if positions.get_device() != device:
             raise InvalidArgument(f"{n}_positions is not on the tensors' GPU")
-        if positions.shape != (b, t):
-            raise InvalidArgument(f"{n}_positions must be {(b, t)} (got "
-                                  f"{tuple(positions.shape)})")
+        pb, pt = positions.shape
         ps, inner = positions.stride()
+        if pb != b or pt != t:
+            raise InvalidArgument(f"{n}_positions must be {(b, t)} (got {(pb, pt)})")
         if inner != 1 and t > 1:
             raise InvalidArgument(f"{n}_positions: the tokens of a batch entry must be adjacent")
         pp = positions.data_ptr()
-    return (b, t, h) + xv, wp, (tp, rows, pp, ps)
+    return (b, t, h, *xv, *g, *out, wp, dw or 0, *table, pp, ps)
 
 
-def _rotated(x, table, name):
-    """Values that the table turns (0 without one), None for an absent x."""
-    if x is None:
-        return None
-    if table is None:
-        return 0
-    if table.dim() != 2:
-        raise InvalidArgument(f"{name} must be [rows, rotated values] (got "
-                              f"{tuple(table.shape)})")
-    return table.shape[1]
+def _table(t, name, device):
+    """(pointer, rows) of a rotation table and the values it turns."""
+    if t is None:
+        return (0, 0), 0
+    if t.dim() != 2:
+        raise InvalidArgument(f"{name} must be [rows, rotated values] (got {tuple(t.shape)})")
+    rows, rot = t.shape
+    return (_small(name, t, torch.float32, device), rows), rot
 
 
-def _same_shape(name, t, x, dtype, device):
-    v = _view(name, t, dtype, device)
-    if t.shape != x.shape:
-        raise InvalidArgument(f"{name} must have its input's shape {tuple(x.shape)}")
-    return v
+_NONE2 = (None, None)
 
 
 def _qk_pack(q, k, grads, outs, dweights, q_weight, k_weight, q_table, k_table, q_positions,
              k_positions, eps, interleaved, ws=(0, 0)):
-    """igc_qk_norm, packed.  grads and dweights: pairs or None; outs: a pair
-    of tensors to check, or of views of new ones."""
+    """igc_qk_norm, packed.  grads, outs and dweights: pairs (_part)."""
     first = q if q is not None else k
     device = _device(first, "q" if q is not None else "k")
     dtype = first.dtype
-    if dtype not in DTYPE_CODES:
+    code = DTYPE_CODES.get(dtype)
+    if code is None:
         raise InvalidArgument(f"dtype {dtype} is not bf16 or fp16")
     if first.dim() != 4:
         raise InvalidArgument(f"tensors must be [batch, token, head, D] (got "
                               f"{tuple(first.shape)})")
     d = first.shape[3]
-    rot, rot_k = _rotated(q, q_table, "q_table"), _rotated(k, k_table, "k_table")
-    if rot is None:
-        rot = rot_k
-    elif rot_k is not None and rot_k != rot:
-        raise InvalidArgument("q_table and k_table must rotate the same number of values")
-    flat = ()
-    for i, (n, x, w, tab, pos) in enumerate((("q", q, q_weight, q_table, q_positions),
-                                             ("k", k, k_weight, k_table, k_positions))):
-        if x is None:
-            flat += _NO_PART
-            continue
-        head, wp, tail = _part(n, x, w, tab, pos, dtype, device, d, rot)
-        g = _NO_VIEW if grads is None else _same_shape("d" + n, grads[i], x, dtype, device)
-        o = outs[i]
-        if not isinstance(o, tuple):
-            o = _same_shape(n + " output", o, x, dtype, device)
-        dw = 0
-        if dweights is not None and dweights[i] is not None:
-            dw = dweights[i]
-            if isinstance(dw, torch.Tensor):
-                if dw.shape != (d,):
-                    raise InvalidArgument(f"the gradient of {n}_weight must be {(d,)}")
-                dw = _small(n + "_weight gradient", dw, torch.float32, device)
-        flat += head + g + o + (wp, dw) + tail
-    return _QK.pack(*flat, d, rot, 1 if interleaved else 0, DTYPE_CODES[dtype], eps, *ws), device
+    a = b = _NO_PART
+    rot = None
+    if q is not None:
+        table, rot = _table(q_table, "q_table", device)
+        a = _part("q", q, grads[0], outs[0], dweights[0], q_weight, table, q_positions, dtype,
+                  device, d)
+    if k is not None:
+        if q is None or k_table is not q_table:
+            table, rot_k = _table(k_table, "k_table", device)
+            if rot is not None and rot_k != rot:
+                raise InvalidArgument("q_table and k_table must rotate the same number of values")
+            rot = rot_k
+        b = _part("k", k, grads[1], outs[1], dweights[1], k_weight, table, k_positions, dtype,
+                  device, d)
+    return _QK.pack(*a, *b, d, rot, 1 if interleaved else 0, code, eps, *ws), device
 
 
 def _dense(t, shape):
@@ -403,7 +402,7 @@ def qk_norm_rope_fwd(q, k, q_out, k_out, *, q_weight=None, k_weight=None, q_tabl
     """Enqueue the norm and rotation of q and k (either may be None) into
     q_out, k_out (q and k themselves: in place).  1 handled, 0 declined, < 0
     HIP error."""
-    packed, device = _qk_pack(q, k, None, (q_out, k_out), None, q_weight, k_weight, q_table,
+    packed, device = _qk_pack(q, k, _NONE2, (q_out, k_out), _NONE2, q_weight, k_weight, q_table,
                               k_table, q_positions, k_positions, eps, interleaved)
     if _elsewhere(device, stream):
         with _on(device, stream):
@@ -416,7 +415,7 @@ def qk_norm_rope_fwd_check(q, k, q_out, k_out, *, q_weight=None, k_weight=None, 
                            interleaved=False) -> int:
     """Host-only gate of qk_norm_rope_fwd: 0 or a decline reason code."""
     return lib().qk_norm_rope_fwd_check(
-        _qk_pack(q, k, None, (q_out, k_out), None, q_weight, k_weight, q_table, k_table,
+        _qk_pack(q, k, _NONE2, (q_out, k_out), _NONE2, q_weight, k_weight, q_table, k_table,
                  q_positions, k_positions, eps, interleaved)[0])
 
 
@@ -454,7 +453,7 @@ def qk_norm_rope(q, k=None, *, q_weight=None, k_weight=None, q_table=None, k_tab
     else:
         k_out = _like(k)
         outs = (_dense(q_out, q.shape), _dense(k_out, k.shape))
-    packed, _ = _qk_pack(q, k, None, outs, None, q_weight, k_weight, q_table, k_table,
+    packed, _ = _qk_pack(q, k, _NONE2, outs, _NONE2, q_weight, k_weight, q_table, k_table,
                          q_positions, k_positions, eps, interleaved)
     L = lib()
     rc = L.qk_norm_rope_fwd(packed, _raw_stream(device))
@@ -479,16 +478,16 @@ def qk_norm_rope_bwd(dq, dk, q, k=None, *, q_weight=None, k_weight=None, q_table
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise InvalidArgument("q and k must be [batch, token, head, D]")
     d = q.shape[3]
-    dw = torch.empty((2, d), dtype=torch.float32, device=q.device)
-    dqw, dkw = dw.unbind(0)
+    dqw = torch.empty(d, dtype=torch.float32, device=q.device)
     dq_out = _like(q)
     if k is None:
         dk_out = dkw = None
-        outs, dws = (_dense(dq_out, q.shape), None), (dw.data_ptr(), None)
+        outs, dws = (_dense(dq_out, q.shape), None), (dqw.data_ptr(), None)
     else:
         dk_out = _like(k)
         outs = (_dense(dq_out, q.shape), _dense(dk_out, k.shape))
-        dws = (dw.data_ptr(), dw.data_ptr() + 4 * d)
+        dkw = torch.empty_like(dqw)
+        dws = (dqw.data_ptr(), dkw.data_ptr())
     packed, _ = _qk_pack(q, k, (dq, dk), outs, dws, q_weight, k_weight, q_table, k_table,
                          q_positions, k_positions, eps, interleaved)
     L = lib()
