@@ -52,7 +52,7 @@ __device__ __forceinline__ float ds_scale(const AttnArgs& a, int64_t bh, int lan
     return range_scale(2.0f * sqrtf(g) * sqrtf(v));
 }
 
-// Delta and lse of the packed rows [bh][rows_pad], and for fp16 the squared
+// -Delta and lse of the packed rows [bh][rows_pad], and for fp16 the squared
 // maxima of do and v of this workgroup's share of a head.  16 lanes a row.
 template <int DT>
 __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnArgs a) {
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnArgs a) {
                 if (l == -__builtin_inff()) l = __builtin_inff();
             }
             lse2[r] = l;
-            delta[r] = live && l != __builtin_inff() ? s : 0.0f;
+            delta[r] = live && l != __builtin_inff() ? -s : 0.0f;
         }
     }
     if constexpr (DT == DT_FP16) {
@@ -226,7 +226,6 @@ __global__ __launch_bounds__(NWK * RG * 64, OCC) void attn_bwd_kv_kernel(AttnArg
     const float f = ds_scale<DT>(a, bh, lane);
     constexpr float PS = DT == DT_FP16 ? 14.0f : 0.0f;   // p carries 2^PS
     const float fp = DT == DT_FP16 ? f * 0.00006103515625f : f;
-    const float none = valid ? 0.0f : -__builtin_inff();
 
     const uint8_t* qbase = a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h;
     const uint8_t* gbase = a.dout + (int64_t)b * a.do_b + (int64_t)hk * a.G * a.do_h;
@@ -263,42 +262,29 @@ __global__ __launch_bounds__(NWK * RG * 64, OCC) void attn_bwd_kv_kernel(AttnArg
 #pragma unroll
             for (int rx = 0; rx < QT / 32 / RG; ++rx) {
                 const int rb = rx * RG + rg;
+                // columns (keys) do not mix: those of keys that are not valid
+                // sum anything and are left out at the end
                 f32x16 s, dp;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    s[i] = none;
-                    dp[i] = 0.0f;
-                }
+                for (int i = 0; i < 16; ++i) s[i] = 0.0f;
 #pragma unroll
                 for (int x = 0; x < KS; ++x) {
                     const i32x4 qf = frag_row<DP>(ql, 32 * rb + (lane & 31), 2 * x + half);
                     const i32x4 kx = KV_LDS ? frag_row<DP>(kl, lane & 31, 2 * x + half) : kf[x];
                     s = mfma32<DT>(&qf, &kx, s);
                 }
-#pragma unroll
-                for (int x = 0; x < KS; ++x) {
-                    const i32x4 gf = frag_row<DP>(gl, 32 * rb + (lane & 31), 2 * x + half);
-                    const i32x4 vx = KV_LDS ? frag_row<DP>(vl, lane & 31, 2 * x + half) : vf[x];
-                    dp = mfma32<DT>(&gf, &vx, dp);
-                }
                 float p[16], ds[16];
+                i32x4 pf[2], df[2];
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const f32x4 L =
                         *reinterpret_cast<const f32x4*>(ls + 32 * rb + 8 * g + 4 * half);
-                    const f32x4 De =
-                        *reinterpret_cast<const f32x4*>(ls + QT + 32 * rb + 8 * g + 4 * half);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int e = 4 * g + i;
-                        p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], a.c, PS - L[i]));
-                        ds[e] = p[e] * (dp[e] - De[i]);
-                        if constexpr (DT == DT_FP16) ds[e] *= fp;
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        p[4 * g + i] = __builtin_amdgcn_exp2f(
+                            __builtin_fmaf(s[4 * g + i], a.c, PS - L[i]));
                 }
-                i32x4 pf[2], df[2];
                 pack_frag<DT>(p, pf);
-                pack_frag<DT>(ds, df);
 #pragma unroll
                 for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -306,6 +292,26 @@ __global__ __launch_bounds__(NWK * RG * 64, OCC) void attn_bwd_kv_kernel(AttnArg
                         const i32x4 gt = frag_col<DP>(gl, 32 * rb + 16 * g, d, lane);
                         dv[d] = mfma32<DT>(&gt, &pf[g], dv[d]);
                     }
+                // dp starts from -Delta
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const f32x4 De =
+                        *reinterpret_cast<const f32x4*>(ls + QT + 32 * rb + 8 * g + 4 * half);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dp[4 * g + i] = De[i];
+                }
+#pragma unroll
+                for (int x = 0; x < KS; ++x) {
+                    const i32x4 gf = frag_row<DP>(gl, 32 * rb + (lane & 31), 2 * x + half);
+                    const i32x4 vx = KV_LDS ? frag_row<DP>(vl, lane & 31, 2 * x + half) : vf[x];
+                    dp = mfma32<DT>(&gf, &vx, dp);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    ds[e] = p[e] * dp[e];
+                    if constexpr (DT == DT_FP16) ds[e] *= fp;
+                }
+                pack_frag<DT>(ds, df);
 #pragma unroll
                 for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -473,7 +479,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_bwd_q_kernel(AttnArgs a) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], a.c, -L));
-                        ds[i] = p * (dp[i] - De) * f;
+                        ds[i] = p * (dp[i] + De) * f;
                     }
                     if (word != ~0ull) {
 #pragma unroll

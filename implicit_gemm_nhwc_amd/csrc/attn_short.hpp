@@ -232,7 +232,7 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_short_rows_kern
         }
         const unsigned soff = half == 0 ? (unsigned)lane * 4 : kOut;
         store4(attn_rsrc(lse2 + blk * 32), soff, L);
-        store4(attn_rsrc(delta + blk * 32), soff, L != __builtin_inff() ? De : 0.0f);
+        store4(attn_rsrc(delta + blk * 32), soff, L != __builtin_inff() ? -De : 0.0f);
         if (a.dq) {
             f32x16 dq[DB];
 #pragma unroll
