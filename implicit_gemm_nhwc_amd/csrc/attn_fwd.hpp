@@ -1,7 +1,7 @@
 // Cross attention, forward.
 //
 // Rows are the Tq * G queries that share one key head (G query heads a key
-// head), so grouped heads read their keys once.  Each wave keeps QB blocks of
+// head), so grouped heads read their keys once.  Each wave keeps a block of
 // 32 rows: scores come as S^T = K Q^T (keys down the registers, one row a
 // lane), which makes the softmax statistics of a row a sum over one lane's
 // registers plus one exchange between the wave's halves, and lets P^T go into
@@ -104,19 +104,17 @@ __device__ __forceinline__ void fwd_finish(const AttnArgs& a, int b, int hk, int
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: NW waves of QB blocks of 32 rows walk the keys in tiles of 64,
-// double buffered in LDS through direct loads, one barrier a tile.
+// Many rows: NW waves of 32 rows walk the keys in tiles of 64, double buffered
+// in LDS through direct loads, one barrier a tile.
 // Waves a SIMD that the registers of the kernel below are cut to (and its LDS
 // allows): one register more than 512 / waves costs a wave.
-constexpr int fwd_waves(int dp, int qb) {
-    return qb > 1 ? 1 : dp <= 64 ? 4 : dp <= 96 ? 3 : 2;
-}
+constexpr int fwd_waves(int dp) { return dp <= 64 ? 4 : dp <= 96 ? 3 : 2; }
 
 // MASK: a key mask is given, so that any tile may have keys that are not
 // valid; their score products then start from -inf (LDS), which costs eight
 // LDS reads a tile instead of three instructions a score.
-template <int DT, int DP, int QB, int NW, bool MASK>
-__global__ __launch_bounds__(NW * 64, fwd_waves(DP, QB)) void attn_fwd_kernel(AttnArgs a) {
+template <int DT, int DP, int NW, bool MASK>
+__global__ __launch_bounds__(NW * 64, fwd_waves(DP)) void attn_fwd_kernel(AttnArgs a) {
     constexpr int KT = 64, KB = 2, DB = DP / 32, KS = DP / 16;
     constexpr int TILE = KT * DP * 2;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -135,23 +133,17 @@ __global__ __launch_bounds__(NW * 64, fwd_waves(DP, QB)) void attn_fwd_kernel(At
     const int len = a.lens ? max(0, min(a.lens[b], a.Tk)) : a.Tk;
     const int j_begin = sp * a.split, j_end = min(len, j_begin + a.split);
 
-    i32x4 qf[QB][KS];
-    f32x16 acc[QB][DB];
-    float m[QB], l[QB];
-    const int row0 = (rt * NW + wave) * (32 * QB), t0 = div_g(a, row0);
+    i32x4 qf[KS];
+    f32x16 acc[DB];
+    float m = -__builtin_inff(), l = 0.0f;
+    const int row0 = (rt * NW + wave) * 32, t0 = div_g(a, row0);
     const __amdgpu_buffer_rsrc_t qrs = attn_rsrc(
         a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h + (int64_t)t0 * a.q_t);
+    load_rows<DP>(qrs, packed_off(a, row0 + (lane & 31), t0, a.q_t, a.q_h), a.D, half, qf);
 #pragma unroll
-    for (int r = 0; r < QB; ++r) {
-        load_rows<DP>(qrs, packed_off(a, row0 + 32 * r + (lane & 31), t0, a.q_t, a.q_h), a.D, half,
-                      qf[r]);
-        m[r] = -__builtin_inff();
-        l[r] = 0.0f;
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[r][d][i] = 0.0f;
-    }
+        for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
 
     const uint8_t* kbase = a.k + (int64_t)b * a.k_b + (int64_t)hk * a.k_h;
     const uint8_t* vbase = a.v + (int64_t)b * a.v_b + (int64_t)hk * a.v_h;
@@ -182,40 +174,32 @@ __global__ __launch_bounds__(NW * 64, fwd_waves(DP, QB)) void attn_fwd_kernel(At
                     bias[(buf ^ 1) * KT + lane] = (next >> lane) & 1 ? 0.0f : -__builtin_inff();
             }
             if (word != 0) {
-                f32x16 s[QB][KB];
+                f32x16 s[KB];
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
-                    for (int r = 0; r < QB; ++r)
+                    for (int g = 0; g < 4; ++g) {
+                        f32x4 x = {0, 0, 0, 0};
+                        if constexpr (MASK)
+                            x = *reinterpret_cast<const f32x4*>(bias + buf * KT + 32 * kb + 8 * g +
+                                                                4 * half);
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            f32x4 x = {0, 0, 0, 0};
-                            if constexpr (MASK)
-                                x = *reinterpret_cast<const f32x4*>(bias + buf * KT + 32 * kb +
-                                                                    8 * g + 4 * half);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) s[r][kb][4 * g + i] = x[i];
-                        }
+                        for (int i = 0; i < 4; ++i) s[kb][4 * g + i] = x[i];
+                    }
 #pragma unroll
                     for (int x = 0; x < KS; ++x) {
                         const i32x4 kf = frag_row<DP>(kl, 32 * kb + (lane & 31), 2 * x + half);
-#pragma unroll
-                        for (int r = 0; r < QB; ++r)
-                            s[r][kb] = mfma32<DT>(&kf, &qf[r][x], s[r][kb]);
+                        s[kb] = mfma32<DT>(&kf, &qf[x], s[kb]);
                     }
                 }
-                i32x4 pf[QB][KB][2];
+                softmax_step<DT, KB, DB>(s, word, MASK || word == ~0ull, a.c, m, l, acc, half);
+                i32x4 pf[KB][2];
 #pragma unroll
-                for (int r = 0; r < QB; ++r) {
-                    softmax_step<DT, KB, DB>(s[r], word, MASK || word == ~0ull, a.c, m[r], l[r],
-                                             acc[r], half);
+                for (int kb = 0; kb < KB; ++kb) {
+                    float p[16];
 #pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        float p[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) p[i] = s[r][kb][i];
-                        pack_frag<DT>(p, pf[r][kb]);
-                    }
+                    for (int i = 0; i < 16; ++i) p[i] = s[kb][i];
+                    pack_frag<DT>(p, pf[kb]);
                 }
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
@@ -224,18 +208,14 @@ __global__ __launch_bounds__(NW * 64, fwd_waves(DP, QB)) void attn_fwd_kernel(At
 #pragma unroll
                         for (int d = 0; d < DB; ++d) {
                             const i32x4 vf = frag_col<DP>(vl, 32 * kb + 16 * g, d, lane);
-#pragma unroll
-                            for (int r = 0; r < QB; ++r)
-                                acc[r][d] = mfma32<DT>(&vf, &pf[r][kb][g], acc[r][d]);
+                            acc[d] = mfma32<DT>(&vf, &pf[kb][g], acc[d]);
                         }
             }
             word = next;
             buf ^= 1;
         }
     }
-#pragma unroll
-    for (int r = 0; r < QB; ++r)
-        fwd_finish<DT, DB>(a, b, hk, sp, row0 + 32 * r, lane, acc[r], m[r], l[r]);
+    fwd_finish<DT, DB>(a, b, hk, sp, row0, lane, acc, m, l);
 }
 
 // ---------------------------------------------------------------------------

@@ -12,7 +12,6 @@ namespace igc {
 struct AttnPlan {
     bool token;       // at most 32 rows a key head: attn_token_kernel
     bool few_keys;    // at most kShortKeys keys: attn_short_fwd_kernel
-    int qb;           // 32-row blocks a wave
     int row_tiles, nsplit, split;
     int64_t part_floats, stat_floats;   // workspace of split launches
 };
@@ -30,7 +29,7 @@ struct AttnGradPlan {
 
 constexpr int kAttnWaves = 4;     // waves a workgroup
 constexpr int kShortKeys = 128;   // keys that the few-keys kernels hold in LDS
-constexpr int kRowTile = 128;     // largest row tile of the dk dv kernel; padding of row statistics
+constexpr int kRowTile = 64;      // rows a tile of the dk dv kernel; padding of row statistics
 constexpr int kKeyTile = 64;      // keys a tile of the forward kernel
 constexpr int kTokenStep = 128;   // keys a round of the single-token kernel's waves
 

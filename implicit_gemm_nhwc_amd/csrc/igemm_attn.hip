@@ -117,7 +117,6 @@ AttnPlan fwd_plan(const igc_cross_attn* p) {
     const int64_t bh = p->batch * p->kv_heads;
     const int64_t rows = p->kv_heads ? p->q_len * (p->q_heads / p->kv_heads) : 0;
     x.token = rows <= 32;
-    x.qb = 1;
     x.nsplit = 1;
     x.split = kLim31 - 1;
     x.few_keys = !x.token && p->kv_len <= kShortKeys;
@@ -131,7 +130,7 @@ AttnPlan fwd_plan(const igc_cross_attn* p) {
         groups = bh;
         step = kTokenStep;
     } else {
-        x.row_tiles = (int)ceil_div(rows, kAttnWaves * 32 * x.qb);
+        x.row_tiles = (int)ceil_div(rows, kAttnWaves * 32);
         groups = bh * x.row_tiles;
         step = kKeyTile;
     }

@@ -10,9 +10,9 @@
 namespace igc {
 namespace {
 
-template <int DT, int DP, int QB, bool MASK>
+template <int DT, int DP, bool MASK>
 hipError_t launch_rows(const AttnArgs& a, hipStream_t stream) {
-    auto kern = attn_fwd_kernel<DT, DP, QB, kAttnWaves, MASK>;
+    auto kern = attn_fwd_kernel<DT, DP, kAttnWaves, MASK>;
     constexpr size_t lds = 4 * (size_t)kKeyTile * DP * 2 + 2 * kKeyTile * 4;
     static LdsAttr attr;
     const hipError_t e = ensure_lds(attr, (const void*)kern, lds);
@@ -51,13 +51,8 @@ hipError_t launch_dp(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
     hipError_t e;
     if (p.token) e = launch_token<DT, DP>(a, stream);
     else if (p.few_keys) e = launch_short<DT, DP>(a, stream);
-#ifdef FQB
-    else if (a.mask) e = launch_rows<DT, DP, FQB, true>(a, stream);
-    else e = launch_rows<DT, DP, FQB, false>(a, stream);
-#else
-    else if (a.mask) e = launch_rows<DT, DP, 1, true>(a, stream);
-    else e = launch_rows<DT, DP, 1, false>(a, stream);
-#endif
+    else if (a.mask) e = launch_rows<DT, DP, true>(a, stream);
+    else e = launch_rows<DT, DP, false>(a, stream);
     if (e != hipSuccess || a.nsplit <= 1) return e;
     const int64_t n = (int64_t)a.B * a.Hk * a.rows;
     hipLaunchKernelGGL(attn_join_kernel<DT>, dim3((unsigned)n), dim3(256), 0, stream, a);
