@@ -6,10 +6,13 @@ _build/ and linked into one shared library.  The same sources are also built
 as libigemmconv_ldspoison.so with IGC_LDS_POISON defined: a debug build whose
 kernels first fill their LDS with NaN bytes, so that a read running ahead of
 its data (a missing wait or barrier) shows up as NaN outputs in the tests.
+The attention binding's C++ part (_attn_marshal.so) is built with g++ beside
+them.
 """
 import concurrent.futures
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libigemmconv.so")
 POISON_LIB = os.path.join(PKG, "libigemmconv_ldspoison.so")
+MARSHAL = os.path.join(PKG, "_attn_marshal.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 ARCH = "gfx950"
 
@@ -46,6 +50,19 @@ HIPCC_FLAGS = [
 
 def _hipcc():
     return os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
+
+
+def _marshal_cmd():
+    """g++ line of the attention binding's C++ part (torch's headers; no GPU code)."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", INCLUDE, "-isystem", os.path.join(root, "include"), "-isystem",
+            sysconfig.get_paths()["include"], os.path.join(CSRC, "attn_marshal.cpp"),
+            "-o", MARSHAL + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def _newest_source():
@@ -79,6 +96,8 @@ def build(verbose: bool = False, jobs: int = None, incremental: bool = False,
                          os.path.join(CSRC, src), "-o", obj])
         links.append((lib, [hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o",
                             lib + ".tmp"]))
+    if not (incremental and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) > newest):
+        cmds.insert(0, _marshal_cmd())
     if jobs is None:
         jobs = max(1, min(len(cmds), os.cpu_count() or 1))
 
@@ -93,6 +112,8 @@ def build(verbose: bool = False, jobs: int = None, incremental: bool = False,
     for lib, link in links:
         run(link)
         os.replace(lib + ".tmp", lib)
+    if os.path.exists(MARSHAL + ".tmp"):
+        os.replace(MARSHAL + ".tmp", MARSHAL)
     return LIB
 
 

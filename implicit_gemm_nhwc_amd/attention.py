@@ -20,11 +20,17 @@ workspace given); cross_attention, cross_attention_bwd, qk_norm_rope and
 qk_norm_rope_bwd allocate their outputs and raise on failure; rope_table and rope_table_2d make the
 rotation's tables.
 """
+import ctypes
 import struct
 
 import torch
 
 from . import DTYPE_CODES, REASONS, Declined, InvalidArgument, lib
+
+try:   # the ordinary calls in C++ (csrc/attn_marshal.cpp); without it, all through Python
+    from . import _attn_marshal as _fast
+except ImportError:
+    _fast = None
 
 _ATTN = struct.Struct("@26qdqqq")
 _VIEWS = struct.Struct("@16q")   # dout, dq, dk, dv
@@ -32,6 +38,7 @@ _QK = struct.Struct("@42q4qdqq")   # two parts of 21 fields
 _NO_PART = (0,) * 21
 _NO_VIEW = (0, 0, 0, 0)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_gpu = torch._C._cuda_getDevice
 
 
 def _view(name, t, dtype, device):
@@ -104,7 +111,22 @@ class _on:
 
 
 def _elsewhere(device, stream):
-    return stream is not None or device != torch._C._cuda_getDevice()
+    return stream is not None or device != _current_gpu()
+
+
+def _entries():
+    """The current library's entries as attn_marshal.cpp takes them."""
+    L = lib()
+    try:
+        return L.attn_entries
+    except AttributeError:
+        pass
+    L.attn_entries = _fast.bind(*(
+        ctypes.cast(getattr(L, n), ctypes.c_void_p).value
+        for n in ("cross_attn_fwd", "cross_attn_fwd_workspace_bytes", "cross_attn_bwd",
+                  "cross_attn_bwd_workspace_bytes", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
+                  "qk_norm_rope_bwd_workspace_bytes")))
+    return L.attn_entries
 
 
 def _raise(name, rc, check, packed):
@@ -209,6 +231,11 @@ def cross_attention(q, k, v, *, scale=None, kv_lens=None, key_mask=None, return_
     return_lse also the fp32 row statistics [b, hq, tq] for
     cross_attention_bwd."""
     device = _device(q)
+    if _fast is not None and stream is None:
+        r = _fast.cross_attention(_entries(), q, k, v, scale, kv_lens, key_mask, return_lse,
+                                  _raw_stream(device), _current_gpu())
+        if r is not None:
+            return r
     if _elsewhere(device, stream):
         with _on(device, stream):
             return cross_attention(q, k, v, scale=scale, kv_lens=kv_lens, key_mask=key_mask,
@@ -284,6 +311,11 @@ def cross_attention_bwd(dout, q, k, v, out, lse, *, scale=None, kv_lens=None, ke
     dout, with its out and lse (return_lse) and the same scale, kv_lens and
     key_mask.  dk and dv sum over the query heads that share a key head."""
     device = _device(q)
+    if _fast is not None and stream is None:
+        r = _fast.cross_attention_bwd(_entries(), dout, q, k, v, out, lse, scale, kv_lens,
+                                      key_mask, _raw_stream(device), _current_gpu())
+        if r is not None:
+            return r
     if _elsewhere(device, stream):
         with _on(device, stream):
             return cross_attention_bwd(dout, q, k, v, out, lse, scale=scale, kv_lens=kv_lens,
@@ -440,6 +472,12 @@ def qk_norm_rope(q, k=None, *, q_weight=None, k_weight=None, q_table=None, k_tab
     number).  Returns the two results, dense; k may be None (then q's result
     alone)."""
     device = _device(q)
+    if _fast is not None and stream is None:
+        r = _fast.qk_norm_rope(_entries(), q, k, q_weight, k_weight, q_table, k_table,
+                               q_positions, k_positions, eps, interleaved, _raw_stream(device),
+                               _current_gpu())
+        if r is not None:
+            return r
     if _elsewhere(device, stream):
         with _on(device, stream):
             return qk_norm_rope(q, k, q_weight=q_weight, k_weight=k_weight, q_table=q_table,
@@ -470,6 +508,12 @@ def qk_norm_rope_bwd(dq, dk, q, k=None, *, q_weight=None, k_weight=None, q_table
     (fp32; also for a weight of None, which counts as ones); k may be None
     (its two gradients are then None)."""
     device = _device(q)
+    if _fast is not None and stream is None:
+        r = _fast.qk_norm_rope_bwd(_entries(), dq, dk, q, k, q_weight, k_weight, q_table, k_table,
+                                   q_positions, k_positions, eps, interleaved,
+                                   _raw_stream(device), _current_gpu())
+        if r is not None:
+            return r
     if _elsewhere(device, stream):
         with _on(device, stream):
             return qk_norm_rope_bwd(dq, dk, q, k, q_weight=q_weight, k_weight=k_weight,

@@ -220,20 +220,23 @@ __global__ __launch_bounds__(NW * 64, fwd_waves(DP)) void attn_fwd_kernel(AttnAr
 
 // ---------------------------------------------------------------------------
 // At most 32 rows (single tokens): the waves of a workgroup take blocks of 32
-// keys in turn, each through its own two LDS buffers without barriers, so the
-// key and value bytes stream with two blocks a wave in flight; the waves'
-// results are joined through LDS at the end.
+// keys in turn, each through LDS of its own without barriers.  A wave asks
+// for its next block's keys as soon as the score products have read the
+// present ones, and for the next values after the second product, so that its
+// memory requests never pause; the waves' results are joined through LDS at
+// the end.  A round of all waves is one memory latency; eight waves in half
+// the LDS each beat four with whole double buffers.
 template <int DT, int DP, int NW>
-__global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
+__global__ __launch_bounds__(NW * 64, 2) void attn_token_kernel(AttnArgs a) {
     constexpr int KT = 32, DB = DP / 32, KS = DP / 16;
     constexpr int TILE = KT * DP * 2;
     constexpr int STAGE = 2 * TILE;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-    lds_poison<NW * 64>(lds, NW * 2 * STAGE + NW * 64 * 4);
+    lds_poison<NW * 64>(lds, NW * STAGE + NW * 64 * 4);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int half = lane >> 5;
-    uint8_t* mine = lds + wave * 2 * STAGE;
-    float* st_m = reinterpret_cast<float*>(lds + NW * 2 * STAGE);   // [NW][32] m, then l
+    uint8_t* mine = lds + wave * STAGE;   // keys, values
+    float* st_m = reinterpret_cast<float*>(lds + NW * STAGE);   // [NW][32] m, then l
     float* st_l = st_m + NW * 32;
 
     int idx = launch_place(a);
@@ -260,7 +263,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
     TileStage<DP, KT, 1> ks, vs;
     ks.init(0, lane, a.D, (unsigned)a.k_t);
     vs.init(0, lane, a.D, (unsigned)a.v_t);
-    constexpr int LOADS = 2 * TileStage<DP, KT, 1>::PIECES;
+    constexpr int LOADS = TileStage<DP, KT, 1>::PIECES;   // requests a block of keys, or of values
     constexpr int STEP = NW * KT;
 
     auto word_at = [&](uint32_t mb, int j) -> uint32_t {
@@ -268,55 +271,52 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
     };
     if (j_begin < j_end) {
         uint32_t w0 = word_at(mask_byte(mrow, j_begin, j_end, lane), j_begin), w1 = 0;
+        uint32_t mb = mask_byte(mrow, j_begin + STEP, j_end, lane);
         ks.issue(kbase + (int64_t)j_begin * a.k_t, w0, mine, 0);
         vs.issue(vbase + (int64_t)j_begin * a.v_t, w0, mine + TILE, 0);
-        uint32_t mb = mask_byte(mrow, j_begin + STEP, j_end, lane);
-        int buf = 0;
         for (int j = j_begin; j < j_end; j += STEP) {
-            if (j + STEP < j_end) {
+            const bool more = j + STEP < j_end;
+            // the keys: all but the values requested after them
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+            f32x16 s[1];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[0][i] = 0.0f;
+#pragma unroll
+            for (int x = 0; x < KS; ++x) {
+                const i32x4 kf = frag_row<DP>(mine, lane & 31, 2 * x + half);
+                s[0] = mfma32<DT>(&kf, &qf[x], s[0]);
+            }
+            // their LDS is read: the next block's may arrive
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (more) {
                 w1 = word_at(mb, j + STEP);
-                uint8_t* nl = mine + (buf ^ 1) * STAGE;
-                // the reads of this buffer two blocks ago have returned: the
-                // products that used them are in program order before
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                ks.issue(kbase + (int64_t)(j + STEP) * a.k_t, w1, nl, 0);
-                vs.issue(vbase + (int64_t)(j + STEP) * a.v_t, w1, nl + TILE, 0);
                 mb = mask_byte(mrow, j + 2 * STEP, j_end, lane);
-                // all but the block just requested (the mask byte is younger)
-                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
-            } else {
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                ks.issue(kbase + (int64_t)(j + STEP) * a.k_t, w1, mine, 0);
             }
-            const uint8_t* kl = mine + buf * STAGE;
-            const uint8_t* vl = kl + TILE;
-            if (w0 != 0) {
-                f32x16 s[1];
+            softmax_step<DT, 1, DB>(s, w0, w0 == ~0u, a.c, m, l, acc, half);
+            i32x4 pf[2];
+            float p[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[0][i] = 0.0f;
+            for (int i = 0; i < 16; ++i) p[i] = s[0][i];
+            pack_frag<DT>(p, pf);
+            // the values: all but the next keys (the mask byte is older)
+            if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-                for (int x = 0; x < KS; ++x) {
-                    const i32x4 kf = frag_row<DP>(kl, lane & 31, 2 * x + half);
-                    s[0] = mfma32<DT>(&kf, &qf[x], s[0]);
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const i32x4 vf = frag_col<DP>(mine + TILE, 16 * g, d, lane);
+                    acc[d] = mfma32<DT>(&vf, &pf[g], acc[d]);
                 }
-                softmax_step<DT, 1, DB>(s, w0, w0 == ~0u, a.c, m, l, acc, half);
-                i32x4 pf[2];
-                float p[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) p[i] = s[0][i];
-                pack_frag<DT>(p, pf);
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        const i32x4 vf = frag_col<DP>(vl, 16 * g, d, lane);
-                        acc[d] = mfma32<DT>(&vf, &pf[g], acc[d]);
-                    }
-            }
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (more) vs.issue(vbase + (int64_t)(j + STEP) * a.v_t, w1, mine + TILE, 0);
             w0 = w1;
-            buf ^= 1;
         }
     }
-    // join: wave w's rows as floats [rows][DP] over its own first buffer
+    // join: wave w's rows as floats [rows][DP] over its own LDS
     l = sum_halves(l);
     float* po = reinterpret_cast<float*>(mine);
     if (row < a.rows) {
@@ -347,7 +347,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_token_kernel(AttnArgs a) {
             const float f = __builtin_amdgcn_exp2f(st_m[w * 32 + r] - ms);
             ll = __builtin_fmaf(st_l[w * 32 + r], f, ll);
             const f32x4 x = *reinterpret_cast<const f32x4*>(
-                reinterpret_cast<const float*>(lds + w * 2 * STAGE) + r * DP + d);
+                reinterpret_cast<const float*>(lds + w * STAGE) + r * DP + d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
         }

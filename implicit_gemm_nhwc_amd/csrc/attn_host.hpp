@@ -31,7 +31,8 @@ constexpr int kAttnWaves = 4;     // waves a workgroup
 constexpr int kShortKeys = 128;   // keys that the few-keys kernels hold in LDS
 constexpr int kRowTile = 64;      // rows a tile of the dk dv kernel; padding of row statistics
 constexpr int kKeyTile = 64;      // keys a tile of the forward kernel
-constexpr int kTokenStep = 128;   // keys a round of the single-token kernel's waves
+constexpr int kTokenWaves = 8;    // waves a workgroup of the single-token kernel
+constexpr int kTokenStep = 32 * kTokenWaves;   // keys a round of its waves
 
 // D rounded up to the tile widths the kernels are built for.
 inline int padded_dim(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 96 ? 96 : 128; }

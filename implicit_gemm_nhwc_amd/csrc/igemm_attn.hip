@@ -135,14 +135,21 @@ AttnPlan fwd_plan(const igc_cross_attn* p) {
         step = kKeyTile;
     }
     const int64_t steps = ceil_div(p->kv_len, step);
-    // Workgroups for two a CU.  A round of the token kernel is one memory
-    // latency (about 1.5 us) and the join of split keys another launch: at 7
-    // rounds both ways take 11.4 us (32 key heads, 784 keys of 128), below
-    // the split loses, above every round given to another workgroup gains.
-    // The tile kernel keeps four tiles a split.
-    const int64_t want = groups > 0 ? 2 * kNumCUs / groups : 1;
-    const int64_t most = !x.token ? steps / 4 : steps > 7 ? steps : 1;
-    int64_t n = want < most ? want : most;
+    int64_t n = 1;
+    if (!x.token) {
+        // two workgroups a CU, four tiles a split at least
+        n = groups > 0 ? 2 * kNumCUs / groups : 1;
+        if (n > steps / 4) n = steps / 4;
+    } else if (steps > 4) {
+        // The join is another launch: four rounds of the waves (1024 keys of
+        // 128, 32 key heads) take 10.9 us in one workgroup a head and 10.7
+        // split, two 7.8 and 10.7.  Splits fill the card once (3072 keys:
+        // 16.9 us, in twice as many 18.8); from 16 rounds a split on, four
+        // times over, so that ragged lengths even out (4 x 30000 .. 65537
+        // keys: 145 us, filled once 170, equal lengths 194 and 197).
+        n = groups > 0 ? kNumCUs / groups : 1;
+        if (ceil_div(steps, n < 1 ? 1 : n) > 16) n = groups > 0 ? 4 * kNumCUs / groups : 1;
+    }
     if (n < 1) n = 1;
     const int64_t per = ceil_div(steps > 0 ? steps : 1, n);
     x.nsplit = (int)ceil_div(steps > 0 ? steps : 1, per);

@@ -36,13 +36,13 @@ hipError_t launch_short(const AttnArgs& a, hipStream_t stream) {
 
 template <int DT, int DP>
 hipError_t launch_token(const AttnArgs& a, hipStream_t stream) {
-    auto kern = attn_token_kernel<DT, DP, kAttnWaves>;
-    constexpr size_t lds = (size_t)kAttnWaves * 2 * 2 * 32 * DP * 2 + kAttnWaves * 64 * 4;
+    auto kern = attn_token_kernel<DT, DP, kTokenWaves>;
+    constexpr size_t lds = (size_t)kTokenWaves * (2 * 32 * DP * 2 + 64 * 4);
     static LdsAttr attr;
     const hipError_t e = ensure_lds(attr, (const void*)kern, lds);
     if (e != hipSuccess) return e;
     const unsigned grid = (unsigned)((int64_t)a.B * a.Hk * a.nsplit);
-    hipLaunchKernelGGL(kern, dim3(grid), dim3(kAttnWaves * 64), lds, stream, a);
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(kTokenWaves * 64), lds, stream, a);
     return hipGetLastError();
 }
 

@@ -86,6 +86,55 @@ def test_decoder_reads_as_the_block_does():
     assert _rel(got, y) < 2.0 ** -7
 
 
+def test_both_ways_through_the_binding(monkeypatch):
+    """The calls that go through the binding's C++ part give the same bits
+    and the same refusals through Python alone."""
+    from implicit_gemm_nhwc_amd import attention as binding
+    assert binding._fast is not None
+    q, kv = _rnd(2, 40, 8, 64, seed=6), _rnd(2, 70, 2, 4, 64, seed=7)
+    k, v = kv[:, :, 0], kv[:, :, 1]
+    go = _rnd(2, 40, 8, 64, seed=8)
+    lens = torch.tensor([70, 9], dtype=torch.int32, device=DEV)
+    mask = torch.rand(2, 70, device=DEV) < 0.8
+    table = igc.rope_table(80, 32, device=DEV)
+    at = torch.randint(0, 80, (2, 40), device=DEV).to(torch.int32)
+    w = torch.rand(64, device=DEV)
+
+    def calls():
+        kw = dict(kv_lens=lens, key_mask=mask, scale=0.2)
+        out, lse = igc.cross_attention(q, k, v, return_lse=True, **kw)
+        norm = dict(q_weight=w, q_table=table, k_table=table, q_positions=at, eps=1e-5,
+                    interleaved=True)
+        alone = {n: x for n, x in norm.items() if n != "k_table"}
+        return [out, lse, igc.cross_attention(q, k, v),
+                *igc.cross_attention_bwd(go, q, k, v, out, lse, **kw),
+                *igc.qk_norm_rope(q, k, **norm), igc.qk_norm_rope(q, **alone),
+                *igc.qk_norm_rope_bwd(go, k, q, k, **norm),
+                *igc.qk_norm_rope_bwd(go, None, q, **alone)]
+
+    def refusals():
+        seen = []
+        for bad in (lambda: igc.cross_attention(q, k[:1], v), lambda: igc.cross_attention(q, k, go),
+                    lambda: igc.cross_attention(q, k, v, scale=-1.0),
+                    lambda: igc.cross_attention(q.float(), k, v),
+                    lambda: igc.cross_attention(q, k, v, kv_lens=lens.long()),
+                    lambda: igc.qk_norm_rope(q, k, q_table=table),
+                    lambda: igc.qk_norm_rope(q, eps=-1.0),
+                    lambda: igc.qk_norm_rope_bwd(go[:1], None, q)):
+            with pytest.raises((igc.InvalidArgument, igc.Declined)) as e:
+                bad()
+            seen.append((e.type, str(e.value)))
+        return seen
+
+    fast, said = calls(), refusals()
+    monkeypatch.setattr(binding, "_fast", None)
+    slow = calls()
+    assert said == refusals()
+    for a, b in zip(fast, slow):
+        assert (a is None and b is None) or (a.shape == b.shape and torch.equal(a, b))
+        assert a is None or (a.stride() == b.stride() and a.dtype == b.dtype)
+
+
 def test_example_runs(capsys):
     import cross_attention_block
     cross_attention_block.main()
