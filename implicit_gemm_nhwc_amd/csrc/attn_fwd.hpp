@@ -375,27 +375,31 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_token_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Join of split launches.  A workgroup takes one packed row: groups of
-// kJoinLanes lanes (4 values a lane) sum every 8th split, and the 8 sums are
-// added in order through LDS.
-constexpr int kJoinLanes = 32;
-template <int DT>
+// Join of split launches.  32 lanes take a packed row, 4 values a lane.  Few
+// rows of many splits: a workgroup a row, its GR = 8 groups of lanes sum
+// every 8th split, and the 8 sums are added in order through LDS.  Few splits
+// (GR = 1): 8 rows a workgroup, each group sums its row's splits in order
+// (2 splits of 19800 rows: 20.6 us with a workgroup a row).
+constexpr int kJoinLanes = 32, kJoinFew = 8;
+template <int DT, int GR>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-    __shared__ f32x4 part[8][kJoinLanes];
-    __shared__ float sum[8];
+    __shared__ f32x4 part[GR][kJoinLanes];
+    __shared__ float sum[GR];
     const int64_t n = (int64_t)a.B * a.Hk * a.rows;
-    const int64_t at = blockIdx.x;
-    const int g = threadIdx.x / kJoinLanes, d = (threadIdx.x % kJoinLanes) * 4;
+    const int lane = threadIdx.x % kJoinLanes, group = threadIdx.x / kJoinLanes;
+    const int64_t at = GR > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + group;
+    const int g = GR > 1 ? group : 0, d = lane * 4;
+    if (at >= n) return;   // GR = 1 only, which has no barrier below
     // the maximum over the splits, by every group of 32 lanes
     float mm = -__builtin_inff();
-    for (int s = threadIdx.x % kJoinLanes; s < a.nsplit; s += kJoinLanes)
+    for (int s = lane; s < a.nsplit; s += kJoinLanes)
         mm = fmaxf(mm, a.stat[(s * n + at) * 2]);
 #pragma unroll
     for (int o = 1; o < kJoinLanes; o <<= 1) mm = fmaxf(mm, __shfl_xor(mm, o, 64));
     const float ms = mm == -__builtin_inff() ? 0.0f : mm;
     float ll = 0.0f;
     f32x4 o = {0, 0, 0, 0};
-    for (int s = g; s < a.nsplit; s += 8) {
+    for (int s = g; s < a.nsplit; s += GR) {
         const float f = __builtin_amdgcn_exp2f(a.stat[(s * n + at) * 2] - ms);
         ll = __builtin_fmaf(a.stat[(s * n + at) * 2 + 1], f, ll);
         if (d < a.D) {
@@ -404,15 +408,18 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
             for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
         }
     }
-    part[g][threadIdx.x % kJoinLanes] = o;
-    if (d == 0) sum[g] = ll;
-    __syncthreads();
-    if (g != 0 || d >= a.D) return;
-    ll = sum[0];
-    for (int i = 1; i < 8; ++i) {
-        ll += sum[i];
-        o += part[i][threadIdx.x];
+    if constexpr (GR > 1) {
+        part[g][lane] = o;
+        if (d == 0) sum[g] = ll;
+        __syncthreads();
+        if (g != 0) return;
+        ll = sum[0];
+        for (int i = 1; i < GR; ++i) {
+            ll += sum[i];
+            o += part[i][lane];
+        }
     }
+    if (d >= a.D) return;
     const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
     const int64_t bh = at / a.rows;
     const int r = (int)(at - bh * a.rows);

@@ -275,12 +275,11 @@ AttnGradPlan bwd_plan(const igc_cross_attn* p) {
     if (n > x.rows_pad / 16) n = x.rows_pad / 16;
     if (n > 256) n = 256;
     x.bound_n = (int)(n < 1 ? 1 : n);
-    // splits for one workgroup a CU (dk dv: eight waves) or two (dq: four),
-    // of four tiles at least
-    auto split = [](int64_t want, int64_t groups, int64_t tiles, int64_t unit, int* nsplit,
-                    int* len) {
+    // splits of `least` tiles at least, for `want` workgroups
+    auto split = [](int64_t want, int64_t least, int64_t groups, int64_t tiles, int64_t unit,
+                    int* nsplit, int* len) {
         int64_t n = groups > 0 ? want / groups : 1;
-        if (n > tiles / 4) n = tiles / 4;
+        if (n > tiles / least) n = tiles / least;
         if (n < 1) n = 1;
         const int64_t per = ceil_div(tiles > 0 ? tiles : 1, n);
         *nsplit = (int)ceil_div(tiles > 0 ? tiles : 1, per);
@@ -289,9 +288,11 @@ AttnGradPlan bwd_plan(const igc_cross_attn* p) {
     const int64_t key32 = ceil_div(p->kv_len, 32);
     x.kv_waves = (int)(key32 < 1 ? 1 : key32 < kAttnWaves ? key32 : kAttnWaves);
     x.key_tiles = (int)ceil_div(key32, x.kv_waves);
-    split(kNumCUs, bh * x.key_tiles, row64, kRowTile, &x.kv_nsplit, &x.kv_split);
+    // dk dv: one workgroup a CU (eight waves of many registers)
+    split(kNumCUs, 2, bh * x.key_tiles, row64, kRowTile, &x.kv_nsplit, &x.kv_split);
     x.row_tiles = (int)ceil_div(rows, kAttnWaves * 32);
-    split(2 * kNumCUs, bh * x.row_tiles, key64, kKeyTile, &x.q_nsplit, &x.q_split);
+    // dq: two a CU (four waves)
+    split(2 * kNumCUs, 4, bh * x.row_tiles, key64, kKeyTile, &x.q_nsplit, &x.q_split);
     x.few_keys = p->kv_len <= kShortKeys;
     if (x.few_keys) {
         x.row_tiles = (int)short_tiles(bh, x.rows_pad, (p->head_dim <= 64 ? 2 : 1) * kNumCUs);

@@ -55,7 +55,11 @@ hipError_t launch_dp(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
     else e = launch_rows<DT, DP, false>(a, stream);
     if (e != hipSuccess || a.nsplit <= 1) return e;
     const int64_t n = (int64_t)a.B * a.Hk * a.rows;
-    hipLaunchKernelGGL(attn_join_kernel<DT>, dim3((unsigned)n), dim3(256), 0, stream, a);
+    if (a.nsplit <= kJoinFew)
+        hipLaunchKernelGGL((attn_join_kernel<DT, 1>), dim3((unsigned)((n + 7) / 8)), dim3(256), 0,
+                           stream, a);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<DT, 8>), dim3((unsigned)n), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
