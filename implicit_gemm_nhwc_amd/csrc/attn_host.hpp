@@ -21,7 +21,8 @@ struct AttnGradPlan {
     bool few_keys;        // at most kShortKeys keys: attn_short_rows_kernel instead of
                           // the row pass and the dq kernel
     int rows_pad, bound_n;
-    int kv_waves;         // dk dv: waves a workgroup, 32 keys each
+    int kv_waves;         // dk dv: key blocks (32 keys) a workgroup,
+    int kv_groups;        // and waves a block, which take alternate row blocks
     int key_tiles, kv_nsplit, kv_split;   // dk dv: key tiles, splits of the rows
     int row_tiles, q_nsplit, q_split;     // dq: row tiles, splits of the keys
     int64_t stat_floats, bound_words, part_floats;   // workspace

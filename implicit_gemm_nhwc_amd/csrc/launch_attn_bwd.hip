@@ -32,14 +32,18 @@ hipError_t launch_kv(AttnArgs a, const AttnGradPlan& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Two row groups a workgroup and two waves a SIMD.  Up to 64 values a head
-// the keys' operands stay in registers (32 x 77 keys of 64, 784 rows: 21.5 us,
-// from LDS 24.2); wider heads do not fit two waves that way and read them
-// from LDS (2 x 2048 keys of 128, 8192 rows: 275 us; in registers with one
-// wave a SIMD 375, spilling 467).
+// Two waves a SIMD.  Up to 96 values a head the keys' operands stay in
+// registers (32 x 77 keys of 64, 784 rows: 21.5 us, from LDS 24.2); 128 do not
+// fit two waves that way and are read from LDS (2 x 2048 keys, 8192 rows:
+// 275 us; in registers with one wave a SIMD 375, spilling 467).
 template <int DT, int DP, int NWK>
 hipError_t launch_kv_dp(const AttnArgs& a, const AttnGradPlan& p, hipStream_t stream) {
-    return launch_kv<DT, DP, NWK, 2, kRowTile, (DP > 64), 2>(a, p, stream);
+    if constexpr (DP <= 96) {
+        if (p.kv_groups == 1) return launch_kv<DT, DP, NWK, 1, kRowTile, false, 2>(a, p, stream);
+        return launch_kv<DT, DP, NWK, 2, kRowTile, false, 2>(a, p, stream);
+    } else {
+        return launch_kv<DT, DP, NWK, 2, kRowTile, true, 2>(a, p, stream);
+    }
 }
 
 template <int DT, int DP>
