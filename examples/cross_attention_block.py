@@ -65,7 +65,8 @@ class CrossAttentionBlock:
     def norm_args(self, x, states):
         n, h, w, _ = x.shape
         return dict(q_weight=self.q_weight, k_weight=self.k_weight,
-                    q_table=self._table("map", h, w), k_table=self._table("states", states.shape[1]))
+                    q_table=self._table("map", h, w),
+                    k_table=self._table("states", states.shape[1]))
 
     def forward(self, x, states, kv_lens=None, key_mask=None):
         q, k, v = self.project(x, states)

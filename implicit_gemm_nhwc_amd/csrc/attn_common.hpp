@@ -31,8 +31,10 @@ struct AttnArgs {
     const int32_t* lens;
     const uint8_t* mask;
     float* part;           // partial results of split launches
-    float* stat;           // their (m, l); backward: [2][B][Hk][rows_pad] lse in powers of two, -Delta
-    uint32_t* bound;       // backward, fp16: [B][Hk][bound_n] squared maxima of do and v, float bits
+    float* stat;           // their (m, l); backward: [2][B][Hk][rows_pad], lse in powers of two
+                           // and -Delta
+    uint32_t* bound;       // backward, fp16: [B][Hk][bound_n] squared maxima of do and v, as
+                           // float bits
     // strides in bytes
     int64_t q_b, q_t, q_h, k_b, k_t, k_h, v_b, v_t, v_h, o_b, o_t, o_h;
     int64_t do_b, do_t, do_h, dq_b, dq_t, dq_h, dk_b, dk_t, dk_h, dv_b, dv_t, dv_h;

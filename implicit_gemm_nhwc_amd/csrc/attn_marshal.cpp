@@ -326,7 +326,8 @@ PyObject* bind(PyObject*, PyObject* const* o, Py_ssize_t n) {
 
 #define FAST(f) {#f, (PyCFunction)(void*)f, METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {FAST(bind),         FAST(cross_attention),  FAST(cross_attention_bwd),
-                          FAST(qk_norm_rope), FAST(qk_norm_rope_bwd), {nullptr, nullptr, 0, nullptr}};
+                          FAST(qk_norm_rope), FAST(qk_norm_rope_bwd),
+                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_attn_marshal", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 

@@ -214,7 +214,8 @@ __global__ __launch_bounds__(NW * 64, DP > 64 ? 1 : 2) void attn_short_rows_kern
                     s[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], a.c, -L));
                 float t[2] = {0, 0};
 #pragma unroll
-                for (int i = 0; i < 16; ++i) t[i & 1] = __builtin_fmaf(s[kb][i], dp[kb][i], t[i & 1]);
+                for (int i = 0; i < 16; ++i)
+                    t[i & 1] = __builtin_fmaf(s[kb][i], dp[kb][i], t[i & 1]);
                 De += t[0] + t[1];
             }
         De = sum_halves(De);

@@ -137,16 +137,19 @@ AttnPlan fwd_plan(const igc_cross_attn* p) {
     const int64_t steps = ceil_div(p->kv_len, step);
     int64_t n = 1;
     if (!x.token) {
-        // two workgroups a CU, four tiles a split at least
+        // two workgroups a CU, three tiles a split at least (four: a training
+        // call of 46.4 us, masked fp16, takes 43.6 with three; one workgroup or
+        // four a CU are slower on the other middle-sized calls)
         n = groups > 0 ? 2 * kNumCUs / groups : 1;
-        if (n > steps / 4) n = steps / 4;
+        if (n > steps / 3) n = steps / 3;
     } else if (steps > 4) {
         // The join is another launch: four rounds of the waves (1024 keys of
         // 128, 32 key heads) take 10.9 us in one workgroup a head and 10.7
-        // split, two 7.8 and 10.7.  Splits fill the card once (3072 keys:
-        // 16.9 us, in twice as many 18.8); from 16 rounds a split on, four
-        // times over, so that ragged lengths even out (4 x 30000 .. 65537
-        // keys: 145 us, filled once 170, equal lengths 194 and 197).
+        // split, two 7.8 and 10.7.  Splits fill the card once (2048 keys of
+        // 64, 64 key heads: 13.2 us, in twice as many 14.8); from 16 rounds a
+        // split on, four times over, so that ragged lengths even out (4 x
+        // 30000 .. 65537 keys: 145 us, filled once 170, equal lengths 194 and
+        // 197).
         n = groups > 0 ? kNumCUs / groups : 1;
         if (ceil_div(steps, n < 1 ? 1 : n) > 16) n = groups > 0 ? 4 * kNumCUs / groups : 1;
     }
@@ -294,11 +297,11 @@ AttnGradPlan bwd_plan(const igc_cross_attn* p) {
     // and then leave room for one workgroup a CU instead of two: up to eight
     // row tiles one wave is as fast or faster (3 tiles of 3882 keys of 64:
     // 21 us, two waves 30; 8 tiles 16 both; 13 tiles of 77 keys 24 and 21).
-    x.kv_groups = p->head_dim <= 96 && ceil_div(x.kv_split < rows ? x.kv_split : rows, kRowTile) <= 8
-                      ? 1 : 2;
+    const int64_t walk = ceil_div(x.kv_split < rows ? x.kv_split : rows, kRowTile);
+    x.kv_groups = p->head_dim <= 96 && walk <= 8 ? 1 : 2;
     x.row_tiles = (int)ceil_div(rows, kAttnWaves * 32);
     // dq: two a CU (four waves)
-    split(2 * kNumCUs, 4, bh * x.row_tiles, key64, kKeyTile, &x.q_nsplit, &x.q_split);
+    split(2 * kNumCUs, 3, bh * x.row_tiles, key64, kKeyTile, &x.q_nsplit, &x.q_split);
     x.few_keys = p->kv_len <= kShortKeys;
     if (x.few_keys) {
         x.row_tiles = (int)short_tiles(bh, x.rows_pad, (p->head_dim <= 64 ? 2 : 1) * kNumCUs);

@@ -183,7 +183,8 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_fwd_kernel(QkArgs a) {
     const uint8_t* x = p.x + b * p.x_b + t * p.x_t + h0 * p.x_h + c * 16;
 #pragma unroll
     for (int i = 0; i < kQkHeads; ++i)
-        raw[i] = mine && i < nh ? *reinterpret_cast<const u32x4*>(x + i * p.x_h) : u32x4{0, 0, 0, 0};
+        raw[i] = mine && i < nh ? *reinterpret_cast<const u32x4*>(x + i * p.x_h)
+                                : u32x4{0, 0, 0, 0};
     Turn<MODE> turn;
     qk_turn(p, a.R, b, t, c, &turn);
     float w[8];
