@@ -20,7 +20,7 @@ constexpr int64_t kLim31 = (int64_t)1 << 31;
 constexpr int64_t kStrideLim = (int64_t)1 << 23;        // token and head strides, elements
 constexpr int64_t kBatchStrideLim = (int64_t)1 << 40;   // batch strides, elements
 constexpr int64_t kMaxGrid = kLim31 - 1;
-constexpr int64_t kQkBwdBlocks = 1024;                  // four workgroups a CU
+constexpr int64_t kQkBwdBlocks = 3 * kNumCUs;           // three a CU: what the registers hold
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
@@ -399,19 +399,33 @@ bool same_view(const Tensor& a, const Tensor& b) {
     return a.p == b.p && a.b == b.b && a.t == b.t && a.h == b.h;
 }
 
-// Workgroups of one part.
-int64_t qk_blocks(const igc_qk_part& x, int64_t d, bool backward) {
+// Rounds of 256 threads that one part needs.
+int64_t qk_tiles(const igc_qk_part& x, int64_t d) {
     if (qk_empty(x)) return 0;
     const int64_t items = x.batch * x.tokens * ceil_div(x.heads, kQkHeads);
-    const int64_t n = ceil_div(items, kQkThreads / qk_lanes((int)d));
-    // backward: the workgroups loop, so that the partial weight gradients
-    // stay few
-    return backward && n > kQkBwdBlocks ? kQkBwdBlocks : n;
+    return ceil_div(items, kQkThreads / qk_lanes((int)d));
+}
+
+// Workgroups of one part.  Backward they loop, so that the partial weight
+// gradients stay few: as many as run at once, both parts together (one more
+// would run alone at the end: 16 x 4096 queries and 1024 keys of 128, 242 us
+// with 769 workgroups), with the same number of rounds each (32 x 3136 queries
+// and 333 keys, 8 heads of 64: 74 us; with up to 1024 a part 83).  Registers
+// for a fourth workgroup a CU would spill (82 us).
+int64_t qk_blocks(const igc_qk_norm* p, const igc_qk_part& x, bool backward) {
+    const int64_t n = qk_tiles(x, p->head_dim);
+    if (!backward || n == 0) return n;
+    const int64_t q = qk_tiles(p->q, p->head_dim), k = qk_tiles(p->k, p->head_dim);
+    int64_t rounds = ceil_div(q + k, kQkBwdBlocks);
+    // two parts round up
+    if (ceil_div(q, rounds) + ceil_div(k, rounds) > kQkBwdBlocks)
+        rounds = ceil_div(q + k, kQkBwdBlocks - 1);
+    return ceil_div(n, rounds);
 }
 
 size_t qk_ws(const igc_qk_norm* p) {
     if (!p->q.dweight && !p->k.dweight) return 0;
-    return (size_t)((qk_blocks(p->q, p->head_dim, true) + qk_blocks(p->k, p->head_dim, true)) *
+    return (size_t)((qk_blocks(p, p->q, true) + qk_blocks(p, p->k, true)) *
                     qk_lanes((int)p->head_dim) * 8) * sizeof(float);
 }
 
@@ -421,7 +435,6 @@ int32_t check_qk(const igc_qk_norm* p, bool backward, QkTensors t[2]) {
     const igc_qk_part* parts[2] = {&p->q, &p->k};
     const int64_t d = p->head_dim;
     const size_t ws = backward ? qk_ws(p) : 0;
-    int64_t blocks = 0;
     bool in_place = true;
     for (int i = 0; i < 2; ++i) {
         const igc_qk_part& x = *parts[i];
@@ -451,8 +464,9 @@ int32_t check_qk(const igc_qk_norm* p, bool backward, QkTensors t[2]) {
             in_place = false;
             if (meet(t[i].o.p, t[i].o.bytes, t[i].x.p, t[i].x.bytes)) return IGC_DECLINE_OVERLAP;
         }
-        blocks += qk_blocks(x, d, backward);
     }
+    // both parts are of checked sizes here
+    const int64_t blocks = qk_blocks(p, p->q, backward) + qk_blocks(p, p->k, backward);
     if (blocks > kMaxGrid) return IGC_DECLINE_SIZE_LIMIT;
     for (int i = 0; i < 2; ++i) {
         const Tensor &o = t[i].o, &ox = t[1 - i].x, &og = t[1 - i].g;
@@ -523,7 +537,7 @@ int32_t run_qk(const igc_qk_norm* p, bool backward, void* stream) {
         o.H = (int)x.heads;
         o.hc = (int)ceil_div(x.heads, kQkHeads);
         o.items = qk_empty(x) ? 0 : x.batch * x.tokens * o.hc;
-        o.blocks = (int)qk_blocks(x, p->head_dim, backward);
+        o.blocks = (int)qk_blocks(p, x, backward);
     }
     const int mode = p->interleaved ? ROT_PAIRS : a.R % 16 == 0 ? ROT_HALVES : ROT_HALVES_ANY;
     const hipStream_t st = (hipStream_t)stream;
