@@ -53,7 +53,8 @@ __device__ __forceinline__ float ds_scale(const AttnArgs& a, int64_t bh, int lan
 }
 
 // -Delta and lse of the packed rows [bh][rows_pad], and for fp16 the squared
-// maxima of do and v of this workgroup's share of a head.  16 lanes a row.
+// maxima of do and v of this workgroup's share of a head.  16 lanes a row;
+// bound by the bytes of o and do (2 x 4096 rows, 16 heads of 128: 14 us).
 template <int DT>
 __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnArgs a) {
     const int bh = blockIdx.x / a.bound_n, ch = blockIdx.x - bh * a.bound_n;
@@ -160,7 +161,10 @@ __device__ __forceinline__ void issue_packed(const TileStage<DP, ROWS, NW>& st, 
 // tiles.  The keys' own operands (k and v) stay in registers, or in LDS
 // (KV_LDS) where the registers of two waves a SIMD do not hold them.  RG = 2:
 // two waves a key block take alternate blocks of 32 rows, and their sums are
-// added through LDS at the end.
+// added through LDS at the end.  Long walks keep the matrix cores busy for
+// half of the time (2 x 4096 rows x 2048 keys ragged, 16 heads on 8 of 128:
+// 255 to 280 us); short ones are bound by their rows' round trips (32 x 784
+// rows, 77 keys, 8 heads of 64: 21 us, of which the loads alone take 14).
 template <int DP, int NWK, int RG, int QT, bool KV_LDS>
 struct KvShape {
     static constexpr int NW = NWK * RG;
@@ -394,6 +398,8 @@ __global__ __launch_bounds__(NWK * RG * 64, OCC) void attn_bwd_kv_kernel(AttnArg
 // ---------------------------------------------------------------------------
 // dq: the forward kernel's walk (32 rows a wave, keys in tiles of 64) with
 // both score products, S^T = K Q^T and dP^T = V dO^T, and dq^T += K^T ds^T.
+// Bound as that kernel (2 x 4096 rows x 2048 keys ragged, 16 heads on 8 of
+// 128: 158 to 175 us, matrix cores busy for half of it).
 template <int DT, int DP, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void attn_bwd_q_kernel(AttnArgs a) {
     constexpr int KT = 64, DB = DP / 32, KS = DP / 16;

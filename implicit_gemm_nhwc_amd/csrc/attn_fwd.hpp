@@ -105,7 +105,12 @@ __device__ __forceinline__ void fwd_finish(const AttnArgs& a, int b, int hk, int
 
 // ---------------------------------------------------------------------------
 // Many rows: NW waves of 32 rows walk the keys in tiles of 64, double buffered
-// in LDS through direct loads, one barrier a tile.
+// in LDS through direct loads, one barrier a tile.  At 128 values a head the
+// matrix cores and the vector units are both busy for half of the time and the
+// power limit sets the clock (2 x 16384 rows x 4096 keys, 16 heads: 1.04 ms,
+// 1.05 PFLOP/s; with two blocks of rows a wave, which leaves one wave a SIMD,
+// 2.7 ms).  At 64 the softmax's vector instructions bound it (4 x 3136 x 1333
+// ragged, 16 heads: 67 to 73 us).
 // Waves a SIMD that the registers of the kernel below are cut to (and its LDS
 // allows): one register more than 512 / waves costs a wave.
 constexpr int fwd_waves(int dp) { return dp <= 64 ? 4 : dp <= 96 ? 3 : 2; }
@@ -224,8 +229,10 @@ __global__ __launch_bounds__(NW * 64, fwd_waves(DP)) void attn_fwd_kernel(AttnAr
 // for its next block's keys as soon as the score products have read the
 // present ones, and for the next values after the second product, so that its
 // memory requests never pause; the waves' results are joined through LDS at
-// the end.  A round of all waves is one memory latency; eight waves in half
-// the LDS each beat four with whole double buffers.
+// the end.  Long caches are bound by HBM (4 sequences of up to 65537 keys, 8
+// key heads of 128: 149 us, 5.4 TB/s), short ones by latency, one a round of
+// all waves: eight waves in half the LDS each (8 x 784 keys: 8.5 us, the long
+// ones 144 to 149) beat four with whole double buffers (11.0 and 158).
 template <int DT, int DP, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void attn_token_kernel(AttnArgs a) {
     constexpr int KT = 32, DB = DP / 32, KS = DP / 16;
