@@ -17,8 +17,8 @@ namespace {
 using namespace igc;
 
 constexpr int64_t kLim31 = (int64_t)1 << 31;
-constexpr int64_t kStrideLim = (int64_t)1 << 23;        // token and head strides, elements
-constexpr int64_t kBatchStrideLim = (int64_t)1 << 40;   // batch strides, elements
+constexpr int64_t kStrideLim = (int64_t)1 << 23;        // strides within a tile, elements
+constexpr int64_t kBatchStrideLim = (int64_t)1 << 40;   // strides between 64-bit bases, elements
 constexpr int64_t kMaxGrid = kLim31 - 1;
 constexpr int64_t kQkBwdBlocks = 3 * kNumCUs;           // three a CU: what the registers hold
 
@@ -40,7 +40,7 @@ struct Tensor {
 
 // Gate of one view; `write` for outputs.  Empty tensors may be NULL.
 int32_t check_view(const igc_attn_view& v, int64_t nb, int64_t nt, int64_t nh, int64_t d,
-                   bool write, Tensor* out) {
+                   bool write, int64_t head_lim, Tensor* out) {
     Tensor x{v.data, 0, 0, 0, 0};
     const int64_t n[3] = {nb, nt, nh};
     int64_t s[3] = {v.batch, v.token, v.head};
@@ -54,8 +54,12 @@ int32_t check_view(const igc_attn_view& v, int64_t nb, int64_t nt, int64_t nh, i
         if (n[i] == 1) s[i] = 0;
         if (s[i] < 0) return IGC_DECLINE_STRIDE;
         if (s[i] % 8) return IGC_DECLINE_ALIGNMENT;
-        if (s[i] >= (i == 0 ? kBatchStrideLim : kStrideLim)) return IGC_DECLINE_SIZE_LIMIT;
+        if (s[i] >= (i == 0 ? kBatchStrideLim : i == 1 ? kStrideLim : head_lim))
+            return IGC_DECLINE_SIZE_LIMIT;
     }
+    // no address space holds more
+    if ((double)nb * (double)s[0] + (double)nt * (double)s[1] + (double)nh * (double)s[2] > 0x1p56)
+        return IGC_DECLINE_SIZE_LIMIT;
     if (write) {
         // axes from the smallest stride up: each has to step over all before
         int ord[3] = {0, 1, 2};
@@ -183,12 +187,17 @@ int32_t check_attn_views(const igc_cross_attn* p, AttnTensors* t, bool write_out
     int32_t r;
     const int64_t d = p->head_dim;
     const bool any = p->batch && p->q_len && p->q_heads;
-    if ((r = check_view(p->q, p->batch, p->q_len, p->q_heads, d, false, &t->q))) return r;
-    if ((r = check_view(p->k, any ? p->batch : 0, p->kv_len, p->kv_heads, d, false, &t->k)))
+    if ((r = check_view(p->q, p->batch, p->q_len, p->q_heads, d, false, kStrideLim, &t->q)))
         return r;
-    if ((r = check_view(p->v, any ? p->batch : 0, p->kv_len, p->kv_heads, d, false, &t->v)))
+    // a head of the keys is a 64-bit base: a long head-major cache has large
+    // head strides
+    const int64_t nb = any ? p->batch : 0;
+    if ((r = check_view(p->k, nb, p->kv_len, p->kv_heads, d, false, kBatchStrideLim, &t->k)))
         return r;
-    if ((r = check_view(p->out, p->batch, p->q_len, p->q_heads, d, write_out, &t->o))) return r;
+    if ((r = check_view(p->v, nb, p->kv_len, p->kv_heads, d, false, kBatchStrideLim, &t->v)))
+        return r;
+    if ((r = check_view(p->out, p->batch, p->q_len, p->q_heads, d, write_out, kStrideLim, &t->o)))
+        return r;
     if (!packed_fits(p, t->q) || !packed_fits(p, t->o)) return IGC_DECLINE_SIZE_LIMIT;
     if (p->kv_lens && !aligned(p->kv_lens, 4)) return IGC_DECLINE_ALIGNMENT;
     if (p->lse && !aligned(p->lse, 4)) return IGC_DECLINE_ALIGNMENT;
@@ -334,16 +343,21 @@ int32_t check_bwd(const igc_cross_attn_grad* p, GradTensors* t, AttnGradPlan* pl
     const int64_t d = f->head_dim;
     const bool rows = f->batch && f->q_len && f->q_heads;
     if (rows && !f->lse) return IGC_DECLINE_NULL_POINTER;
-    if ((r = check_view(p->dout, f->batch, f->q_len, f->q_heads, d, false, &t->g))) return r;
+    if ((r = check_view(p->dout, f->batch, f->q_len, f->q_heads, d, false, kStrideLim, &t->g)))
+        return r;
     t->dq = t->dk = t->dv = Tensor{nullptr, 0, 0, 0, 0};
     if (p->dq.data &&
-        (r = check_view(p->dq, f->batch, f->q_len, f->q_heads, d, true, &t->dq)))
+        (r = check_view(p->dq, f->batch, f->q_len, f->q_heads, d, true, kStrideLim, &t->dq)))
         return r;
     if (f->batch && f->kv_len && f->kv_heads && !p->dk.data != !p->dv.data)
         return IGC_DECLINE_NULL_POINTER;
     if (p->dk.data) {
-        if ((r = check_view(p->dk, f->batch, f->kv_len, f->kv_heads, d, true, &t->dk))) return r;
-        if ((r = check_view(p->dv, f->batch, f->kv_len, f->kv_heads, d, true, &t->dv))) return r;
+        if ((r = check_view(p->dk, f->batch, f->kv_len, f->kv_heads, d, true, kBatchStrideLim,
+                            &t->dk)))
+            return r;
+        if ((r = check_view(p->dv, f->batch, f->kv_len, f->kv_heads, d, true, kBatchStrideLim,
+                            &t->dv)))
+            return r;
     }
     for (const Tensor* x : {&t->g, &t->dq})
         if (!packed_fits(f, *x)) return IGC_DECLINE_SIZE_LIMIT;
@@ -439,10 +453,11 @@ int32_t check_qk(const igc_qk_norm* p, bool backward, QkTensors t[2]) {
     for (int i = 0; i < 2; ++i) {
         const igc_qk_part& x = *parts[i];
         const int64_t nb = qk_empty(x) ? 0 : x.batch;
-        if ((r = check_view(x.x, nb, x.tokens, x.heads, d, false, &t[i].x))) return r;
-        if ((r = check_view(x.out, nb, x.tokens, x.heads, d, true, &t[i].o))) return r;
+        const int64_t lim = kBatchStrideLim;   // every row has a 64-bit address
+        if ((r = check_view(x.x, nb, x.tokens, x.heads, d, false, lim, &t[i].x))) return r;
+        if ((r = check_view(x.out, nb, x.tokens, x.heads, d, true, lim, &t[i].o))) return r;
         t[i].g = t[i].x;
-        if (backward && (r = check_view(x.grad, nb, x.tokens, x.heads, d, false, &t[i].g)))
+        if (backward && (r = check_view(x.grad, nb, x.tokens, x.heads, d, false, lim, &t[i].g)))
             return r;
         if (!aligned(x.weight, 4) || !aligned(x.dweight, 4) || !aligned(x.table, 4) ||
             !aligned(x.positions, 4))

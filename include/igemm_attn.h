@@ -71,9 +71,10 @@ typedef struct igc_attn_view {
  * partial results (fp32, in the workspace) a second launch joins in a fixed
  * order: results do not change from run to run.
  * Limits: kv_len and batch * heads below 2^31, q_len * q_heads / kv_heads
- * below 2^29; token and head strides of q, k, v, out (and of the gradients)
- * below 2^23 elements; of q and out (dout, dq) 65 token strides and the
- * strides over the heads of a group together below 2^31 bytes.
+ * below 2^29; token strides of q, k, v, out (and of the gradients), and head
+ * strides of q and out (dout, dq), below 2^23 elements; of these 65 token
+ * strides and the strides over the heads of a group together below 2^31
+ * bytes.  Batch strides, and head strides of k and v (dk, dv), below 2^40.
  */
 typedef struct igc_cross_attn {
     int64_t batch, q_len, kv_len, q_heads, kv_heads, head_dim;

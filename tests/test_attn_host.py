@@ -93,6 +93,26 @@ def test_attention_refusals(kw, reason):
     assert L.cross_attn_fwd(packed, None) == 0
 
 
+def test_head_major_strides():
+    """Keys and values of a long head-major cache have head strides of
+    kv_len * D; queries stay within what a tile addresses in 32 bits."""
+    L = igc.lib()
+    # far above the other buffers of the calls
+    far = 1 << 46
+    for head, reason in ((1 << 23, 0), (1 << 39, 0), (1 << 40, "size_limit")):
+        for n in "kv":
+            rc = L.cross_attn_fwd_check(_attn(**{n + "_head": head, n + "_data": far}))
+            assert rc == 0 if reason == 0 else _reason(rc) == reason
+    for name in ("q_head", "o_head"):
+        assert _reason(L.cross_attn_fwd_check(_attn(**{name: 1 << 23}))) == "size_limit"
+    # more than an address space holds
+    rc = L.cross_attn_fwd_check(_attn(b=1 << 22, k_batch=1 << 39))
+    assert _reason(rc) == "size_limit"
+    for n in ("dk", "dv"):
+        views = {n: dict(data=far, batch=1 << 39, head=1 << 24)}
+        assert L.cross_attn_bwd_check(_grad(views)) == 0
+
+
 def test_attention_workspace_rules():
     L = igc.lib()
     few = dict(b=1, tq=1, tk=20000, hq=8, hk=8)

@@ -293,6 +293,29 @@ def test_offsets_past_32_bits(tq):
     assert torch.equal(lib_dk.contiguous(), y_dk(go, q, kc, vc, out, lse))
 
 
+@pytest.mark.parametrize("tq", [1, 40])
+def test_head_major_cache(tq):
+    """Keys and values [b, heads, tokens, D] seen as [b, tokens, heads, D],
+    with heads further apart than 2^23 elements: the dense cache's bits."""
+    tk, d = 70000, 128
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    q, go = (torch.randn(1, tq, 4, d, device=DEV, generator=gen).to(BF) for _ in range(2))
+    kv = torch.randn(2, 1, 2, tk, d, device=DEV, generator=gen).to(BF)
+    k, v = kv.transpose(2, 3)
+    assert k.stride(2) > 1 << 23
+    kc, vc = k.contiguous(), v.contiguous()
+    out, lse = igc.cross_attention(q, k, v, return_lse=True)
+    want, want_lse = igc.cross_attention(q, kc, vc, return_lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    grads = igc.cross_attention_bwd(go, q, kc, vc, out, lse)
+    dkv = torch.full_like(kv, 7.0)
+    dk, dv = dkv.transpose(2, 3)
+    dq = torch.empty_like(q)
+    assert igc.cross_attn_bwd(go, q, k, v, out, lse, dq, dk, dv) == 1
+    for x, y in zip((dq, dk, dv), grads):
+        assert torch.equal(x, y)
+
+
 def y_dk(*a):
     return igc.cross_attention_bwd(*a)[1]
 

@@ -170,6 +170,21 @@ def test_strides_in_place_and_guards():
     assert torch.equal(e[2], igc.qk_norm_rope(x, q_weight=w, q_table=table)[0])
 
 
+def test_head_major_rows():
+    """Heads further apart than 2^23 elements, in place in a cache."""
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    cache = torch.randn(1, 2, 70000, 128, device=DEV, generator=gen).to(torch.bfloat16)
+    k = cache.transpose(1, 2)
+    assert k.stride(2) > 1 << 23
+    g = torch.randn(1, 70000, 2, 128, device=DEV, generator=gen).to(torch.bfloat16)
+    table = igc.rope_table(70000, 128, device=DEV)
+    want = igc.qk_norm_rope(k.contiguous(), q_table=table)
+    assert torch.equal(igc.qk_norm_rope(k, q_table=table), want)
+    for x, y in zip(igc.qk_norm_rope_bwd(g, None, k, q_table=table),
+                    igc.qk_norm_rope_bwd(g, None, k.contiguous(), q_table=table)):
+        assert x is y is None or torch.equal(x, y)
+
+
 def test_empty_extents():
     table = igc.rope_table(8, 64, device=DEV)
     for shape in ((0, 4, 2, 64), (2, 0, 2, 64), (2, 4, 0, 64)):
