@@ -199,7 +199,7 @@ __global__ __launch_bounds__(NWK * RG * 64, OCC) void attn_bwd_kv_kernel(AttnArg
     const bool valid = mask_byte(mrow, key0, len, kr) != 0 && key0 + kr < len;
     // the whole workgroup's keys may be out of range: nothing to sum then
     const int r_begin = sp * a.split;
-    const int r_end = kt * NWK * 32 < len ? min(a.rows, r_begin + a.split) : r_begin;
+    const int r_end = kt * NWK * 32 < len ? split_end(r_begin, a.split, a.rows) : r_begin;
     const bool idle = !__any(valid);   // this wave then only stages
 
     i32x4 kf[KS], vf[KS];
@@ -416,7 +416,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_bwd_q_kernel(AttnArgs a) {
     const int bh = idx / a.nsplit;
     const int hk = bh % a.Hk, b = bh / a.Hk;
     const int len = a.lens ? max(0, min(a.lens[b], a.Tk)) : a.Tk;
-    const int j_begin = sp * a.split, j_end = min(len, j_begin + a.split);
+    const int j_begin = sp * a.split, j_end = split_end(j_begin, a.split, len);
 
     const int row0 = (rt * NW + wave) * 32, row = row0 + (lane & 31), t0 = div_g(a, row0);
     i32x4 qf[KS], gf[KS];

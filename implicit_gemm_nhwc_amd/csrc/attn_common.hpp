@@ -12,6 +12,7 @@
 // (ds_read_b64_tr_b16: each lane gets 4 consecutive rows of one column).
 #pragma once
 
+#include "attn_split.hpp"
 #include "igemm_kernels.hpp"
 
 namespace igc {

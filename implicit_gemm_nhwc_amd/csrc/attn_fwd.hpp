@@ -136,7 +136,7 @@ __global__ __launch_bounds__(NW * 64, fwd_waves(DP)) void attn_fwd_kernel(AttnAr
     const int hk = idx % a.Hk, b = idx / a.Hk;
 
     const int len = a.lens ? max(0, min(a.lens[b], a.Tk)) : a.Tk;
-    const int j_begin = sp * a.split, j_end = min(len, j_begin + a.split);
+    const int j_begin = sp * a.split, j_end = split_end(j_begin, a.split, len);
 
     i32x4 qf[KS];
     f32x16 acc[DB];
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_token_kernel(AttnArgs a) {
     idx /= a.nsplit;
     const int hk = idx % a.Hk, b = idx / a.Hk;
     const int len = a.lens ? max(0, min(a.lens[b], a.Tk)) : a.Tk;
-    const int j_begin = sp * a.split + wave * KT, j_end = min(len, sp * a.split + a.split);
+    const int j_begin = sp * a.split + wave * KT, j_end = split_end(sp * a.split, a.split, len);
 
     const int row = lane & 31;
     i32x4 qf[KS];
