@@ -326,6 +326,10 @@ __global__ __launch_bounds__(NWK * RG * 64, OCC) void attn_bwd_kv_kernel(AttnArg
             }
             buf ^= 1;
         }
+    } else if constexpr (KV_LDS) {
+        // without rows nothing above has waited for the keys' direct loads,
+        // and the sums below take their place in LDS
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
     if constexpr (RG > 1) {
         // the row groups' sums through LDS, dk then dv, lane by lane: the upper

@@ -1,0 +1,47 @@
+"""Forms of the attention kernels that ordinary small calls do not reach."""
+import os
+import sys
+
+import pytest
+import torch
+
+import implicit_gemm_nhwc_amd as igc
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, HF = torch.bfloat16, torch.float16
+
+
+def setup_module(_):
+    if not (os.path.exists(igc.LIB_PATH) and os.path.exists(igc.POISON_LIB_PATH)):
+        import __graft_entry__
+        __graft_entry__.build()
+
+
+def _say(msg):
+    print(msg, flush=True)
+    sys.stdout.flush()
+
+
+def _rnd(dt, *shape, seed=0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dt).to(DEV)
+
+
+@pytest.mark.parametrize("library", ["ordinary", "poisoned"])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("d", [8, 40, 64, 96, 104, 128])
+def test_no_query_rows(d, dt, library):
+    """The sums over no rows are 0, also where the kernel has staged the keys
+    in LDS (D above 96), whose place its sums of row groups take."""
+    path = igc.LIB_PATH if library == "ordinary" else igc.POISON_LIB_PATH
+    for tk in (1, 31, 64, 130, 777):
+        _say(f"no rows {d} {dt} {library} {tk}")
+        q = torch.empty(3, 0, 4, d, dtype=dt, device=DEV)
+        k, v = _rnd(dt, 3, tk, 2, d, seed=1), _rnd(dt, 3, tk, 2, d, seed=2)
+        lens = torch.tensor([tk, 0, tk // 2], dtype=torch.int32, device=DEV)
+        with igc.using_library(path):
+            for kw in ({}, {"kv_lens": lens}):
+                out, lse = igc.cross_attention(q, k, v, return_lse=True, **kw)
+                dq, dk, dv = igc.cross_attention_bwd(q, q, k, v, out, lse, **kw)
+                assert dq.shape == q.shape and dk.shape == k.shape
+                assert (dk == 0).all() and (dv == 0).all()
