@@ -62,6 +62,13 @@ int64_t type_code(at::ScalarType t) {
 
 bool given(PyObject* o) { return o != Py_None; }
 
+// Truth value of an argument (one that has none is Python's to report).
+bool truth(PyObject* o) {
+    const int t = PyObject_IsTrue(o);
+    if (t < 0) no();
+    return t != 0;
+}
+
 template <typename T>
 T* dense(PyObject* o, at::ScalarType type, int64_t device, at::IntArrayRef sizes) {
     const at::Tensor& t = on_gpu(o, type, device, (int64_t)sizes.size());
@@ -171,7 +178,7 @@ PyObject* cross_attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
         const at::Tensor& q = tensor(o[1]);
         at::Tensor out = fresh(q), lse, ws;
         a.out = view(out);
-        const bool with_lse = PyObject_IsTrue(o[7]) == 1;
+        const bool with_lse = truth(o[7]);
         if (with_lse) {
             lse = floats(q, {a.batch, a.q_heads, a.q_len});
             a.lse = static_cast<float*>(lse.data_ptr());
@@ -259,7 +266,7 @@ igc_qk_norm norm_args(PyObject* const* o, int64_t device) {
     a.rot_dim = rot;
     a.eps = PyFloat_AsDouble(o[8]);
     if (PyErr_Occurred()) no();
-    a.interleaved = PyObject_IsTrue(o[9]) == 1;
+    a.interleaved = truth(o[9]);
     return a;
 }
 
