@@ -259,9 +259,9 @@ AttnArgs attn_args(const igc_cross_attn* p, const AttnTensors& t) {
     a.Tk = (int)p->kv_len;
     a.Hq = (int)p->q_heads;
     a.Hk = (int)p->kv_heads;
-    a.G = a.Hk ? a.Hq / a.Hk : 1;
+    a.G = a.Hq && a.Hk ? a.Hq / a.Hk : 1;   // a divisor also without query heads
     a.D = (int)p->head_dim;
-    a.rows = a.Tq * a.G;
+    a.rows = a.Hq ? a.Tq * a.G : 0;
     a.scale = (float)p->scale;
     a.c = (float)(p->scale * 1.4426950408889634);
     if (a.G > 1) {

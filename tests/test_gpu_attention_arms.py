@@ -45,3 +45,18 @@ def test_no_query_rows(d, dt, library):
                 dq, dk, dv = igc.cross_attention_bwd(q, q, k, v, out, lse, **kw)
                 assert dq.shape == q.shape and dk.shape == k.shape
                 assert (dk == 0).all() and (dv == 0).all()
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("d", [40, 64, 128])
+def test_no_query_heads(d, dt):
+    """Keys that no head reads: no outputs, and gradients of 0."""
+    for b, tq, tk, hk in ((2, 5, 77, 3), (1, 200, 300, 1), (2, 0, 64, 2)):
+        _say(f"no heads {d} {dt} {b} {tq} {tk} {hk}")
+        q = torch.empty(b, tq, 0, d, dtype=dt, device=DEV)
+        k, v = _rnd(dt, b, tk, hk, d, seed=1), _rnd(dt, b, tk, hk, d, seed=2)
+        out, lse = igc.cross_attention(q, k, v, return_lse=True)
+        assert out.shape == q.shape and lse.shape == (b, 0, tq)
+        dq, dk, dv = igc.cross_attention_bwd(q, q, k, v, out, lse)
+        assert dq.shape == q.shape and (dk == 0).all() and (dv == 0).all()
+        assert dk.shape == k.shape and dv.shape == v.shape
