@@ -19,6 +19,7 @@ using namespace igc;
 constexpr int64_t kLim31 = (int64_t)1 << 31;
 constexpr int64_t kStrideLim = (int64_t)1 << 23;        // strides within a tile, elements
 constexpr int64_t kBatchStrideLim = (int64_t)1 << 40;   // strides between 64-bit bases, elements
+constexpr double kExtentLim = 0x1p56;                   // no address space holds more
 constexpr int64_t kMaxGrid = kLim31 - 1;
 constexpr int64_t kQkBwdBlocks = 3 * kNumCUs;           // three a CU: what the registers hold
 
@@ -57,8 +58,8 @@ int32_t check_view(const igc_attn_view& v, int64_t nb, int64_t nt, int64_t nh, i
         if (s[i] >= (i == 0 ? kBatchStrideLim : i == 1 ? kStrideLim : head_lim))
             return IGC_DECLINE_SIZE_LIMIT;
     }
-    // no address space holds more
-    if ((double)nb * (double)s[0] + (double)nt * (double)s[1] + (double)nh * (double)s[2] > 0x1p56)
+    if ((double)nb * (double)s[0] + (double)nt * (double)s[1] + (double)nh * (double)s[2] >
+        kExtentLim)
         return IGC_DECLINE_SIZE_LIMIT;
     if (write) {
         // axes from the smallest stride up: each has to step over all before
@@ -203,6 +204,8 @@ int32_t check_attn_views(const igc_cross_attn* p, AttnTensors* t, bool write_out
     if (p->lse && !aligned(p->lse, 4)) return IGC_DECLINE_ALIGNMENT;
     if (p->key_mask && (p->key_mask_stride < 0 || p->key_mask_stride >= kBatchStrideLim))
         return IGC_DECLINE_STRIDE;
+    if (p->key_mask && (double)(p->batch - 1) * (double)p->key_mask_stride > kExtentLim)
+        return IGC_DECLINE_SIZE_LIMIT;
     return IGC_OK;
 }
 
@@ -468,6 +471,8 @@ int32_t check_qk(const igc_qk_norm* p, bool backward, QkTensors t[2]) {
         if (p->rot_dim && x.positions && x.table_rows == 0) return IGC_DECLINE_SHAPE;
         if (x.positions && (x.positions_stride < 0 || x.positions_stride >= kBatchStrideLim))
             return IGC_DECLINE_STRIDE;
+        if (x.positions && (double)(x.batch - 1) * (double)x.positions_stride > kExtentLim)
+            return IGC_DECLINE_SIZE_LIMIT;
         if (backward) {
             if (meet(t[i].o.p, t[i].o.bytes, t[i].x.p, t[i].x.bytes)) return IGC_DECLINE_OVERLAP;
             if (!same_view(t[i].o, t[i].g)) {

@@ -5,7 +5,7 @@ import threading
 import pytest
 
 import implicit_gemm_nhwc_amd as igc
-from test_attn_host import _grad, _reason
+from test_attn_host import _attn, _grad, _norm, _reason
 
 
 def _ends(f, *args):
@@ -30,3 +30,40 @@ def test_groups_of_many_heads(hq):
     assert _reason(L.cross_attn_bwd_check(packed)) == "ok"
     assert L.cross_attn_bwd_workspace_bytes(packed) == 0
     assert _ends(L.cross_attn_bwd, packed, None) == 1
+
+
+# a tensor of which every batch entry is the same (inputs), or small (out)
+_SHARED = dict(tq=1, tk=500, hq=1, hk=1, d=8, q_batch=0, k_batch=0, v_batch=0)
+FAR = 1 << 60      # above all buffers of the calls
+
+
+@pytest.mark.parametrize("b,stride,reason", [
+    (1 << 30, (1 << 40) - 1, "size_limit"),       # 2^70: passes 64 bits
+    ((1 << 24) + 1, 1 << 39, "size_limit"),       # 2^63: a negative product
+    ((1 << 25) + 1, 1 << 39, "size_limit"),       # 2^64: the product is 0
+    (1 << 20, 1 << 37, "size_limit"),             # 2^57: more than an address space
+    (1 << 20, 500, "ok"), (1 << 20, 0, "ok"), (1, (1 << 40) - 1, "ok"),
+])
+def test_mask_extents(b, stride, reason):
+    L = igc.lib()
+    packed = _attn(b=b, mask=FAR, mask_stride=stride, **_SHARED)
+    assert _reason(L.cross_attn_fwd_check(packed)) == reason
+    none = dict(data=0)
+    same = dict(batch=0, token=0, head=0)
+    packed = _grad(dict(go=same, dq=none, dk=none, dv=none), b=b, mask=FAR, mask_stride=stride,
+                   **_SHARED)
+    assert _reason(L.cross_attn_bwd_check(packed)) == reason
+
+
+@pytest.mark.parametrize("b,stride,reason", [
+    (1 << 30, (1 << 40) - 1, "size_limit"), ((1 << 24) + 1, 1 << 39, "size_limit"),
+    ((1 << 25) + 1, 1 << 39, "size_limit"), (1 << 20, 1 << 37, "size_limit"),
+    (1 << 20, 100, "ok"), (1 << 20, 0, "ok"), (1, (1 << 40) - 1, "ok"),
+])
+def test_position_extents(b, stride, reason):
+    L = igc.lib()
+    part = dict(b=b, t=1, h=1, x_b=0, g_b=0, o=FAR >> 1, o_b=64, o_t=64, pos=FAR, pos_b=stride)
+    none = dict(b=0, x=0, o=0, g=0)
+    for packed in (_norm(q=part, k=none), _norm(q=none, k=part)):
+        assert _reason(L.qk_norm_rope_fwd_check(packed)) == reason
+        assert _reason(L.qk_norm_rope_bwd_check(packed)) == reason
