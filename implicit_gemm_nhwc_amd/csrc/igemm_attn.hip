@@ -83,6 +83,9 @@ int32_t check_view(const igc_attn_view& v, int64_t nb, int64_t nt, int64_t nh, i
     return IGC_OK;
 }
 
+// scale * log2(e), as the kernels hold it.
+float scale_log2(const igc_cross_attn* p) { return (float)(p->scale * 1.4426950408889634); }
+
 // Shapes and parameters of cross attention.
 int32_t check_attn_shape(const igc_cross_attn* p) {
     if (!p) return IGC_DECLINE_NULL_POINTER;
@@ -91,7 +94,7 @@ int32_t check_attn_shape(const igc_cross_attn* p) {
         return IGC_DECLINE_SHAPE;
     if (p->q_heads > 0 && (p->kv_heads == 0 || p->q_heads % p->kv_heads)) return IGC_DECLINE_GROUPS;
     if (p->head_dim < 8 || p->head_dim > 128 || p->head_dim % 8) return IGC_DECLINE_HEAD_DIM;
-    if (!(p->scale > 0.0) || !isfinite((float)p->scale) || (float)p->scale < 1e-30f)
+    if (!(p->scale > 0.0) || (float)p->scale < 1e-30f || !isfinite(scale_log2(p)))
         return IGC_DECLINE_SCALE;
     if (p->batch >= kLim31 || p->q_len >= kLim31 || p->kv_len >= kLim31 || p->q_heads >= kLim31 ||
         p->kv_heads >= kLim31)
@@ -266,7 +269,7 @@ AttnArgs attn_args(const igc_cross_attn* p, const AttnTensors& t) {
     a.D = (int)p->head_dim;
     a.rows = a.Hq ? a.Tq * a.G : 0;
     a.scale = (float)p->scale;
-    a.c = (float)(p->scale * 1.4426950408889634);
+    a.c = scale_log2(p);
     if (a.G > 1) {
         // row / G = mulhi(row, ceil(2^(31 + L) / G)) >> (L - 1), L = ceil(log2 G)
         int L = 0;

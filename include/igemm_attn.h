@@ -42,8 +42,8 @@ extern "C" {
 enum {
     IGC_DECLINE_HEAD_DIM = 15,  /* D not one of 8, 16, ... 128; for the norm an
                                    odd or too large number of rotated values */
-    IGC_DECLINE_SCALE = 16      /* scale not positive and finite; eps negative
-                                   or not finite */
+    IGC_DECLINE_SCALE = 16      /* scale below 1e-30, or scale * log2(e) not
+                                   finite in fp32; eps negative or not finite */
 };
 
 typedef struct igc_attn_view {

@@ -67,3 +67,15 @@ def test_position_extents(b, stride, reason):
     for packed in (_norm(q=part, k=none), _norm(q=none, k=part)):
         assert _reason(L.qk_norm_rope_fwd_check(packed)) == reason
         assert _reason(L.qk_norm_rope_bwd_check(packed)) == reason
+
+
+@pytest.mark.parametrize("scale,reason", [
+    (3e38, "scale"),       # finite in fp32, but scale * log2(e), which the kernels hold, is not
+    (2.36e38, "scale"), (2.35e38, "ok"), (1e-30, "ok"), (9e-31, "scale"),
+])
+def test_scale_range(scale, reason):
+    L = igc.lib()
+    assert _reason(L.cross_attn_fwd_check(_attn(scale=scale))) == reason
+    assert _reason(L.cross_attn_bwd_check(_grad(scale=scale))) == reason
+    if reason != "ok":
+        assert L.cross_attn_fwd(_attn(scale=scale), None) == 0
