@@ -20,8 +20,14 @@ constexpr int64_t kLim31 = (int64_t)1 << 31;
 constexpr int64_t kStrideLim = (int64_t)1 << 23;        // strides within a tile, elements
 constexpr int64_t kBatchStrideLim = (int64_t)1 << 40;   // strides between 64-bit bases, elements
 constexpr double kExtentLim = 0x1p56;                   // no address space holds more
-constexpr int64_t kMaxGrid = kLim31 - 1;
 constexpr int64_t kQkBwdBlocks = 3 * kNumCUs;           // three a CU: what the registers hold
+
+// Whether a launch of so many workgroups holds fewer than 2^32 threads; HIP
+// takes the count modulo 2^32 (2^24 - 16 workgroups of 512 threads ran half of
+// themselves and reported success).
+bool launchable(int64_t groups, int64_t threads) {
+    return groups <= (((int64_t)1 << 32) - 1) / threads;
+}
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
@@ -230,7 +236,8 @@ int32_t check_fwd(const igc_cross_attn* p, AttnTensors* t, AttnPlan* plan) {
     if ((r = check_attn_shape(p))) return r;
     if ((r = check_attn_views(p, t, true))) return r;
     *plan = fwd_plan(p);
-    if (p->batch * p->kv_heads * plan->row_tiles > kMaxGrid / plan->nsplit)
+    if (!launchable(p->batch * p->kv_heads * plan->row_tiles * plan->nsplit,
+                    (plan->token ? kTokenWaves : kAttnWaves) * 64))
         return IGC_DECLINE_SIZE_LIMIT;
     const size_t ws = fwd_ws(*plan);
     if (meets_inputs(p, *t, t->o.p, t->o.bytes) || meets_inputs(p, *t, p->lse, lse_bytes(p)) ||
@@ -369,9 +376,11 @@ int32_t check_bwd(const igc_cross_attn_grad* p, GradTensors* t, AttnGradPlan* pl
         if (!packed_fits(f, *x)) return IGC_DECLINE_SIZE_LIMIT;
     *plan = bwd_plan(f);
     const int64_t bh = f->batch * f->kv_heads;
-    if (bh * plan->key_tiles > kMaxGrid / (plan->kv_nsplit > 0 ? plan->kv_nsplit : 1) ||
-        bh * plan->row_tiles > kMaxGrid / (plan->q_nsplit > 0 ? plan->q_nsplit : 1) ||
-        bh > kMaxGrid / (plan->bound_n > 0 ? plan->bound_n : 1))
+    if (bh > 0 &&
+        (!launchable(bh * plan->key_tiles * plan->kv_nsplit,
+                     plan->kv_waves * plan->kv_groups * 64) ||
+         !launchable(bh * plan->row_tiles * plan->q_nsplit, kAttnWaves * 64) ||
+         (!plan->few_keys && !launchable(bh * plan->bound_n, kAttnWaves * 64))))
         return IGC_DECLINE_SIZE_LIMIT;
     const size_t ws = bwd_ws(*plan);
     auto meets = [&](const void* w, size_t n) {
@@ -490,7 +499,7 @@ int32_t check_qk(const igc_qk_norm* p, bool backward, QkTensors t[2]) {
     }
     // both parts are of checked sizes here
     const int64_t blocks = qk_blocks(p, p->q, backward) + qk_blocks(p, p->k, backward);
-    if (blocks > kMaxGrid) return IGC_DECLINE_SIZE_LIMIT;
+    if (!launchable(blocks, kQkThreads)) return IGC_DECLINE_SIZE_LIMIT;
     for (int i = 0; i < 2; ++i) {
         const Tensor &o = t[i].o, &ox = t[1 - i].x, &og = t[1 - i].g;
         if ((!in_place || backward) && meet(o.p, o.bytes, ox.p, ox.bytes))

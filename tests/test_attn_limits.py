@@ -79,3 +79,55 @@ def test_scale_range(scale, reason):
     assert _reason(L.cross_attn_bwd_check(_grad(scale=scale))) == reason
     if reason != "ok":
         assert L.cross_attn_fwd(_attn(scale=scale), None) == 0
+
+
+@pytest.mark.parametrize("heads,tq,tk,most", [
+    (1, 1, 300, (1 << 23) - 1),     # single tokens: 512 threads a key head
+    (16, 1, 1, (1 << 19) - 1),
+    (1, 200, 300, (1 << 23) - 1),   # two row tiles of 256 threads
+    (1, 64, 77, (1 << 24) - 1),     # few keys
+])
+def test_threads_of_an_attention_launch(heads, tq, tk, most):
+    """A launch of 2^32 threads or more would run only a part of itself."""
+    L = igc.lib()
+    kw = dict(tq=tq, tk=tk, hq=heads, hk=heads, d=8, k_batch=0, v_batch=0, q_batch=0, o_data=FAR)
+    assert _reason(L.cross_attn_fwd_check(_attn(b=most, **kw))) == "ok"
+    packed = _attn(b=most + 1, **kw)
+    assert _reason(L.cross_attn_fwd_check(packed)) == "size_limit"
+    assert L.cross_attn_fwd(packed, None) == 0
+
+
+@pytest.mark.parametrize("tq,tk,most", [
+    (1, 77, (1 << 24) - 1),          # rows in 256 threads, keys in three waves
+    (64, 300, (1 << 24) // 3),       # three key tiles of 256 threads
+    (1000, 100, (1 << 23) - 1),      # 16 row tiles a head walked: 512 threads
+])
+def test_threads_of_a_gradient_launch(tq, tk, most):
+    L = igc.lib()
+    none = dict(data=0)
+    views = dict(go=dict(batch=0, token=8, head=8), dq=none, dk=none, dv=none)
+    kw = dict(tq=tq, tk=tk, hq=1, hk=1, d=8, k_batch=0, v_batch=0, q_batch=0, o_data=FAR,
+              lse=FAR >> 1)
+    assert _reason(L.cross_attn_bwd_check(_grad(views, b=most, **kw))) == "ok"
+    packed = _grad(views, b=most + 1, **kw)
+    assert _reason(L.cross_attn_bwd_check(packed)) == "size_limit"
+    assert L.cross_attn_bwd(packed, None) == 0
+
+
+@pytest.mark.parametrize("d,items", [(8, 64), (64, 32), (128, 16)])
+def test_threads_of_a_norm_launch(d, items):
+    """items: a workgroup's lane groups (four heads of a token each)."""
+    L = igc.lib()
+    most = ((1 << 24) - 1) * items
+    none = dict(b=0, x=0, o=0, g=0)
+
+    def call(tokens):
+        part = dict(b=1, t=tokens, h=4, x_t=4 * d, x_h=d, g_t=4 * d, g_h=d, o_t=4 * d, o_h=d,
+                    x=1 << 50, g=1 << 51, o=1 << 52, table=0, rows=0)
+        return _norm(q=part, k=none, d=d, rot=0)
+
+    assert _reason(L.qk_norm_rope_fwd_check(call(most))) == "ok"
+    assert _reason(L.qk_norm_rope_fwd_check(call(most + 1))) == "size_limit"
+    assert L.qk_norm_rope_fwd(call(most + 1), None) == 0
+    # backward the workgroups loop
+    assert _reason(L.qk_norm_rope_bwd_check(call(most + 1))) == "ok"

@@ -60,3 +60,21 @@ def test_no_query_heads(d, dt):
         dq, dk, dv = igc.cross_attention_bwd(q, q, k, v, out, lse)
         assert dq.shape == q.shape and (dk == 0).all() and (dv == 0).all()
         assert dk.shape == k.shape and dv.shape == v.shape
+
+
+def test_many_single_tokens():
+    """As many key heads as one launch takes (2^23 - 16 workgroups of eight
+    waves), one key each: the output is its value, and so is dv dout."""
+    b = (1 << 19) - 1
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    q, k, v, go = (torch.randn(b, 1, 16, 8, device=DEV, generator=gen).to(BF) for _ in range(4))
+    out, lse = igc.cross_attention(q, k, v, return_lse=True)
+    assert torch.equal(out, v)
+    s = (q.double() * k.double()).sum(-1).transpose(1, 2) * 8 ** -0.5
+    assert ((lse.double() - s).abs() <= 2.0 ** -20 * (1 + s.abs())).all()
+    dq, dk, dv = igc.cross_attention_bwd(go, q, k, v, out, lse)
+    # p differs from 1 by fp32 roundings, which one rounding of dv may show
+    assert ((dv.float() - go.float()).abs() <= 2.0 ** -8 * go.float().abs()).all()
+    q2, k2 = (torch.cat([t, t[:1]]) for t in (q, k))
+    with pytest.raises(igc.Declined, match="size_limit"):
+        igc.cross_attention(q2, k2, k2)
