@@ -65,11 +65,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t attn_rsrc(const void* base) {
                                              0x00020000);
 }
 // A buffer offset past the range: loads return zero, stores are dropped.
-// Every masked access of these kernels goes this way, by selecting the
-// offset, and none by a branch on the lane: the kernels fill the register
-// file, and where a value is moved to an accumulation register at the join of
-// such a branch the compiler was seen to put the copy before the execution
-// mask is restored, which loses the other lanes' values.
+// Every masked access of the kernels with matrix products goes this way while
+// their accumulators are needed further, by selecting the offset, and none by
+// a branch on the lane: they fill the register file, and where a value is
+// moved to an accumulation register at the join of such a branch the compiler
+// was seen to put the copy before the execution mask is restored, which loses
+// the other lanes' values.  (The single-token kernel's accumulators end in the
+// branch that stores them; the joins of split launches and the row pass of the
+// backward hold none; the compiler makes small lane branches of its own, such
+// as around a division.  tests/test_attn_assembly.py reads the built code for
+// such copies.)
 constexpr unsigned kOut = 0x80000000u;
 
 __device__ __forceinline__ u32x4 load16(const __amdgpu_buffer_rsrc_t& rs, unsigned off) {

@@ -323,7 +323,9 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_token_kernel(AttnArgs a) {
             w0 = w1;
         }
     }
-    // join: wave w's rows as floats [rows][DP] over its own LDS
+    // join: wave w's rows as floats [rows][DP] over its own LDS.  The one lane
+    // branch around accumulators: they end in it, so that nothing is copied at
+    // its join (all 32 rows stored without it: 8 x 784 keys 9.5 -> 11.9 us)
     l = sum_halves(l);
     float* po = reinterpret_cast<float*>(mine);
     if (row < a.rows) {
