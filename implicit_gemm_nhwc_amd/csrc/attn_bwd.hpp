@@ -115,7 +115,8 @@ __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnArgs a) {
             for (int o = 1; o < 16; o <<= 1) n += __shfl_xor(n, o, 64);
             vmax = fmaxf(vmax, n);
         }
-        __shared__ float red[2][16];
+        __shared__ __attribute__((aligned(16))) float red[2][16];
+        lds_poison<256>(reinterpret_cast<uint8_t*>(red), sizeof(red));
         if (c == 0) {
             red[0][sub] = gmax;
             red[1][sub] = vmax;

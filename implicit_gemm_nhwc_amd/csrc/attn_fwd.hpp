@@ -393,7 +393,11 @@ constexpr int kJoinLanes = 32, kJoinFew = 8;
 template <int DT, int GR>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     __shared__ f32x4 part[GR][kJoinLanes];
-    __shared__ float sum[GR];
+    __shared__ __attribute__((aligned(16))) float sum[GR > 4 ? GR : 4];
+    if constexpr (GR > 1) {
+        lds_poison<256>(reinterpret_cast<uint8_t*>(part), sizeof(part));
+        lds_poison<256>(reinterpret_cast<uint8_t*>(sum), sizeof(sum));
+    }
     const int64_t n = (int64_t)a.B * a.Hk * a.rows;
     const int lane = threadIdx.x % kJoinLanes, group = threadIdx.x / kJoinLanes;
     const int64_t at = GR > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + group;

@@ -170,7 +170,9 @@ __device__ __forceinline__ void qk_turn(const QkPart& p, int R, int b, int t, in
 
 template <int DT, int LPR, int MODE>
 __global__ __launch_bounds__(kQkThreads) void qk_norm_fwd_kernel(QkArgs a) {
-    __shared__ float pad[MODE == ROT_HALVES_ANY ? kQkThreads * 8 : 1];
+    __shared__ __attribute__((aligned(16))) float
+        pad[MODE == ROT_HALVES_ANY ? kQkThreads * 8 : 4];
+    lds_poison<kQkThreads>(reinterpret_cast<uint8_t*>(pad), sizeof(pad));
     const bool second = (int)blockIdx.x >= a.part[0].blocks;
     const QkPart& p = a.part[second];
     const int lane = threadIdx.x & 63, c = lane % LPR;
@@ -212,7 +214,8 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_fwd_kernel(QkArgs a) {
 
 template <int DT, int LPR, int MODE>
 __global__ __launch_bounds__(kQkThreads) void qk_norm_bwd_kernel(QkArgs a) {
-    __shared__ float pad[kQkThreads * 8];
+    __shared__ __attribute__((aligned(16))) float pad[kQkThreads * 8];
+    lds_poison<kQkThreads>(reinterpret_cast<uint8_t*>(pad), sizeof(pad));
     const bool second = (int)blockIdx.x >= a.part[0].blocks;
     const QkPart& p = a.part[second];
     const int lane = threadIdx.x & 63, c = lane % LPR;
@@ -288,7 +291,8 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_bwd_kernel(QkArgs a) {
 // 18 us).
 template <int DT>
 __global__ __launch_bounds__(1024) void qk_norm_dw_kernel(QkArgs a, int width) {
-    __shared__ float sum[64][17];
+    __shared__ __attribute__((aligned(16))) float sum[64][17];
+    lds_poison<1024>(reinterpret_cast<uint8_t*>(sum), sizeof(sum));
     const int part = blockIdx.y;
     const QkPart& p = a.part[part];
     if (!p.dw) return;
