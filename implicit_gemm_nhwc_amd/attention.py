@@ -11,6 +11,10 @@ Tensors are [batch, token, head, D], D adjacent, any other strides that are
 multiples of 16 bytes; an NHWC map [N, H, W, heads * D] is
 map.view(N, H * W, heads, D).
 
+Results carry no autograd history, whatever the inputs require: a training
+program calls the backward entries itself (or from its own
+torch.autograd.Function).
+
   cross_attn_fwd, cross_attn_fwd_check, cross_attn_fwd_workspace_bytes,
   cross_attn_bwd, cross_attn_bwd_check, cross_attn_bwd_workspace_bytes,
   qk_norm_rope_fwd, qk_norm_rope_fwd_check,
@@ -229,7 +233,8 @@ def cross_attention(q, k, v, *, scale=None, kv_lens=None, key_mask=None, return_
     and key_mask (uint8 or bool [b, tk], nonzero = attend) say which keys are
     valid; a row without one gives 0.  Returns out, dense like q, and with
     return_lse also the fp32 row statistics [b, hq, tq] for
-    cross_attention_bwd."""
+    cross_attention_bwd, which is the way to gradients (none are recorded for
+    autograd)."""
     device = _device(q)
     if _fast is not None and stream is None:
         r = _fast.cross_attention(_entries(), q, k, v, scale, kv_lens, key_mask, return_lse,
@@ -470,7 +475,7 @@ def qk_norm_rope(q, k=None, *, q_weight=None, k_weight=None, q_table=None, k_tab
     table.shape[1] values rotated in pairs by the table row (fp32 {cosines,
     sines}, rope_table) of their position (int32 [b, t] or None: the token's
     number).  Returns the two results, dense; k may be None (then q's result
-    alone)."""
+    alone).  Gradients by qk_norm_rope_bwd (none are recorded for autograd)."""
     device = _device(q)
     if _fast is not None and stream is None:
         r = _fast.qk_norm_rope(_entries(), q, k, q_weight, k_weight, q_table, k_table,

@@ -55,6 +55,9 @@ __device__ __forceinline__ float ds_scale(const AttnArgs& a, int64_t bh, int lan
 // -Delta and lse of the packed rows [bh][rows_pad], and for fp16 the squared
 // maxima of do and v of this workgroup's share of a head.  16 lanes a row;
 // bound by the bytes of o and do (2 x 4096 rows, 16 heads of 128: 14 us).
+// Delta takes the rounded out: over more than 128 keys out is small against
+// the values, and so is what its rounding adds to ds (few keys: Delta from the
+// probabilities, attn_short.hpp).
 template <int DT>
 __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnArgs a) {
     const int bh = blockIdx.x / a.bound_n, ch = blockIdx.x - bh * a.bound_n;

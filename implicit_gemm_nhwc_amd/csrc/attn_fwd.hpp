@@ -110,7 +110,7 @@ __device__ __forceinline__ void fwd_finish(const AttnArgs& a, int b, int hk, int
 // power limit sets the clock (2 x 16384 rows x 4096 keys, 16 heads: 1.04 ms,
 // 1.05 PFLOP/s; with two blocks of rows a wave, which leaves one wave a SIMD,
 // 2.7 ms).  At 64 the softmax's vector instructions bound it (4 x 3136 x 1333
-// ragged, 16 heads: 67 to 73 us).
+// ragged, 16 heads: 67 to 75 us).
 // Waves a SIMD that the registers of the kernel below are cut to (and its LDS
 // allows): one register more than 512 / waves costs a wave.
 constexpr int fwd_waves(int dp) { return dp <= 64 ? 4 : dp <= 96 ? 3 : 2; }
