@@ -75,9 +75,10 @@ typedef struct igc_attn_view {
  * strides of q and out (dout, dq), below 2^23 elements; of these 65 token
  * strides and the strides over the heads of a group together below 2^31
  * bytes.  Batch strides, and head strides of k and v (dk, dv), below 2^40.  A
- * launch holds fewer than 2^32 threads: batch * kv_heads below 2^23 for at
- * most 32 rows (q_len * q_heads / kv_heads), and below 2^24 over the row tiles
- * of 128 (at most 128 keys: over what the card runs at once) for more rows.
+ * launch holds fewer than 2^32 threads: with at most 32 rows (q_len * q_heads
+ * / kv_heads) batch * kv_heads is below 2^23; with more, batch * kv_heads times
+ * the tiles of 128 rows is below 2^24 (with at most 128 keys, where workgroups
+ * walk their rows, batch * kv_heads alone for large batches).
  */
 typedef struct igc_cross_attn {
     int64_t batch, q_len, kv_len, q_heads, kv_heads, head_dim;
@@ -154,9 +155,9 @@ size_t cross_attn_bwd_workspace_bytes(const igc_cross_attn_grad* args);
  * grad (backward) exactly; otherwise the ranges may not meet.  With both
  * parts in place the two may interleave in one buffer, provided no element
  * belongs to both.
- * Limits: the forward launches a workgroup for 8192 values of lane groups (a
- * token's heads in fours, D rounded up to 32, 64 or 128, 8 values a lane), and
- * has fewer than 2^24 of them.
+ * Limits: each axis below 2^31 and batch * tokens * heads below 2^40; the
+ * forward launches one workgroup for every 8192 values, heads rounded up to a
+ * multiple of four and D to 32, 64 or 128, and fewer than 2^24 of them.
  */
 typedef struct igc_qk_part {
     int64_t batch, tokens, heads;
