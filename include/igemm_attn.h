@@ -115,9 +115,9 @@ size_t cross_attn_fwd_workspace_bytes(const igc_cross_attn* args);
  *          workspace of this call
  * ds and p are rounded to the element type before their products, which
  * accumulate in fp32 (for fp16 scaled by powers of two that keep them in
- * range).  Sums are taken in a fixed order.  Limits as the forward.  dq, dk
- * and dv may interleave in one buffer, provided no element belongs to two of
- * them.
+ * range).  Sums are taken in a fixed order.  Limits as the forward, and batch *
+ * kv_heads times the tiles of 128 keys below 2^23.  dq, dk and dv may
+ * interleave in one buffer, provided no element belongs to two of them.
  */
 typedef struct igc_cross_attn_grad {
     igc_cross_attn fwd;
