@@ -178,6 +178,13 @@ def _load(path):
     for name in ("cross_attn_fwd_workspace_bytes", "cross_attn_bwd_workspace_bytes",
                  "qk_norm_rope_bwd_workspace_bytes"):
         getattr(L, name).argtypes, getattr(L, name).restype = [buf], sz
+    # the packed argument structs of include/igemm_decoder.h
+    for name in ("layer_norm_fwd", "layer_norm_bwd"):
+        getattr(L, name).argtypes, getattr(L, name).restype = [buf, vp], i32
+        check = getattr(L, name + "_check")
+        check.argtypes, check.restype = [buf], i32
+    for name in ("layer_norm_bwd_workspace_bytes",):
+        getattr(L, name).argtypes, getattr(L, name).restype = [buf], sz
     _libs[path] = L
     return L
 
@@ -836,3 +843,8 @@ from .attention import (  # noqa: E402,F401
     cross_attn_fwd_workspace_bytes,
     qk_norm_rope, qk_norm_rope_bwd, qk_norm_rope_bwd_check, qk_norm_rope_fwd,
     qk_norm_rope_fwd_check, rope_table, rope_table_2d)
+
+# ------------------------------------------- operators around the attention
+from .decoder import (  # noqa: E402,F401
+    layer_norm, layer_norm_bwd, layer_norm_bwd_check, layer_norm_bwd_workspace_bytes,
+    layer_norm_fwd, layer_norm_fwd_check, layer_norm_grad)

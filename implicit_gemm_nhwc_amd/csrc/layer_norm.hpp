@@ -1,0 +1,305 @@
+// Layer norm over the channels, and its gradient.
+//
+// A row is the C channels of one pixel or token.  mean = sum x / C,
+// r = (sum (x - mean)^2 / C + eps)^-1/2, xh = (x - mean) r, y = xh w + b.  The
+// gradient, with u = dy w:  dx = r (u - mean(u) - xh mean(u xh)),
+// dw = sum over rows of dy xh,  db = sum dy.
+//
+// Both are bound by HBM: a row stays in the registers of its LPR lanes (NC
+// chunks of 8 values a lane), so that the variance is taken about the mean
+// (no cancellation), the gradient needs no statistics of the forward pass, and
+// each value is read and written once.
+#pragma once
+
+#include "attn_common.hpp"
+
+namespace igc {
+
+struct LnArgs {
+    const uint8_t* x;
+    const uint8_t* dy;
+    uint8_t* out;          // y forward, dx backward
+    const float *w, *b;    // [C] or null
+    float *dw, *db;        // [C] or null
+    float* partial;        // backward: [blocks][2][C]
+    int64_t x_s[3], g_s[3], o_s[3];   // row strides of the three leading axes, bytes
+    int n1, n2;            // the inner two leading axes
+    int flat;              // one stride (index 2) reaches every row
+    int rows, C;
+    int blocks;            // backward
+    float eps, inv_c;
+};
+
+typedef uint32_t u32x4h __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4w __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ int64_t ln_row(const LnArgs& a, const int64_t* s, int row) {
+    if (a.flat) return row * s[2];
+    const int i01 = row / a.n2, i0 = i01 / a.n1;
+    return i0 * s[0] + (i01 - i0 * a.n1) * s[1] + (row - i01 * a.n2) * s[2];
+}
+
+// 8 values from p (2-byte aligned), `left` of them in the row; zeros past it.
+template <int DT>
+__device__ __forceinline__ u32x4 ln_load(const uint8_t* p, int left) {
+    if (left >= 8) return u32x4(*reinterpret_cast<const u32x4h*>(p));
+    u32x4 r = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+        if (j < left)
+            r[j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + 2 * j) << (16 * (j & 1));
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ void ln_store(uint8_t* p, int left, const float* v) {
+    const u32x4 r = pack8<DT>(v);
+    if (left >= 8) {
+        *reinterpret_cast<u32x4h*>(p) = r;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+        if (j < left)
+            *reinterpret_cast<uint16_t*>(p + 2 * j) = (uint16_t)(r[j / 2] >> (16 * (j & 1)));
+}
+// 8 of the C values of w from c on (`none` without w and past the end).
+__device__ __forceinline__ void ln_weights(const float* w, int c, int C, float none, float* v) {
+    if (w && c + 8 <= C) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const f32x4w x = *reinterpret_cast<const f32x4w*>(w + c + 4 * k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * k + j] = x[j];
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = w && c + j < C ? w[c + j] : none;
+}
+
+// Sums over the lanes of a row.  Rows of more than a wave add the waves' sums
+// in order through LDS; consecutive sums use the two slots in turn, so that
+// one barrier each is enough.
+template <int LPR>
+struct RowSum {
+    static constexpr int NW = LPR > 64 ? LPR / 64 : 1;
+    float* lds;   // [2][2][NW]
+    int slot = 0;
+    __device__ __forceinline__ void add(float& x) {
+        float y = 0.0f;
+        add<1>(x, y);
+    }
+    template <int N = 2>
+    __device__ __forceinline__ void add(float& x, float& y) {
+#pragma unroll
+        for (int o = 1; o < (LPR < 64 ? LPR : 64); o <<= 1) {
+            x += __shfl_xor(x, o, 64);
+            if constexpr (N > 1) y += __shfl_xor(y, o, 64);
+        }
+        if constexpr (LPR > 64) {
+            float* s = lds + slot * 2 * NW;
+            slot ^= 1;
+            const int wave = threadIdx.x >> 6;
+            if ((threadIdx.x & 63) == 0) {
+                s[wave] = x;
+                if constexpr (N > 1) s[NW + wave] = y;
+            }
+            __syncthreads();
+            x = s[0];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) x += s[w];
+            if constexpr (N > 1) {
+                y = s[NW];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) y += s[NW + w];
+            }
+        }
+    }
+};
+
+// v -> v - mean (zeros past the row); returns r.
+template <int LPR, int NC>
+__device__ __forceinline__ float ln_stats(RowSum<LPR>& sum, float (&v)[NC][8], int c0, int C,
+                                          float inv_c, float eps) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        float t = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t += v[i][j];
+        s += t;
+    }
+    sum.add(s);
+    // divided, not times the rounded 1 / C: a constant row gives zeros
+    const float mean = s / (float)C;
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int left = C - (c0 + i * LPR * 8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[i][j] = j < left ? v[i][j] - mean : 0.0f;
+            q = __builtin_fmaf(v[i][j], v[i][j], q);
+        }
+    }
+    sum.add(q);
+    return 1.0f / sqrtf(__builtin_fmaf(q, inv_c, eps));
+}
+
+template <int DT, int LPR, int NC, int NT>
+__global__ __launch_bounds__(NT) void layer_norm_fwd_kernel(LnArgs a) {
+    __shared__ __attribute__((aligned(16))) float red[4 * RowSum<LPR>::NW];
+    lds_poison<NT>(reinterpret_cast<uint8_t*>(red), sizeof(red));
+    RowSum<LPR> sum{red};
+    const int c0 = (int)(threadIdx.x % LPR) * 8;
+    const int row = (int)(blockIdx.x * (NT / LPR) + threadIdx.x / LPR);
+    const bool live = row < a.rows;   // rows of more than a wave always are
+    const uint8_t* x = a.x + (live ? ln_row(a, a.x_s, row) : 0);
+    float v[NC][8];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = c0 + i * LPR * 8;
+        unpack8<DT>(ln_load<DT>(x + 2 * c, live ? a.C - c : 0), v[i]);
+    }
+    const float r = ln_stats<LPR, NC>(sum, v, c0, a.C, a.inv_c, a.eps);
+    if (!live) return;
+    uint8_t* y = a.out + ln_row(a, a.o_s, row);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = c0 + i * LPR * 8;
+        float w[8], b[8];
+        ln_weights(a.w, c, a.C, 1.0f, w);
+        ln_weights(a.b, c, a.C, 0.0f, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j] * r, w[j], b[j]);
+        ln_store<DT>(y + 2 * c, a.C - c, v[i]);
+    }
+}
+
+// Workgroups walk the rows, so that the partial gradients of the weights stay
+// few; every lane of a workgroup runs the same number of rounds.
+template <int DT, int LPR, int NC, int NT>
+__global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(LnArgs a) {
+    constexpr int PER = NT / LPR;
+    constexpr int W = LPR * NC * 8;   // channels of a row, rounded up
+    __shared__ __attribute__((aligned(16))) float red[PER > 1 ? PER * W : 4 * RowSum<LPR>::NW];
+    lds_poison<NT>(reinterpret_cast<uint8_t*>(red), sizeof(red));
+    RowSum<LPR> sum{red};
+    const int c0 = (int)(threadIdx.x % LPR) * 8;
+    float w[NC][8], dw[NC][8], db[NC][8];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        ln_weights(a.w, c0 + i * LPR * 8, a.C, 1.0f, w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
+    }
+    const int rounds = (int)(((int64_t)a.rows + (int64_t)a.blocks * PER - 1) /
+                             ((int64_t)a.blocks * PER));
+    for (int k = 0; k < rounds; ++k) {
+        const int64_t at = ((int64_t)k * a.blocks + blockIdx.x) * PER + threadIdx.x / LPR;
+        const bool live = at < a.rows;
+        const int row = live ? (int)at : 0;
+        const uint8_t* x = a.x + ln_row(a, a.x_s, row);
+        const uint8_t* g = a.dy + ln_row(a, a.g_s, row);
+        u32x4 rx[NC], rg[NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = c0 + i * LPR * 8, left = live ? a.C - c : 0;
+            rx[i] = ln_load<DT>(x + 2 * c, left);
+            rg[i] = ln_load<DT>(g + 2 * c, left);
+        }
+        float v[NC][8];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) unpack8<DT>(rx[i], v[i]);
+        float r = ln_stats<LPR, NC>(sum, v, c0, a.C, a.inv_c, a.eps);
+        if (!live) r = 0.0f;   // eps = 0 gives infinity there
+        float s = 0.0f, q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            float u[8];
+            unpack8<DT>(rg[i], u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[i][j] *= r;   // xh
+                // rows past the last hold zeros in u
+                dw[i][j] = __builtin_fmaf(u[j], v[i][j], dw[i][j]);
+                db[i][j] += u[j];
+                const float t = u[j] * w[i][j];
+                s += t;
+                q = __builtin_fmaf(t, v[i][j], q);
+            }
+        }
+        sum.add(s, q);
+        s *= a.inv_c;
+        q *= a.inv_c;
+        if (live) {
+            uint8_t* dx = a.out + ln_row(a, a.o_s, row);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = c0 + i * LPR * 8;
+                float u[8];
+                unpack8<DT>(rg[i], u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    u[j] = r * (__builtin_fmaf(u[j], w[i][j], -s) - v[i][j] * q);
+                ln_store<DT>(dx + 2 * c, a.C - c, u);
+            }
+        }
+    }
+    if (!a.partial) return;
+    // the workgroup's sums, row groups in order
+    float* dst = a.partial + (int64_t)blockIdx.x * 2 * a.C;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        if constexpr (PER > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    red[(threadIdx.x / LPR) * W + c0 + i * LPR * 8 + j] = p ? db[i][j] : dw[i][j];
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.C; c += NT) {
+                float s = 0.0f;
+#pragma unroll
+                for (int g = 0; g < PER; ++g) s += red[g * W + c];
+                dst[p * a.C + c] = s;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = c0 + i * LPR * 8 + j;
+                    if (c < a.C) dst[p * a.C + c] = p ? db[i][j] : dw[i][j];
+                }
+        }
+    }
+}
+
+// Sum of the workgroups' partial gradients of weight and bias in a fixed
+// order: a workgroup takes 16 of the 2 C values, 64 groups of 16 lanes every
+// 64th partial, and the groups' sums are added as a tree.
+template <int DT>
+__global__ __launch_bounds__(1024) void layer_norm_dw_kernel(LnArgs a) {
+    __shared__ __attribute__((aligned(16))) float sum[64][17];
+    lds_poison<1024>(reinterpret_cast<uint8_t*>(sum), sizeof(sum));
+    const int x = threadIdx.x & 15, g = threadIdx.x >> 4;
+    const int c = (int)blockIdx.x * 16 + x, n = 2 * a.C;
+    float s = 0.0f;
+    if (c < n) {
+#pragma unroll 8
+        for (int i = g; i < a.blocks; i += 64) s += a.partial[(int64_t)i * n + c];
+    }
+    sum[g][x] = s;
+    for (int k = 32; k; k >>= 1) {
+        __syncthreads();
+        if (g < k) sum[g][x] += sum[g + k][x];
+    }
+    if (g == 0 && c < n) {
+        float* dst = c < a.C ? a.dw : a.db;
+        if (dst) dst[c < a.C ? c : c - a.C] = sum[0][x];
+    }
+}
+
+}  // namespace igc
