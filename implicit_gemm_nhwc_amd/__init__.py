@@ -179,11 +179,12 @@ def _load(path):
                  "qk_norm_rope_bwd_workspace_bytes"):
         getattr(L, name).argtypes, getattr(L, name).restype = [buf], sz
     # the packed argument structs of include/igemm_decoder.h
-    for name in ("layer_norm_fwd", "layer_norm_bwd"):
+    for name in ("layer_norm_fwd", "layer_norm_bwd", "quantize_rows", "kv_cache_write",
+                 "kv_cache_read", "cache_attn_fwd"):
         getattr(L, name).argtypes, getattr(L, name).restype = [buf, vp], i32
         check = getattr(L, name + "_check")
         check.argtypes, check.restype = [buf], i32
-    for name in ("layer_norm_bwd_workspace_bytes",):
+    for name in ("layer_norm_bwd_workspace_bytes", "cache_attn_fwd_workspace_bytes"):
         getattr(L, name).argtypes, getattr(L, name).restype = [buf], sz
     _libs[path] = L
     return L
@@ -846,5 +847,7 @@ from .attention import (  # noqa: E402,F401
 
 # ------------------------------------------- operators around the attention
 from .decoder import (  # noqa: E402,F401
+    KVCache, cache_attention, cache_attn_fwd, cache_attn_fwd_check,
+    cache_attn_fwd_workspace_bytes, kv_cache_read, kv_cache_write, kv_cache_write_check,
     layer_norm, layer_norm_bwd, layer_norm_bwd_check, layer_norm_bwd_workspace_bytes,
-    layer_norm_fwd, layer_norm_fwd_check, layer_norm_grad)
+    layer_norm_fwd, layer_norm_fwd_check, layer_norm_grad, quantize_rows)

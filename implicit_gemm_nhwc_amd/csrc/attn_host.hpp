@@ -38,6 +38,17 @@ constexpr int kTokenStep = 32 * kTokenWaves;   // keys a round of its waves
 // D rounded up to the tile widths the kernels are built for.
 inline int padded_dim(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 96 ? 96 : 128; }
 
+// The multiplier of div_g.
+inline void set_group_divisor(AttnArgs* a) {
+    if (a->G > 1) {
+        // row / G = mulhi(row, ceil(2^(31 + L) / G)) >> (L - 1), L = ceil(log2 G)
+        int L = 0;
+        while (((int64_t)1 << L) < a->G) ++L;
+        a->g_mul = (uint32_t)((((uint64_t)1 << (31 + L)) + a->G - 1) / a->G);
+        a->g_shift = L - 1;
+    }
+}
+
 template <int DT>
 hipError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, hipStream_t stream);
 template <int DT>

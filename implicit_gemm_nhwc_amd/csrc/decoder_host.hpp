@@ -2,8 +2,12 @@
 // translation units: per-type launchers and the rules that pick a kernel form.
 #pragma once
 
+#include "attn_host.hpp"
+#include "cache_attn.hpp"
 #include "igemm_host.hpp"
+#include "kv_cache.hpp"
 #include "layer_norm.hpp"
+#include "rows_i8.hpp"
 
 namespace igc {
 
@@ -28,5 +32,22 @@ constexpr LnForm ln_form(int c) {
 
 template <int DT>
 hipError_t launch_layer_norm(const LnArgs& a, bool backward, hipStream_t stream);
+
+constexpr int kQuantMaxChannels = 131071;
+
+// Rows in 8 bits take the norm's forms; longer rows go through the last one in
+// pieces.
+template <int DT>
+hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t stream);
+
+template <int DT>
+hipError_t launch_kv_cache(const CacheArgs& a, bool write, hipStream_t stream);
+
+// Workgroups of the attention over the cache that split launches aim at, a CU.
+constexpr int kCacheFill = 2;
+
+// groups: workgroups of the launch.
+template <int DT>
+hipError_t launch_cache_attn(const CacheAttnArgs& a, unsigned groups, hipStream_t stream);
 
 }  // namespace igc

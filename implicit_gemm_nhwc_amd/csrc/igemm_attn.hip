@@ -205,13 +205,7 @@ AttnArgs attn_args(const igc_cross_attn* p, const AttnTensors& t) {
     a.rows = a.Hq ? a.Tq * a.G : 0;
     a.scale = (float)p->scale;
     a.c = scale_log2(p);
-    if (a.G > 1) {
-        // row / G = mulhi(row, ceil(2^(31 + L) / G)) >> (L - 1), L = ceil(log2 G)
-        int L = 0;
-        while (((int64_t)1 << L) < a.G) ++L;
-        a.g_mul = (uint32_t)((((uint64_t)1 << (31 + L)) + a.G - 1) / a.G);
-        a.g_shift = L - 1;
-    }
+    set_group_divisor(&a);
     return a;
 }
 

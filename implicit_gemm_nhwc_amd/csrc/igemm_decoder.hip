@@ -1,7 +1,7 @@
 // C-ABI entry points of the decoder block's operators (declarations and
 // contracts in include/igemm_decoder.h): the host gates, the launch plans and
 // the workspaces.  Every step of the computation runs in the kernels of
-// layer_norm.hpp.
+// layer_norm.hpp, rows_i8.hpp, kv_cache.hpp and cache_attn.hpp.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -227,9 +227,361 @@ int32_t run_ln(const igc_layer_norm* p, bool backward, void* stream) {
     return finish(e, w, st);
 }
 
+// ------------------------------------------------------------ rows in 8 bits
+int32_t check_quant(const igc_quantize_rows* p, Rows* x, Rows* q) {
+    if (!p) return IGC_DECLINE_NULL_POINTER;
+    if (p->dtype != IGC_DTYPE_BF16 && p->dtype != IGC_DTYPE_FP16) return IGC_DECLINE_DTYPE;
+    for (int64_t n : p->n) {
+        if (n < 0) return IGC_DECLINE_SHAPE;
+        if (n >= kLim31) return IGC_DECLINE_SIZE_LIMIT;
+    }
+    if (p->channels < 1) return IGC_DECLINE_SHAPE;
+    if (p->channels > kQuantMaxChannels) return IGC_DECLINE_SIZE_LIMIT;
+    const int64_t n01 = p->n[0] * p->n[1];
+    if (p->n[2] && (n01 >= kLim31 || n01 * p->n[2] >= kLim31)) return IGC_DECLINE_SIZE_LIMIT;
+    const int64_t rows = n01 * p->n[2];
+    const LnForm f = ln_form((int)p->channels);
+    if (!launchable(ceil_div(rows, f.threads / f.lanes), f.threads)) return IGC_DECLINE_SIZE_LIMIT;
+    int32_t r;
+    if ((r = check_rows(p->x, p->n, p->channels, 2, 2, false, x))) return r;
+    if ((r = check_rows(p->q, p->n, p->channels, 1, 16, true, q))) return r;
+    if (rows == 0) return IGC_OK;
+    if (!p->scale) return IGC_DECLINE_NULL_POINTER;
+    if (!aligned(p->scale, 4)) return IGC_DECLINE_ALIGNMENT;
+    const size_t sb = (size_t)rows * 4;
+    if (meet(q->p, q->bytes, x->p, x->bytes) || meet(p->scale, sb, x->p, x->bytes) ||
+        meet(p->scale, sb, q->p, q->bytes))
+        return IGC_DECLINE_OVERLAP;
+    return IGC_OK;
+}
+
+// ------------------------------------------------------------ the cache
+int64_t cache_pitch(const igc_kv_cache& c) { return ceil_div(c.head_dim, 16) * 16; }
+int64_t cache_rows(const igc_kv_cache& c) { return c.pages * c.kv_heads * c.page_tokens; }
+
+int32_t check_cache(const igc_kv_cache& c) {
+    if (c.pages < 0 || c.kv_heads < 0) return IGC_DECLINE_SHAPE;
+    if (c.page_tokens < 16 || c.page_tokens > 1024 || log2_exact(c.page_tokens) < 0)
+        return IGC_DECLINE_SHAPE;
+    if (c.head_dim < 8 || c.head_dim > 128 || c.head_dim % 8) return IGC_DECLINE_HEAD_DIM;
+    if (c.pages >= kLim31 || c.kv_heads >= kLim31 ||
+        (c.kv_heads && c.pages > ((int64_t)1 << 40) / (c.kv_heads * c.page_tokens)))
+        return IGC_DECLINE_SIZE_LIMIT;
+    if (cache_rows(c) == 0) return IGC_OK;
+    if (!c.k || !c.v || !c.k_scale || !c.v_scale) return IGC_DECLINE_NULL_POINTER;
+    if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.k_scale, 16) ||
+        !aligned(c.v_scale, 16))
+        return IGC_DECLINE_ALIGNMENT;
+    const size_t kb = (size_t)(cache_rows(c) * cache_pitch(c)), sb = (size_t)cache_rows(c) * 4;
+    const struct { const void* p; size_t n; } part[4] = {
+        {c.k, kb}, {c.v, kb}, {c.k_scale, sb}, {c.v_scale, sb}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (meet(part[i].p, part[i].n, part[j].p, part[j].n)) return IGC_DECLINE_OVERLAP;
+    return IGC_OK;
+}
+
+bool meets_cache(const igc_kv_cache& c, const void* w, size_t n) {
+    const size_t kb = (size_t)(cache_rows(c) * cache_pitch(c)), sb = (size_t)cache_rows(c) * 4;
+    return meet(w, n, c.k, kb) || meet(w, n, c.v, kb) || meet(w, n, c.k_scale, sb) ||
+           meet(w, n, c.v_scale, sb);
+}
+
+// Gate of a table of `batch` rows; its bytes.
+int32_t check_table(const int32_t* table, int64_t batch, int64_t stride, int64_t entries,
+                    size_t* bytes) {
+    *bytes = 0;
+    if (entries < 0) return IGC_DECLINE_SHAPE;
+    if (entries >= kLim31) return IGC_DECLINE_SIZE_LIMIT;
+    if (batch == 0 || entries == 0) return IGC_OK;
+    if (!table) return IGC_DECLINE_NULL_POINTER;
+    if (!aligned(table, 4)) return IGC_DECLINE_ALIGNMENT;
+    if (stride < 0 || stride >= kBatchStrideLim) return IGC_DECLINE_STRIDE;
+    if ((double)(batch - 1) * (double)stride > kExtentLim) return IGC_DECLINE_SIZE_LIMIT;
+    *bytes = (size_t)((batch - 1) * stride + entries) * 4;
+    return IGC_OK;
+}
+
+// Lane groups that a launch of kv_cache_write / read takes for keys or values.
+int64_t io_items(const igc_kv_io* p) {
+    return p->batch * p->tokens * ceil_div(p->cache.kv_heads, kCacheHeads);
+}
+
+int32_t check_io(const igc_kv_io* p, bool write, Tensor t[2]) {
+    if (!p) return IGC_DECLINE_NULL_POINTER;
+    if (p->dtype != IGC_DTYPE_BF16 && p->dtype != IGC_DTYPE_FP16) return IGC_DECLINE_DTYPE;
+    if (p->batch < 0 || p->tokens < 0) return IGC_DECLINE_SHAPE;
+    int32_t r;
+    if ((r = check_cache(p->cache))) return r;
+    if (p->batch >= kLim31 || p->tokens >= kLim31) return IGC_DECLINE_SIZE_LIMIT;
+    const igc_kv_cache& c = p->cache;
+    const int64_t hc = ceil_div(c.kv_heads, kCacheHeads);
+    if (hc && p->batch * p->tokens > ((int64_t)1 << 40) / hc) return IGC_DECLINE_SIZE_LIMIT;
+    const int64_t per = kCacheThreads / qk_lanes((int)c.head_dim);
+    if (!launchable(2 * ceil_div(io_items(p), per), kCacheThreads)) return IGC_DECLINE_SIZE_LIMIT;
+    const igc_attn_view* v[2] = {&p->k, &p->v};
+    for (int i = 0; i < 2; ++i)
+        if ((r = check_view(*v[i], p->batch, p->tokens, c.kv_heads, c.head_dim, !write,
+                            kBatchStrideLim, &t[i])))
+            return r;
+    size_t tb;
+    if ((r = check_table(p->table, p->batch, p->table_stride, p->table_entries, &tb))) return r;
+    if (io_items(p) == 0) return IGC_OK;
+    if (!p->start) return IGC_DECLINE_NULL_POINTER;
+    if (!aligned(p->start, 4) || !aligned(p->lens, 4)) return IGC_DECLINE_ALIGNMENT;
+    const size_t bb = (size_t)p->batch * 4;
+    const struct { const void* p; size_t n; } small[3] = {
+        {p->table, tb}, {p->start, bb}, {p->lens, bb}};
+    for (int i = 0; i < 2; ++i)
+        if (meets_cache(c, t[i].p, t[i].bytes)) return IGC_DECLINE_OVERLAP;
+    for (const auto& s : small) {
+        if (write && meets_cache(c, s.p, s.n)) return IGC_DECLINE_OVERLAP;
+        if (!write)
+            for (int i = 0; i < 2; ++i)
+                if (meet(s.p, s.n, t[i].p, t[i].bytes)) return IGC_DECLINE_OVERLAP;
+    }
+    // the two outputs may interleave in one buffer, not meet in an element:
+    // the halves of one projection are strided views of the same rows
+    if (!write && t[0].p == t[1].p) return IGC_DECLINE_OVERLAP;
+    return IGC_OK;
+}
+
+int32_t run_io(const igc_kv_io* p, bool write, void* stream) {
+    Tensor t[2];
+    if (check_io(p, write, t) != IGC_OK) return 0;
+    if (io_items(p) == 0) return 1;
+    const igc_kv_cache& c = p->cache;
+    CacheArgs a{};
+    a.pool[0] = c.k;
+    a.pool[1] = c.v;
+    a.scale[0] = c.k_scale;
+    a.scale[1] = c.v_scale;
+    for (int i = 0; i < 2; ++i) {
+        a.t[i] = (uint8_t*)const_cast<void*>(t[i].p);
+        a.t_b[i] = t[i].b;
+        a.t_t[i] = t[i].t;
+        a.t_h[i] = t[i].h;
+    }
+    a.table = p->table;
+    a.start = p->start;
+    a.lens = p->lens;
+    a.table_stride = p->table_stride;
+    a.B = (int)p->batch;
+    a.T = (int)p->tokens;
+    a.H = (int)c.kv_heads;
+    a.D = (int)c.head_dim;
+    a.Dp = (int)cache_pitch(c);
+    a.hc = (int)ceil_div(c.kv_heads, kCacheHeads);
+    a.items = io_items(p);
+    a.entries = (int)p->table_entries;
+    a.pages = (int)c.pages;
+    a.shift = log2_exact(c.page_tokens);
+    const hipStream_t st = (hipStream_t)stream;
+    const hipError_t e = p->dtype == IGC_DTYPE_BF16 ? launch_kv_cache<DT_BF16>(a, write, st)
+                                                    : launch_kv_cache<DT_FP16>(a, write, st);
+    return e == hipSuccess ? 1 : -(int32_t)e;
+}
+
+// ------------------------------------------------------------ attention over it
+struct CacheAttnPlan {
+    int64_t row_tiles, slots, groups;   // slots of cache_plan.hpp; workgroups
+    int64_t capacity;
+    bool split;
+    int64_t part_floats, stat_floats;
+};
+
+// The attention arguments whose gates are cross attention's.
+int32_t check_cache_attn_shape(const igc_cache_attn* p) {
+    if (!p) return IGC_DECLINE_NULL_POINTER;
+    if (p->dtype != IGC_DTYPE_BF16 && p->dtype != IGC_DTYPE_FP16) return IGC_DECLINE_DTYPE;
+    if (p->batch < 0 || p->q_len < 0 || p->q_heads < 0 || p->table_entries < 0)
+        return IGC_DECLINE_SHAPE;
+    const igc_kv_cache& c = p->cache;
+    if (c.kv_heads < 0 || c.page_tokens < 16 || c.page_tokens > 1024) return IGC_DECLINE_SHAPE;
+    if (p->q_heads > 0 && (c.kv_heads == 0 || p->q_heads % c.kv_heads)) return IGC_DECLINE_GROUPS;
+    if (c.head_dim < 8 || c.head_dim > 128 || c.head_dim % 8) return IGC_DECLINE_HEAD_DIM;
+    const float c2 = (float)(p->scale * 1.4426950408889634);
+    if (!(p->scale > 0.0) || (float)p->scale < 1e-30f || !isfinite(c2)) return IGC_DECLINE_SCALE;
+    if (p->batch >= kLim31 || p->q_len >= kLim31 || p->q_heads >= kLim31 ||
+        c.kv_heads >= kLim31 || p->table_entries >= kLim31)
+        return IGC_DECLINE_SIZE_LIMIT;
+    const int64_t g = c.kv_heads ? p->q_heads / c.kv_heads : 1;
+    if ((g && p->q_len >= kLim31 / 4 / g) || p->batch * p->q_heads >= kLim31 ||
+        p->table_entries * c.page_tokens >= kLim31 - 4096)
+        return IGC_DECLINE_SIZE_LIMIT;
+    return IGC_OK;
+}
+
+CacheAttnPlan cache_attn_plan(const igc_cache_attn* p) {
+    CacheAttnPlan x{};
+    const igc_kv_cache& c = p->cache;
+    const int64_t rows = c.kv_heads ? p->q_len * (p->q_heads / c.kv_heads) : 0;
+    x.row_tiles = ceil_div(rows, 32);
+    x.capacity = p->table_entries * c.page_tokens;
+    const int64_t hr = c.kv_heads * x.row_tiles;
+    x.slots = hr ? kCacheFill * kNumCUs / hr : 0;
+    x.split = cache_splits(x.slots, p->batch) && x.capacity > 4 * kCacheUnit;
+    if (!x.split) x.slots = p->batch;
+    x.groups = hr * (x.split ? cache_slots_bound(x.slots, p->batch, x.capacity) : p->batch);
+    if (x.split) {
+        const int64_t n = x.groups * (rows < 32 ? rows : 32);
+        x.part_floats = n * c.head_dim;
+        x.stat_floats = n * 2;
+    }
+    return x;
+}
+
+size_t cache_attn_ws(const CacheAttnPlan& x) {
+    return (size_t)(x.part_floats + x.stat_floats) * sizeof(float);
+}
+
+int32_t check_cache_attn(const igc_cache_attn* p, Tensor* q, Tensor* o, CacheAttnPlan* plan) {
+    int32_t r;
+    if ((r = check_cache_attn_shape(p))) return r;
+    if ((r = check_cache(p->cache))) return r;
+    const igc_kv_cache& c = p->cache;
+    if ((r = check_view(p->q, p->batch, p->q_len, p->q_heads, c.head_dim, false, kStrideLim, q)))
+        return r;
+    if ((r = check_view(p->out, p->batch, p->q_len, p->q_heads, c.head_dim, true, kStrideLim, o)))
+        return r;
+    const int64_t g = c.kv_heads ? p->q_heads / c.kv_heads : 1;
+    for (const Tensor* x : {q, o})
+        if (33 * x->t + g * x->h >= kLim31) return IGC_DECLINE_SIZE_LIMIT;
+    size_t tb;
+    if ((r = check_table(p->table, p->batch, p->table_stride, p->table_entries, &tb))) return r;
+    if (p->batch && p->q_len && p->q_heads && !p->lens) return IGC_DECLINE_NULL_POINTER;
+    if (!aligned(p->lens, 4) || !aligned(p->lse, 4)) return IGC_DECLINE_ALIGNMENT;
+    *plan = cache_attn_plan(p);
+    if (!launchable(plan->groups, kCacheWaves * 64) ||
+        p->batch * c.kv_heads * plan->row_tiles >= kLim31 / 256)
+        return IGC_DECLINE_SIZE_LIMIT;
+    const size_t lb = (size_t)(p->batch * p->q_heads * p->q_len) * 4, bb = (size_t)p->batch * 4;
+    const size_t ws = cache_attn_ws(*plan);
+    const struct { const void* p; size_t n; } outs[3] = {
+        {o->p, o->bytes}, {p->lse, lb}, {p->workspace, p->workspace ? ws : 0}};
+    for (int i = 0; i < 3; ++i) {
+        if (meet(outs[i].p, outs[i].n, q->p, q->bytes) || meet(outs[i].p, outs[i].n, p->table, tb) ||
+            meet(outs[i].p, outs[i].n, p->lens, bb) || meets_cache(c, outs[i].p, outs[i].n))
+            return IGC_DECLINE_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (meet(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return IGC_DECLINE_OVERLAP;
+    }
+    return check_workspace(p->workspace, p->workspace_bytes, ws);
+}
+
 }  // namespace
 
 extern "C" {
+
+int32_t quantize_rows_check(const igc_quantize_rows* args) {
+    Rows x, q;
+    return check_quant(args, &x, &q);
+}
+
+int32_t quantize_rows(const igc_quantize_rows* args, void* stream) {
+    Rows x, q;
+    if (check_quant(args, &x, &q) != IGC_OK) return 0;
+    QuantArgs a{};
+    a.rows = (int)(args->n[0] * args->n[1] * args->n[2]);
+    if (a.rows == 0) return 1;
+    const Rows* both[2] = {&x, &q};
+    a.flat = one_stride(args->n, both, 2);
+    for (int k = 0; k < 3; ++k) {
+        a.x_s[k] = x.s[k];
+        a.q_s[k] = q.s[k];
+    }
+    if (a.flat) {
+        a.x_s[2] = flat_stride(args->n, x);
+        a.q_s[2] = flat_stride(args->n, q);
+    }
+    a.x = (const uint8_t*)x.p;
+    a.q = (uint8_t*)const_cast<void*>(q.p);
+    a.scale = args->scale;
+    a.n1 = (int)args->n[1];
+    a.n2 = (int)args->n[2];
+    a.C = (int)args->channels;
+    const hipStream_t st = (hipStream_t)stream;
+    const hipError_t e = args->dtype == IGC_DTYPE_BF16 ? launch_quantize_rows<DT_BF16>(a, st)
+                                                       : launch_quantize_rows<DT_FP16>(a, st);
+    return e == hipSuccess ? 1 : -(int32_t)e;
+}
+
+int32_t kv_cache_write_check(const igc_kv_io* args) {
+    Tensor t[2];
+    return check_io(args, true, t);
+}
+
+int32_t kv_cache_read_check(const igc_kv_io* args) {
+    Tensor t[2];
+    return check_io(args, false, t);
+}
+
+int32_t kv_cache_write(const igc_kv_io* args, void* stream) { return run_io(args, true, stream); }
+
+int32_t kv_cache_read(const igc_kv_io* args, void* stream) { return run_io(args, false, stream); }
+
+int32_t cache_attn_fwd_check(const igc_cache_attn* args) {
+    Tensor q, o;
+    CacheAttnPlan plan;
+    return check_cache_attn(args, &q, &o, &plan);
+}
+
+size_t cache_attn_fwd_workspace_bytes(const igc_cache_attn* args) {
+    if (check_cache_attn_shape(args) != IGC_OK) return 0;
+    return cache_attn_ws(cache_attn_plan(args));
+}
+
+int32_t cache_attn_fwd(const igc_cache_attn* args, void* stream) {
+    Tensor q, o;
+    CacheAttnPlan plan;
+    if (check_cache_attn(args, &q, &o, &plan) != IGC_OK) return 0;
+    if (args->batch == 0 || args->q_len == 0 || args->q_heads == 0) return 1;
+    const igc_kv_cache& c = args->cache;
+    CacheAttnArgs x{};
+    AttnArgs& a = x.a;
+    a.q = (const uint8_t*)q.p;
+    a.out = (uint8_t*)const_cast<void*>(o.p);
+    a.q_b = q.b; a.q_t = q.t; a.q_h = q.h;
+    a.o_b = o.b; a.o_t = o.t; a.o_h = o.h;
+    a.lse = args->lse;
+    a.B = (int)args->batch;
+    a.Tq = (int)args->q_len;
+    a.Hq = (int)args->q_heads;
+    a.Hk = (int)c.kv_heads;
+    a.G = a.Hq / a.Hk;
+    a.D = (int)c.head_dim;
+    a.rows = a.Tq * a.G;
+    a.row_tiles = (int)plan.row_tiles;
+    a.scale = (float)args->scale;
+    a.c = (float)(args->scale * 1.4426950408889634);
+    set_group_divisor(&a);
+    x.pool[0] = c.k;
+    x.pool[1] = c.v;
+    x.scales[0] = c.k_scale;
+    x.scales[1] = c.v_scale;
+    x.table = args->table;
+    x.lens = args->lens;
+    x.table_stride = args->table_stride;
+    // a pool without rows is read nowhere
+    x.capacity = cache_rows(c) ? plan.capacity : 0;
+    x.slots = plan.slots;
+    x.entries = (int)args->table_entries;
+    x.pages = (int)c.pages;
+    x.shift = log2_exact(c.page_tokens);
+    x.Dp = (int)cache_pitch(c);
+    x.causal = args->causal != 0;
+    x.split = plan.split;
+    const hipStream_t st = (hipStream_t)stream;
+    Workspace w;
+    hipError_t e = w.take(args->workspace, cache_attn_ws(plan), st);
+    if (e != hipSuccess) return -(int32_t)e;
+    a.part = (float*)w.p;
+    a.stat = a.part + plan.part_floats;
+    e = args->dtype == IGC_DTYPE_BF16
+            ? launch_cache_attn<DT_BF16>(x, (unsigned)plan.groups, st)
+            : launch_cache_attn<DT_FP16>(x, (unsigned)plan.groups, st);
+    return finish(e, w, st);
+}
 
 int32_t layer_norm_fwd_check(const igc_layer_norm* args) {
     LnTensors t;

@@ -1,5 +1,6 @@
 """Binding of the decoder block's operators of include/igemm_decoder.h: layer
-norm with its gradient.
+norm with its gradient, rows in 8 bits, the paged cache of keys and values in 8
+bits, and the attention of new tokens over it.
 
 Argument marshalling only, as in the package's other calls: every step runs in
 the HIP kernels of libigemmconv.so, and there is no fallback.  InvalidArgument
@@ -9,20 +10,27 @@ training program calls the backward entries itself (or from its own
 torch.autograd.Function).
 
   layer_norm_fwd, layer_norm_fwd_check, layer_norm_grad,
-  layer_norm_bwd_check, layer_norm_bwd_workspace_bytes
+  layer_norm_bwd_check, layer_norm_bwd_workspace_bytes,
+  cache_attn_fwd, cache_attn_fwd_check, cache_attn_fwd_workspace_bytes,
+  kv_cache_write_check
 mirror the C entries (layer_norm_grad: layer_norm_bwd; 1 handled, 0 declined,
-< 0 HIP error; outputs and workspace given); layer_norm and layer_norm_bwd
-allocate their outputs and raise on failure.
+< 0 HIP error; outputs and workspace given); layer_norm, layer_norm_bwd,
+quantize_rows, kv_cache_write, kv_cache_read and cache_attention allocate their
+outputs and raise on failure.
 """
 import struct
 
 import torch
 
 from . import DTYPE_CODES, InvalidArgument, lib
-from .attention import (_current_gpu, _device, _elsewhere, _like, _on, _raise, _raw_stream,
-                        _small, _work)
+from .attention import (_current_gpu, _dense, _device, _elsewhere, _like, _on, _raise,
+                        _raw_stream, _small, _view, _work)
 
 _LN = struct.Struct("@20qdqqq")
+_QUANT = struct.Struct("@14q")
+_CACHE = struct.Struct("@8q")
+_IO = struct.Struct("@16q")        # after a cache
+_CATTN = struct.Struct("@17qdqqq")   # after a cache
 _NO_VIEW = (0, 0, 0, 0)
 _FORWARD = object()   # in place of a gradient
 
@@ -164,3 +172,257 @@ def layer_norm_bwd(dy, x, weight=None, *, eps=1e-5, stream=None):
     if rc != 1:
         _raise("layer_norm_bwd", rc, L.layer_norm_bwd_check, packed)
     return dx, dw, db
+
+
+# ------------------------------------------------------------ rows in 8 bits
+def quantize_rows(x, *, stream=None):
+    """Rows of x [..., C] (one to four axes) as integers and a scale: m = max
+    |x| of the row, scale = m / 127 in fp32, q = 127 x / m rounded to nearest,
+    ties to even.  Returns (q int8 [..., C], scale fp32 [...]); q's rows start
+    at multiples of 16 bytes, as linear_i8 reads them.  A row with an infinity
+    or a NaN has scale NaN, one below 2^-110 scale 0."""
+    device = _device(x, "x")
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return quantize_rows(x)
+    code = _element(x, "x")
+    sizes, xv = _rows("x", x, x.dtype, device)
+    c = sizes[3]
+    pitch = -(-c // 16) * 16
+    q = torch.empty((*x.shape[:-1], pitch), dtype=torch.int8, device=x.device)
+    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    packed = _QUANT.pack(*sizes, *xv, q.data_ptr(), sizes[1] * sizes[2] * pitch,
+                         sizes[2] * pitch, pitch, scale.data_ptr(), code)
+    L = lib()
+    rc = L.quantize_rows(packed, _raw_stream(device))
+    if rc != 1:
+        _raise("quantize_rows", rc, L.quantize_rows_check, packed)
+    return (q if pitch == c else q[..., :c]), scale
+
+
+# ------------------------------------------------------------------ the cache
+class KVCache:
+    """A pool of pages of keys and values in 8 bits: k, v int8 [pages,
+    kv_heads, page_tokens, D rounded up to 16] and k_scale, v_scale fp32
+    [pages, kv_heads, page_tokens], all dense.  Sequences reach it through
+    tables of page numbers, int32 [batch, entries]; who owns which page is the
+    caller's to keep."""
+
+    def __init__(self, k, v, k_scale, v_scale, head_dim):
+        device = _device(k, "k")
+        if k.dim() != 4 or k.dtype != torch.int8 or not k.is_contiguous():
+            raise InvalidArgument("k must be a dense int8 [pages, kv_heads, page_tokens, D]")
+        if k.shape[3] != -(-head_dim // 16) * 16:
+            raise InvalidArgument(f"k's rows must hold head_dim ({head_dim}) rounded up to 16 "
+                                  f"(got {tuple(k.shape)})")
+        for name, t, shape, dtype in (("v", v, k.shape, torch.int8),
+                                      ("k_scale", k_scale, k.shape[:3], torch.float32),
+                                      ("v_scale", v_scale, k.shape[:3], torch.float32)):
+            if not isinstance(t, torch.Tensor) or t.shape != shape:
+                raise InvalidArgument(f"{name} must be a tensor of shape {tuple(shape)}")
+            _small(name, t, dtype, device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.head_dim = head_dim
+        pages, heads, tokens, _ = k.shape
+        self.packed = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                  v_scale.data_ptr(), pages, tokens, heads, head_dim)
+
+    @classmethod
+    def empty(cls, pages, page_tokens, kv_heads, head_dim, *, device="cuda"):
+        """A new pool of zeros."""
+        shape = (pages, kv_heads, page_tokens)
+        rows = [torch.zeros((*shape, -(-head_dim // 16) * 16), dtype=torch.int8, device=device)
+                for _ in range(2)]
+        scales = [torch.zeros(shape, dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*rows, *scales, head_dim)
+
+    @property
+    def kv_heads(self):
+        return self.k.shape[1]
+
+
+def _pool(cache):
+    if not isinstance(cache, KVCache):
+        raise InvalidArgument("cache must be a KVCache")
+    return cache.k.get_device()
+
+
+def _page_table(table, b, device):
+    """(pointer, stride, entries) of a table of b rows."""
+    if not isinstance(table, torch.Tensor) or table.dtype is not torch.int32 or table.dim() != 2:
+        raise InvalidArgument("table must be an int32 tensor [batch, entries]")
+    if table.get_device() != device:
+        raise InvalidArgument(f"table is on {table.device}, the cache on GPU {device}")
+    if table.shape[0] != b:
+        raise InvalidArgument(f"table must have {b} rows (got {tuple(table.shape)})")
+    entries = table.shape[1]
+    if table.stride(1) != 1 and entries > 1:
+        raise InvalidArgument("table: the entries of a sequence must be adjacent")
+    return table.data_ptr(), table.stride(0), entries
+
+
+def _per_sequence(name, t, b, device, optional=False):
+    """Pointer of an int32 tensor of one number a sequence."""
+    if t is None and optional:
+        return 0
+    if not isinstance(t, torch.Tensor) or t.shape != (b,):
+        raise InvalidArgument(f"{name} must be an int32 tensor of shape {(b,)}")
+    return _small(name, t, torch.int32, device)
+
+
+def _io_pack(cache, kv, kviews, table, start, lens, dtype, device):
+    b, t = kv[:2]
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise InvalidArgument(f"dtype {dtype} is not bf16 or fp16")
+    return cache.packed + _IO.pack(b, t, *kviews, *_page_table(table, b, device),
+                                   _per_sequence("start", start, b, device),
+                                   _per_sequence("lens", lens, b, device, True),
+                                   DTYPE_CODES[dtype])
+
+
+def _write_pack(cache, k, v, table, start, lens):
+    device = _pool(cache)
+    if not isinstance(k, torch.Tensor):
+        raise InvalidArgument("k must be a tensor")
+    views = _view("k", k, k.dtype, device) + _view("v", v, k.dtype, device)
+    if k.shape != v.shape or k.shape[2] != cache.kv_heads or k.shape[3] != cache.head_dim:
+        raise InvalidArgument(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [batch, tokens, "
+                              f"{cache.kv_heads}, {cache.head_dim}]")
+    return _io_pack(cache, k.shape, views, table, start, lens, k.dtype, device), device
+
+
+def kv_cache_write_check(cache, k, v, table, start, *, lens=None) -> int:
+    """Host-only gate of kv_cache_write: 0 or a decline reason code."""
+    return lib().kv_cache_write_check(_write_pack(cache, k, v, table, start, lens)[0])
+
+
+def kv_cache_write(cache, k, v, table, start, *, lens=None, stream=None):
+    """Quantise k and v (bf16 or fp16 [batch, tokens, kv_heads, D], any
+    strides) into the cache: token i < lens[b] (int32 [batch]; None: all) of
+    sequence b goes to position start[b] + i (int32 [batch]), which is token
+    p % page_tokens of page table[b, p // page_tokens].  Positions past the
+    table and pages outside the pool are left out.  The page of a place must
+    not be written twice in one call."""
+    packed, device = _write_pack(cache, k, v, table, start, lens)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return kv_cache_write(cache, k, v, table, start, lens=lens)
+    L = lib()
+    rc = L.kv_cache_write(packed, _raw_stream(device))
+    if rc != 1:
+        _raise("kv_cache_write", rc, L.kv_cache_write_check, packed)
+
+
+def kv_cache_read(cache, table, start, tokens, *, lens=None, dtype=torch.bfloat16, stream=None):
+    """The keys and values that the cache holds at positions start[b] .. start[b]
+    + tokens - 1, as dense tensors [batch, tokens, kv_heads, D] of dtype; zeros
+    from lens[b] on, NaN where a position or page does not exist."""
+    device = _pool(cache)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return kv_cache_read(cache, table, start, tokens, lens=lens, dtype=dtype)
+    b = table.shape[0] if isinstance(table, torch.Tensor) and table.dim() else 0
+    shape = (b, tokens, cache.kv_heads, cache.head_dim)
+    if tokens < 0:
+        raise InvalidArgument(f"tokens must not be negative (got {tokens})")
+    k = torch.empty(shape, dtype=dtype, device=cache.k.device)
+    v = torch.empty_like(k)
+    packed = _io_pack(cache, shape, _dense(k, shape) + _dense(v, shape), table, start, lens,
+                      dtype, device)
+    L = lib()
+    rc = L.kv_cache_read(packed, _raw_stream(device))
+    if rc != 1:
+        _raise("kv_cache_read", rc, L.kv_cache_read_check, packed)
+    return k, v
+
+
+# ------------------------------------------------------- attention over it
+def _cattn_pack(q, cache, table, lens, out, lse, causal, scale, ws=(0, 0)):
+    """igc_cache_attn, packed.  out: a tensor to check, or the view of a new
+    one; lse: a tensor to check, a pointer or None."""
+    device = _pool(cache)
+    if not isinstance(q, torch.Tensor):
+        raise InvalidArgument("q must be a tensor")
+    code = _element(q, "q")
+    qv = _view("q", q, q.dtype, device)
+    b, tq, hq, d = q.shape
+    if d != cache.head_dim:
+        raise InvalidArgument(f"q has heads of {d}, the cache of {cache.head_dim}")
+    if not isinstance(out, tuple):
+        o, out = out, _view("out", out, q.dtype, device)
+        if o.shape != q.shape:
+            raise InvalidArgument(f"out must have q's shape {tuple(q.shape)}")
+    if isinstance(lse, torch.Tensor):
+        if lse.shape != (b, hq, tq):
+            raise InvalidArgument(f"lse must be {(b, hq, tq)} (got {tuple(lse.shape)})")
+        lse = _small("lse", lse, torch.float32, device)
+    if scale is None:
+        scale = d ** -0.5
+    return cache.packed + _CATTN.pack(
+        b, tq, hq, *qv, *out, lse or 0, *_page_table(table, b, device),
+        _per_sequence("lens", lens, b, device), 1 if causal else 0, float(scale), code, *ws)
+
+
+def cache_attn_fwd(q, cache, table, lens, out, *, lse=None, causal=True, scale=None,
+                   workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Enqueue the attention over the cache into out (and lse).  1 handled, 0
+    declined, < 0 HIP error."""
+    device = _pool(cache)
+    packed = _cattn_pack(q, cache, table, lens, out, lse, causal, scale,
+                         _work(workspace, workspace_bytes, device))
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return lib().cache_attn_fwd(packed, _raw_stream(device))
+    return lib().cache_attn_fwd(packed, _raw_stream(device))
+
+
+def cache_attn_fwd_check(q, cache, table, lens, out, *, lse=None, causal=True, scale=None,
+                         workspace=None, workspace_bytes=0) -> int:
+    """Host-only gate of cache_attn_fwd: 0 or a decline reason code."""
+    return lib().cache_attn_fwd_check(
+        _cattn_pack(q, cache, table, lens, out, lse, causal, scale,
+                    _work(workspace, workspace_bytes, _pool(cache))))
+
+
+def cache_attn_fwd_workspace_bytes(q_shape, cache, entries, dtype) -> int:
+    """Workspace of a call with a table of so many entries a sequence (0 when
+    none is needed, or when it would be declined)."""
+    b, tq, hq, _ = q_shape
+    return lib().cache_attn_fwd_workspace_bytes(
+        cache.packed + _CATTN.pack(b, tq, hq, *(0,) * 9, 0, 0, entries, 0, 0, 1.0,
+                                   DTYPE_CODES.get(dtype, -1), 0, 0))
+
+
+def cache_attention(q, cache, table, lens, *, causal=True, scale=None, return_lse=False,
+                    stream=None):
+    """Attention of new tokens q [batch, tq, hq, D] (kv_heads dividing hq) to
+    the lens[b] (int32 [batch]) tokens that sequence b holds in the cache, at
+    the places that table (int32 [batch, entries]) gives its positions.  The
+    new tokens are the last tq of them (kv_cache_write puts them there first)
+    and causal lets token i attend up to its own position only.  scale
+    defaults to 1 / sqrt(D).  A row that attends to nothing gives 0.  Returns
+    out, dense like q, and with return_lse also the fp32 statistics [batch,
+    hq, tq].  No gradients: the cache is for inference."""
+    device = _pool(cache)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return cache_attention(q, cache, table, lens, causal=causal, scale=scale,
+                                   return_lse=return_lse)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise InvalidArgument("q must be a tensor [batch, token, head, D]")
+    out = _like(q)
+    lse = None
+    if return_lse:
+        lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
+                          device=q.device)
+    packed = _cattn_pack(q, cache, table, lens, _dense(out, q.shape),
+                         None if lse is None else lse.data_ptr(), causal, scale)
+    L = lib()
+    need = L.cache_attn_fwd_workspace_bytes(packed)
+    if need:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        packed = packed[:-16] + struct.pack("@qq", ws.data_ptr(), need)
+    rc = L.cache_attn_fwd(packed, _raw_stream(device))
+    if rc != 1:
+        _raise("cache_attn_fwd", rc, L.cache_attn_fwd_check, packed)
+    return (out, lse) if return_lse else out

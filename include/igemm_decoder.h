@@ -74,6 +74,117 @@ int32_t layer_norm_bwd_check(const igc_layer_norm* args);
  * and bias (0 without them, or for sizes that would be declined). */
 size_t layer_norm_bwd_workspace_bytes(const igc_layer_norm* args);
 
+/*
+ * Rows of x in 8 bits (the definition at the top): x [n0, n1, n2, C] as in
+ * igc_layer_norm, q int8 [n0, n1, n2, C] with the strides of its view in
+ * bytes, scale fp32 [n0, n1, n2], dense.
+ * q's pointer and strides are multiples of 16 bytes; bytes between C and the
+ * next row are not written.
+ * Limits: C from 1 to 131071, fewer than 2^31 rows, launches as in
+ * igc_layer_norm (past 16384 values 512 threads a row).
+ */
+typedef struct igc_quantize_rows {
+    int64_t n[3], channels;
+    igc_attn_view x, q;
+    float* scale;
+    int64_t dtype;               /* of x */
+} igc_quantize_rows;
+
+int32_t quantize_rows(const igc_quantize_rows* args, void* stream);
+int32_t quantize_rows_check(const igc_quantize_rows* args);
+
+/*
+ * The paged cache of keys and values in 8 bits.  A pool holds `pages` pages of
+ * page_tokens tokens; k and v are int8 [pages][kv_heads][page_tokens][Dp],
+ * Dp = head_dim rounded up to 16, k_scale and v_scale fp32
+ * [pages][kv_heads][page_tokens]: one row in 8 bits (the definition at the
+ * top) a head of a token.  Sequence b's token at position p is token
+ * p % page_tokens of page table[b][p / page_tokens].  Several sequences may
+ * share pages.
+ * Limits: page_tokens 16, 32, ... 1024 (a power of two), head_dim a multiple
+ * of 8 up to 128, pools 16-byte aligned, pages and kv_heads below 2^31, at
+ * most 2^40 rows.
+ */
+typedef struct igc_kv_cache {
+    int8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t pages, page_tokens, kv_heads, head_dim;
+} igc_kv_cache;
+
+/*
+ * Writing and reading back.  Token i < min(lens[b], tokens) of sequence b has
+ * the position start[b] + i.
+ *   k, v     16-bit [batch, tokens, kv_heads, head_dim], views as in
+ *            igemm_attn.h: inputs of kv_cache_write, outputs of kv_cache_read
+ *   table    int32 rows of table_entries at table_stride elements
+ *   start    int32 [batch];  lens int32 [batch] or NULL (tokens)
+ * kv_cache_write leaves everything else of the pool as it was; tokens whose
+ * position is negative or past the table, or whose page is not one of the
+ * pool, are not written (a negative page number so leaves a page out).  A
+ * place that one call writes twice (a page shared by sequences that both
+ * write to it) holds a mix of the two rows afterwards.
+ * kv_cache_read writes all of k and v: zeros at i >= lens[b], NaN where the
+ * position or the page does not exist.
+ * Limits: batch, tokens below 2^31; a launch holds one group of 4 to 16 lanes
+ * (head_dim / 8, rounded up to a power of two) for every four heads of a
+ * token, of keys and of values, and fewer than 2^32 threads.
+ */
+typedef struct igc_kv_io {
+    igc_kv_cache cache;
+    int64_t batch, tokens;
+    igc_attn_view k, v;
+    const int32_t* table;
+    int64_t table_stride, table_entries;
+    const int32_t *start, *lens;
+    int64_t dtype;
+} igc_kv_io;
+
+int32_t kv_cache_write(const igc_kv_io* args, void* stream);
+int32_t kv_cache_write_check(const igc_kv_io* args);
+int32_t kv_cache_read(const igc_kv_io* args, void* stream);
+int32_t kv_cache_read_check(const igc_kv_io* args);
+
+/*
+ * Attention of new tokens over the cache.  q, out [batch, q_len, q_heads,
+ * head_dim], kv_heads dividing q_heads; lens int32 [batch]: the tokens that a
+ * sequence holds, at positions 0 .. lens[b] - 1 (limited to what its row of
+ * the table reaches; a negative length is 0).  With causal != 0 the new tokens
+ * are the last q_len of them: token i attends to positions below
+ * lens[b] - (q_len - 1 - i).  With the values held, k_j and v_j, and as in
+ * cross_attn_fwd:
+ *   s_j = scale * q . k_j,  lse = log sum_j exp(s_j),  out = sum_j p_j v_j
+ * A row that attends to nothing has out = 0 and lse = -inf; one that attends
+ * to a page outside the pool is NaN.  Positions that a row does not attend to
+ * never enter its sums, whatever the pool holds there.
+ *   lse  fp32 [batch, q_heads, q_len], dense, or NULL
+ * The integers enter the matrix products as they are; p_j times the value's
+ * scale is held in 16 significant bits, sums in fp32.  Sequences of more than
+ * 1024 tokens (by the table's capacity) may be read by several workgroups,
+ * whose results (fp32, in the workspace) a second launch joins in a fixed
+ * order: results do not change from run to run.
+ * Limits: as cross_attn_fwd for q and out; the table's capacity below
+ * 2^31 - 4096, batch * q_heads below 2^31, batch * kv_heads times the tiles of
+ * 32 rows (q_len * q_heads / kv_heads) below 2^23.
+ */
+typedef struct igc_cache_attn {
+    igc_kv_cache cache;
+    int64_t batch, q_len, q_heads;
+    igc_attn_view q, out;
+    float* lse;
+    const int32_t* table;
+    int64_t table_stride, table_entries;
+    const int32_t* lens;
+    int64_t causal;
+    double scale;
+    int64_t dtype;
+    void* workspace;
+    size_t workspace_bytes;
+} igc_cache_attn;
+
+int32_t cache_attn_fwd(const igc_cache_attn* args, void* stream);
+int32_t cache_attn_fwd_check(const igc_cache_attn* args);
+size_t cache_attn_fwd_workspace_bytes(const igc_cache_attn* args);
+
 #ifdef __cplusplus
 }
 #endif
