@@ -179,8 +179,8 @@ def _load(path):
                  "qk_norm_rope_bwd_workspace_bytes"):
         getattr(L, name).argtypes, getattr(L, name).restype = [buf], sz
     # the packed argument structs of include/igemm_decoder.h
-    for name in ("layer_norm_fwd", "layer_norm_bwd", "quantize_rows", "kv_cache_write",
-                 "kv_cache_read", "cache_attn_fwd"):
+    for name in ("layer_norm_fwd", "layer_norm_bwd", "quantize_rows", "linear_i8",
+                 "kv_cache_write", "kv_cache_read", "cache_attn_fwd"):
         getattr(L, name).argtypes, getattr(L, name).restype = [buf, vp], i32
         check = getattr(L, name + "_check")
         check.argtypes, check.restype = [buf], i32
@@ -850,4 +850,5 @@ from .decoder import (  # noqa: E402,F401
     KVCache, cache_attention, cache_attn_fwd, cache_attn_fwd_check,
     cache_attn_fwd_workspace_bytes, kv_cache_read, kv_cache_write, kv_cache_write_check,
     layer_norm, layer_norm_bwd, layer_norm_bwd_check, layer_norm_bwd_workspace_bytes,
-    layer_norm_fwd, layer_norm_fwd_check, layer_norm_grad, quantize_rows)
+    layer_norm_fwd, layer_norm_fwd_check, layer_norm_grad, linear_i8,
+    linear_i8_check, quantize_rows)

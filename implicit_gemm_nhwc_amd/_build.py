@@ -33,7 +33,8 @@ for _dt in ("BF16", "FP16"):
               (f"launch_attn_bwd_{_dt.lower()}", "launch_attn_bwd.hip", [_d]),
               (f"launch_qk_norm_{_dt.lower()}", "launch_qk_norm.hip", [_d]),
               (f"launch_layer_norm_{_dt.lower()}", "launch_layer_norm.hip", [_d]),
-              (f"launch_kv_cache_{_dt.lower()}", "launch_kv_cache.hip", [_d])]
+              (f"launch_kv_cache_{_dt.lower()}", "launch_kv_cache.hip", [_d]),
+              (f"launch_linear_i8_{_dt.lower()}", "launch_linear_i8.hip", [_d])]
 for _dt in ("BF16", "FP16", "FP8"):
     _d = f"-DIGC_DT=igc::DT_{_dt}"
     UNITS += [(f"launch_band_{_dt.lower()}", "launch_band.hip", [_d]),

@@ -7,6 +7,7 @@
 #include "igemm_host.hpp"
 #include "kv_cache.hpp"
 #include "layer_norm.hpp"
+#include "linear_i8.hpp"
 #include "rows_i8.hpp"
 
 namespace igc {
@@ -39,6 +40,17 @@ constexpr int kQuantMaxChannels = 131071;
 // pieces.
 template <int DT>
 hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t stream);
+
+// Form of the product: at most kFewRows rows of x, or square tiles.
+constexpr int kFewRows = 64;
+struct LinForm {
+    int tile;         // 0: few rows
+    int64_t tiles_m, tiles_n;
+    int threads;
+};
+
+template <int DT>
+hipError_t launch_linear_i8(const LinArgs& a, int tile, hipStream_t stream);
 
 template <int DT>
 hipError_t launch_kv_cache(const CacheArgs& a, bool write, hipStream_t stream);

@@ -1,7 +1,7 @@
 // C-ABI entry points of the decoder block's operators (declarations and
 // contracts in include/igemm_decoder.h): the host gates, the launch plans and
 // the workspaces.  Every step of the computation runs in the kernels of
-// layer_norm.hpp, rows_i8.hpp, kv_cache.hpp and cache_attn.hpp.
+// layer_norm.hpp, rows_i8.hpp, linear_i8.hpp, kv_cache.hpp and cache_attn.hpp.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -255,6 +255,52 @@ int32_t check_quant(const igc_quantize_rows* p, Rows* x, Rows* q) {
     return IGC_OK;
 }
 
+// ------------------------------------------------------------ their product
+// The largest tiles that still give every CU one; smaller ones fill the card
+// with fewer rows or columns.
+LinForm lin_form(const igc_linear_i8* p) {
+    if (p->m <= kFewRows) return {0, 1, ceil_div(p->n, 16), kFewWaves * 64};
+    for (int tile : {256, 128}) {
+        const LinForm f{tile, ceil_div(p->m, tile), ceil_div(p->n, tile), tile == 256 ? 512 : 256};
+        if (f.tiles_m * f.tiles_n >= kNumCUs) return f;
+    }
+    return {64, ceil_div(p->m, 64), ceil_div(p->n, 64), 256};
+}
+
+int32_t check_linear(const igc_linear_i8* p) {
+    if (!p) return IGC_DECLINE_NULL_POINTER;
+    if (p->dtype != IGC_DTYPE_BF16 && p->dtype != IGC_DTYPE_FP16) return IGC_DECLINE_DTYPE;
+    if (p->m < 0 || p->n < 0 || p->k < 0) return IGC_DECLINE_SHAPE;
+    if (p->m >= kLim31 || p->n >= kLim31 || p->k > kQuantMaxChannels)
+        return IGC_DECLINE_SIZE_LIMIT;
+    if (p->m == 0 || p->n == 0) return IGC_OK;
+    const int64_t k16 = ceil_div(p->k, 16) * 16;
+    if (!p->y || !p->x_scale || !p->w_scale || (p->k && (!p->x || !p->w)))
+        return IGC_DECLINE_NULL_POINTER;
+    if ((p->k && (!aligned(p->x, 16) || !aligned(p->w, 16) || p->x_pitch % 16 ||
+                  p->w_pitch % 16)) ||
+        !aligned(p->y, 2) || !aligned(p->x_scale, 4) || !aligned(p->w_scale, 4) ||
+        !aligned(p->bias, 4))
+        return IGC_DECLINE_ALIGNMENT;
+    // rows of one may follow each other at any pitch, and x may repeat a row
+    if ((p->k && (p->x_pitch < 0 || p->w_pitch < 0)) || (p->m > 1 && p->y_pitch < p->n))
+        return IGC_DECLINE_STRIDE;
+    const int64_t lim = (int64_t)1 << 22;
+    if (p->x_pitch >= lim || p->w_pitch >= lim || p->y_pitch >= kBatchStrideLim ||
+        (double)p->m * (double)p->y_pitch > kExtentLim)
+        return IGC_DECLINE_SIZE_LIMIT;
+    const LinForm f = lin_form(p);
+    if (!launchable(f.tiles_m * f.tiles_n, f.threads)) return IGC_DECLINE_SIZE_LIMIT;
+    const size_t yb = (size_t)((p->m - 1) * p->y_pitch + p->n) * 2;
+    const size_t xb = p->k ? (size_t)((p->m - 1) * p->x_pitch + k16) : 0;
+    const size_t wb = p->k ? (size_t)((p->n - 1) * p->w_pitch + k16) : 0;
+    if (meet(p->y, yb, p->x, xb) || meet(p->y, yb, p->w, wb) ||
+        meet(p->y, yb, p->x_scale, (size_t)p->m * 4) ||
+        meet(p->y, yb, p->w_scale, (size_t)p->n * 4) || meet(p->y, yb, p->bias, (size_t)p->n * 4))
+        return IGC_DECLINE_OVERLAP;
+    return IGC_OK;
+}
+
 // ------------------------------------------------------------ the cache
 int64_t cache_pitch(const igc_kv_cache& c) { return ceil_div(c.head_dim, 16) * 16; }
 int64_t cache_rows(const igc_kv_cache& c) { return c.pages * c.kv_heads * c.page_tokens; }
@@ -503,6 +549,34 @@ int32_t quantize_rows(const igc_quantize_rows* args, void* stream) {
     const hipStream_t st = (hipStream_t)stream;
     const hipError_t e = args->dtype == IGC_DTYPE_BF16 ? launch_quantize_rows<DT_BF16>(a, st)
                                                        : launch_quantize_rows<DT_FP16>(a, st);
+    return e == hipSuccess ? 1 : -(int32_t)e;
+}
+
+int32_t linear_i8_check(const igc_linear_i8* args) { return check_linear(args); }
+
+int32_t linear_i8(const igc_linear_i8* args, void* stream) {
+    if (check_linear(args) != IGC_OK) return 0;
+    if (args->m == 0 || args->n == 0) return 1;
+    const LinForm f = lin_form(args);
+    LinArgs a{};
+    a.x = (const uint8_t*)args->x;
+    a.w = (const uint8_t*)args->w;
+    a.xs = args->x_scale;
+    a.ws = args->w_scale;
+    a.bias = args->bias;
+    a.y = (uint8_t*)args->y;
+    a.x_p = args->x_pitch;
+    a.w_p = args->w_pitch;
+    a.y_p = args->y_pitch * 2;
+    a.M = (int)args->m;
+    a.N = (int)args->n;
+    a.K = (int)args->k;
+    a.K16 = (int)(ceil_div(args->k, 16) * 16);
+    a.tiles_m = (int)f.tiles_m;
+    a.tiles_n = (int)f.tiles_n;
+    const hipStream_t st = (hipStream_t)stream;
+    const hipError_t e = args->dtype == IGC_DTYPE_BF16 ? launch_linear_i8<DT_BF16>(a, f.tile, st)
+                                                       : launch_linear_i8<DT_FP16>(a, f.tile, st);
     return e == hipSuccess ? 1 : -(int32_t)e;
 }
 

@@ -1,6 +1,6 @@
 """Binding of the decoder block's operators of include/igemm_decoder.h: layer
-norm with its gradient, rows in 8 bits, the paged cache of keys and values in 8
-bits, and the attention of new tokens over it.
+norm with its gradient, rows in 8 bits and their product, the paged cache of
+keys and values in 8 bits, and the attention of new tokens over it.
 
 Argument marshalling only, as in the package's other calls: every step runs in
 the HIP kernels of libigemmconv.so, and there is no fallback.  InvalidArgument
@@ -12,11 +12,11 @@ torch.autograd.Function).
   layer_norm_fwd, layer_norm_fwd_check, layer_norm_grad,
   layer_norm_bwd_check, layer_norm_bwd_workspace_bytes,
   cache_attn_fwd, cache_attn_fwd_check, cache_attn_fwd_workspace_bytes,
-  kv_cache_write_check
+  linear_i8_check, kv_cache_write_check
 mirror the C entries (layer_norm_grad: layer_norm_bwd; 1 handled, 0 declined,
 < 0 HIP error; outputs and workspace given); layer_norm, layer_norm_bwd,
-quantize_rows, kv_cache_write, kv_cache_read and cache_attention allocate their
-outputs and raise on failure.
+quantize_rows, linear_i8, kv_cache_write, kv_cache_read and cache_attention
+allocate their outputs and raise on failure.
 """
 import struct
 
@@ -28,6 +28,7 @@ from .attention import (_current_gpu, _dense, _device, _elsewhere, _like, _on, _
 
 _LN = struct.Struct("@20qdqqq")
 _QUANT = struct.Struct("@14q")
+_LINEAR = struct.Struct("@13q")
 _CACHE = struct.Struct("@8q")
 _IO = struct.Struct("@16q")        # after a cache
 _CATTN = struct.Struct("@17qdqqq")   # after a cache
@@ -198,6 +199,85 @@ def quantize_rows(x, *, stream=None):
     if rc != 1:
         _raise("quantize_rows", rc, L.quantize_rows_check, packed)
     return (q if pitch == c else q[..., :c]), scale
+
+
+def _matrix(name, t, device):
+    """(rows, k, pitch) of an int8 tensor [..., k] whose rows lie one pitch
+    apart, k adjacent, with room for the last row's whole 16-byte pieces."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int8 or t.dim() < 1:
+        raise InvalidArgument(f"{name} must be an int8 tensor [..., k]")
+    if t.get_device() != device:
+        raise InvalidArgument(f"{name} is on {t.device}, the other tensors on GPU {device}")
+    k = t.shape[-1]
+    if t.stride(-1) != 1 and k > 1:
+        raise InvalidArgument(f"{name}: the values of a row must be adjacent")
+    rows, pitch = 1, None
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n != 1 and rows:
+            if pitch is None:
+                pitch = s
+            elif s != pitch * rows:
+                raise InvalidArgument(f"{name}: its rows must lie one stride apart")
+        rows *= n
+    if pitch is None:
+        pitch = -(-k // 16) * 16
+    if rows and k % 16:
+        end = t.storage_offset() + (rows - 1) * pitch + -(-k // 16) * 16
+        if end > t.untyped_storage().nbytes():
+            raise InvalidArgument(f"{name}: the last row's 16-byte pieces end past its storage "
+                                  "(quantize_rows leaves room for them)")
+    return rows, k, pitch
+
+
+def _vector(name, t, shape, device):
+    """Pointer of a dense fp32 tensor of this shape."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
+        raise InvalidArgument(f"{name} must be a tensor of shape {tuple(shape)}")
+    return _small(name, t, torch.float32, device)
+
+
+def _linear_pack(x, x_scale, w, w_scale, bias, out):
+    device = _device(x, "x")
+    rows, k, pitch = _matrix("x", x, device)
+    n, wk, w_pitch = _matrix("w", w, device)
+    if w.dim() != 2 or wk != k:
+        raise InvalidArgument(f"w must be [n, {k}] (got {tuple(w.shape)})")
+    code = _element(out, "y")
+    return _LINEAR.pack(rows, n, k, x.data_ptr(), pitch, w.data_ptr(), w_pitch,
+                        _vector("x_scale", x_scale, x.shape[:-1], device),
+                        _vector("w_scale", w_scale, (n,), device),
+                        0 if bias is None else _vector("bias", bias, (n,), device),
+                        out.data_ptr(), n, code)
+
+
+def linear_i8_check(x, x_scale, w, w_scale, out, *, bias=None) -> int:
+    """Host-only gate of linear_i8 into a dense out: 0 or a decline reason
+    code."""
+    return lib().linear_i8_check(_linear_pack(x, x_scale, w, w_scale, bias, out))
+
+
+def linear_i8(x, x_scale, w, w_scale, *, bias=None, dtype=torch.bfloat16, stream=None):
+    """The product of rows in 8 bits: x int8 [..., k] with x_scale fp32 [...]
+    and w int8 [n, k] with w_scale fp32 [n] (quantize_rows of the tokens and of
+    the weights) give dtype [..., n]: (x w^T) x_scale w_scale + bias (fp32 [n]
+    or None).  The integer sums are exact.  Rows start at multiples of 16 bytes,
+    which their last 16-byte piece may reach past k."""
+    device = _device(x, "x")
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return linear_i8(x, x_scale, w, w_scale, bias=bias, dtype=dtype)
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise InvalidArgument(f"dtype {dtype} is not bf16 or fp16")
+    n = w.shape[0] if isinstance(w, torch.Tensor) and w.dim() else 0
+    if x.dim() < 1:
+        raise InvalidArgument("x must be an int8 tensor [..., k]")
+    y = torch.empty((*x.shape[:-1], n), dtype=dtype, device=x.device)
+    packed = _linear_pack(x, x_scale, w, w_scale, bias, y)
+    L = lib()
+    rc = L.linear_i8(packed, _raw_stream(device))
+    if rc != 1:
+        _raise("linear_i8", rc, L.linear_i8_check, packed)
+    return y
 
 
 # ------------------------------------------------------------------ the cache

@@ -94,6 +94,37 @@ int32_t quantize_rows(const igc_quantize_rows* args, void* stream);
 int32_t quantize_rows_check(const igc_quantize_rows* args);
 
 /*
+ * Product of rows in 8 bits: for x int8 [m][k] with a scale a row (a token) and
+ * w int8 [n][k] with a scale a row (an output channel),
+ *   y[i][j] = (sum_k x[i][k] w[j][k]) x_scale[i] w_scale[j] + bias[j]
+ * The integer sums are exact; scales and bias enter in fp32.
+ *   x, w     pointers and row pitches (bytes) are multiples of 16; a row's last
+ *            16-byte piece is read whole, its bytes past k do not matter.
+ *            Every int8 value is allowed, -128 too
+ *   x_scale  fp32 [m], w_scale fp32 [n], bias fp32 [n] or NULL
+ *   y        dtype (bf16 or fp16) [m][n], any row pitch (elements) from n on,
+ *            and any alignment of the type
+ * Limits: k from 0 to 131071, m and n below 2^31, pitches of x and w below 2^22
+ * and of y below 2^40; a launch holds fewer than 2^32 threads (at most 64 rows:
+ * 512 for every 16 columns; otherwise 512 for a tile of 256 x 256, or 256 for
+ * one of 128 x 128 or 64 x 64, whichever fills the card).
+ */
+typedef struct igc_linear_i8 {
+    int64_t m, n, k;
+    const int8_t* x;
+    int64_t x_pitch;
+    const int8_t* w;
+    int64_t w_pitch;
+    const float *x_scale, *w_scale, *bias;
+    void* y;
+    int64_t y_pitch;
+    int64_t dtype;               /* of y */
+} igc_linear_i8;
+
+int32_t linear_i8(const igc_linear_i8* args, void* stream);
+int32_t linear_i8_check(const igc_linear_i8* args);
+
+/*
  * The paged cache of keys and values in 8 bits.  A pool holds `pages` pages of
  * page_tokens tokens; k and v are int8 [pages][kv_heads][page_tokens][Dp],
  * Dp = head_dim rounded up to 16, k_scale and v_scale fp32
