@@ -6,8 +6,8 @@ _build/ and linked into one shared library.  The same sources are also built
 as libigemmconv_ldspoison.so with IGC_LDS_POISON defined: a debug build whose
 kernels first fill their LDS with NaN bytes, so that a read running ahead of
 its data (a missing wait or barrier) shows up as NaN outputs in the tests.
-The attention binding's C++ part (_attn_marshal.so) is built with g++ beside
-them.
+The bindings' C++ parts (_attn_marshal.so, _decoder_marshal.so) are built with
+g++ beside them.
 """
 import concurrent.futures
 import os
@@ -20,7 +20,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libigemmconv.so")
 POISON_LIB = os.path.join(PKG, "libigemmconv_ldspoison.so")
-MARSHAL = os.path.join(PKG, "_attn_marshal.so")
+# the bindings' C++ parts: source -> extension module
+MARSHALS = {name + ".cpp": os.path.join(PKG, f"_{name}.so")
+            for name in ("attn_marshal", "decoder_marshal")}
 OBJ_DIR = os.path.join(PKG, "_build")
 ARCH = "gfx950"
 
@@ -56,8 +58,8 @@ def _hipcc():
     return os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
 
 
-def _marshal_cmd():
-    """g++ line of the attention binding's C++ part (torch's headers; no GPU code)."""
+def _marshal_cmd(src, out):
+    """g++ line of a binding's C++ part (torch's headers; no GPU code)."""
     import torch
 
     root = os.path.dirname(torch.__file__)
@@ -65,8 +67,8 @@ def _marshal_cmd():
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             "-I", INCLUDE, "-isystem", os.path.join(root, "include"), "-isystem",
-            sysconfig.get_paths()["include"], os.path.join(CSRC, "attn_marshal.cpp"),
-            "-o", MARSHAL + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+            sysconfig.get_paths()["include"], os.path.join(CSRC, src),
+            "-o", out + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def _newest_source():
@@ -100,8 +102,9 @@ def build(verbose: bool = False, jobs: int = None, incremental: bool = False,
                          os.path.join(CSRC, src), "-o", obj])
         links.append((lib, [hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o",
                             lib + ".tmp"]))
-    if not (incremental and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) > newest):
-        cmds.insert(0, _marshal_cmd())
+    for src, out in MARSHALS.items():
+        if not (incremental and os.path.exists(out) and os.path.getmtime(out) > newest):
+            cmds.insert(0, _marshal_cmd(src, out))
     if jobs is None:
         jobs = max(1, min(len(cmds), os.cpu_count() or 1))
 
@@ -116,8 +119,9 @@ def build(verbose: bool = False, jobs: int = None, incremental: bool = False,
     for lib, link in links:
         run(link)
         os.replace(lib + ".tmp", lib)
-    if os.path.exists(MARSHAL + ".tmp"):
-        os.replace(MARSHAL + ".tmp", MARSHAL)
+    for out in MARSHALS.values():
+        if os.path.exists(out + ".tmp"):
+            os.replace(out + ".tmp", out)
     return LIB
 
 

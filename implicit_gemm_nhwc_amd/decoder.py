@@ -18,6 +18,7 @@ mirror the C entries (layer_norm_grad: layer_norm_bwd; 1 handled, 0 declined,
 quantize_rows, linear_i8, kv_cache_write, kv_cache_read and cache_attention
 allocate their outputs and raise on failure.
 """
+import ctypes
 import struct
 
 import torch
@@ -25,6 +26,11 @@ import torch
 from . import DTYPE_CODES, InvalidArgument, lib
 from .attention import (_current_gpu, _dense, _device, _elsewhere, _like, _on, _raise,
                         _raw_stream, _small, _view, _work)
+
+try:   # the ordinary calls in C++ (csrc/decoder_marshal.cpp); without it, all through Python
+    from . import _decoder_marshal as _fast
+except ImportError:
+    _fast = None
 
 _LN = struct.Struct("@20qdqqq")
 _QUANT = struct.Struct("@14q")
@@ -34,6 +40,21 @@ _IO = struct.Struct("@16q")        # after a cache
 _CATTN = struct.Struct("@17qdqqq")   # after a cache
 _NO_VIEW = (0, 0, 0, 0)
 _FORWARD = object()   # in place of a gradient
+
+
+def _entries():
+    """The current library's entries as decoder_marshal.cpp takes them."""
+    L = lib()
+    try:
+        return L.decoder_entries
+    except AttributeError:
+        pass
+    L.decoder_entries = _fast.bind(*(
+        ctypes.cast(getattr(L, n), ctypes.c_void_p).value
+        for n in ("layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes",
+                  "quantize_rows", "linear_i8", "kv_cache_write", "kv_cache_read",
+                  "cache_attn_fwd", "cache_attn_fwd_workspace_bytes")))
+    return L.decoder_entries
 
 
 def _element(t, name):
@@ -139,6 +160,10 @@ def layer_norm(x, weight=None, bias=None, *, eps=1e-5, stream=None):
     a dense tensor like x.  Gradients by layer_norm_bwd (none are recorded for
     autograd)."""
     device = _device(x, "x")
+    if _fast is not None and stream is None:
+        r = _fast.layer_norm(_entries(), x, weight, bias, eps, _raw_stream(device), _current_gpu())
+        if r is not None:
+            return r
     if _elsewhere(device, stream):
         with _on(device, stream):
             return layer_norm(x, weight, bias, eps=eps)
@@ -156,6 +181,11 @@ def layer_norm_bwd(dy, x, weight=None, *, eps=1e-5, stream=None):
     dy, dx dense like x, the others fp32 (also for a weight or bias of None,
     which count as ones and zeros)."""
     device = _device(x, "x")
+    if _fast is not None and stream is None:
+        r = _fast.layer_norm_bwd(_entries(), dy, x, weight, eps, _raw_stream(device),
+                                 _current_gpu())
+        if r is not None:
+            return r
     if _elsewhere(device, stream):
         with _on(device, stream):
             return layer_norm_bwd(dy, x, weight, eps=eps)
@@ -183,6 +213,10 @@ def quantize_rows(x, *, stream=None):
     at multiples of 16 bytes, as linear_i8 reads them.  A row with an infinity
     or a NaN has scale NaN, one below 2^-110 scale 0."""
     device = _device(x, "x")
+    if _fast is not None and stream is None:
+        r = _fast.quantize_rows(_entries(), x, _raw_stream(device), _current_gpu())
+        if r is not None:
+            return r
     if _elsewhere(device, stream):
         with _on(device, stream):
             return quantize_rows(x)
@@ -263,6 +297,11 @@ def linear_i8(x, x_scale, w, w_scale, *, bias=None, dtype=torch.bfloat16, stream
     or None).  The integer sums are exact.  Rows start at multiples of 16 bytes,
     which their last 16-byte piece may reach past k."""
     device = _device(x, "x")
+    if _fast is not None and stream is None:
+        r = _fast.linear_i8(_entries(), x, x_scale, w, w_scale, bias, dtype,
+                            _raw_stream(device), _current_gpu())
+        if r is not None:
+            return r
     if _elsewhere(device, stream):
         with _on(device, stream):
             return linear_i8(x, x_scale, w, w_scale, bias=bias, dtype=dtype)
@@ -301,9 +340,11 @@ class KVCache:
             if not isinstance(t, torch.Tensor) or t.shape != shape:
                 raise InvalidArgument(f"{name} must be a tensor of shape {tuple(shape)}")
             _small(name, t, dtype, device)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._parts = (k, v, k_scale, v_scale)
         self.head_dim = head_dim
         pages, heads, tokens, _ = k.shape
+        self.device = device
+        self.kv_heads = heads
         self.packed = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
                                   v_scale.data_ptr(), pages, tokens, heads, head_dim)
 
@@ -316,15 +357,13 @@ class KVCache:
         scales = [torch.zeros(shape, dtype=torch.float32, device=device) for _ in range(2)]
         return cls(*rows, *scales, head_dim)
 
-    @property
-    def kv_heads(self):
-        return self.k.shape[1]
+    k, v, k_scale, v_scale = (property(lambda self, i=i: self._parts[i]) for i in range(4))
 
 
 def _pool(cache):
     if not isinstance(cache, KVCache):
         raise InvalidArgument("cache must be a KVCache")
-    return cache.k.get_device()
+    return cache.device
 
 
 def _page_table(table, b, device):
@@ -383,7 +422,12 @@ def kv_cache_write(cache, k, v, table, start, *, lens=None, stream=None):
     p % page_tokens of page table[b, p // page_tokens].  Positions past the
     table and pages outside the pool are left out.  The page of a place must
     not be written twice in one call."""
-    packed, device = _write_pack(cache, k, v, table, start, lens)
+    device = _pool(cache)
+    if _fast is not None and stream is None and device == _current_gpu():
+        if _fast.kv_cache_write(_entries(), cache.packed, k, v, table, start, lens,
+                                _raw_stream(device), device):
+            return
+    packed, _ = _write_pack(cache, k, v, table, start, lens)
     if _elsewhere(device, stream):
         with _on(device, stream):
             return kv_cache_write(cache, k, v, table, start, lens=lens)
@@ -398,6 +442,11 @@ def kv_cache_read(cache, table, start, tokens, *, lens=None, dtype=torch.bfloat1
     + tokens - 1, as dense tensors [batch, tokens, kv_heads, D] of dtype; zeros
     from lens[b] on, NaN where a position or page does not exist."""
     device = _pool(cache)
+    if _fast is not None and stream is None and device == _current_gpu():
+        r = _fast.kv_cache_read(_entries(), cache.packed, table, start, tokens, lens, dtype,
+                                _raw_stream(device), device)
+        if r is not None:
+            return r
     if _elsewhere(device, stream):
         with _on(device, stream):
             return kv_cache_read(cache, table, start, tokens, lens=lens, dtype=dtype)
@@ -484,6 +533,11 @@ def cache_attention(q, cache, table, lens, *, causal=True, scale=None, return_ls
     out, dense like q, and with return_lse also the fp32 statistics [batch,
     hq, tq].  No gradients: the cache is for inference."""
     device = _pool(cache)
+    if _fast is not None and stream is None and device == _current_gpu():
+        r = _fast.cache_attention(_entries(), q, cache.packed, table, lens, causal, scale,
+                                  return_lse, _raw_stream(device), device)
+        if r is not None:
+            return r
     if _elsewhere(device, stream):
         with _on(device, stream):
             return cache_attention(q, cache, table, lens, causal=causal, scale=scale,
