@@ -1,6 +1,6 @@
 // Attention of a few new tokens over the paged cache in 8 bits.
 //
-// Rows are the Tq * G queries that share one key head, 32 a workgroup; its
+// Rows are the Tq * G queries that share one key head, 16 RB a workgroup; its
 // waves take blocks of 32 keys in turn.  With k_j = ks_j K_j and v_j = vs_j V_j
 // (integers K, V):
 //   s_j = (q . K_j) ks_j scale,  p_j = 2^(s_j log2 e - m),
@@ -8,11 +8,13 @@
 // so that the integers enter the matrix products as they are: 8 bits are exact
 // in both 16-bit types, and the scales go to the scores and probabilities.
 //
-// Scores come as S^T = K Q^T (keys down the registers, one row a lane).  The
-// result's register i of half h is row 8 (i / 4) + 4 h + i % 4; it is given key
-// 16 (i / 8) + 8 h + i % 8 by reading the keys in that order, so that the 8
-// probabilities of a product's k slots are 8 neighbouring keys: one transposing
-// 8-bit read of the values and two reads of the scales.
+// All products are v_mfma_f32_16x16x32: lane l supplies row (A) or column (B)
+// l % 16 with 8 k at slots 8 (l / 16), and the result has column l % 16 and, in
+// register i, row 4 (l / 16) + i.  Scores come as S^T = K Q^T, two products of
+// 16 keys (t = 0, 1); row r of product t is given key 8 (r / 4) + 4 t + r % 4,
+// so that a lane's 8 scores are 8 neighbouring keys and become a B operand of
+// O^T += V^T P^T without leaving it; the other operand is one transposing 8-bit
+// read of the values.
 //
 // p vs is held as the sum of two bf16 numbers (16 bits of its own), which
 // doubles the second products but leaves the outputs as accurate as fp32
@@ -36,10 +38,11 @@ struct CacheAttnArgs {
     int64_t slots;         // of cache_plan.hpp
     int entries, pages, shift, Dp;
     int causal;
+    int tile;              // rows a workgroup: 16 or 32
     int split;             // whether workgroups share a sequence (then a join follows)
 };
 
-constexpr int kCacheWaves = 8;
+constexpr int kCacheWaves = 8;   // a workgroup
 // The running maximum follows the true one only when a row exceeds it by
 // 2^kCacheSlack: it only guards the range.
 constexpr float kCacheSlack = 8.0f;
@@ -149,71 +152,104 @@ __device__ __forceinline__ i32x4 bytes_frag(uint32_t lo, uint32_t hi) {
     return f;
 }
 
-// Chunk c of row r of a tile of 8-bit rows at its place: 16-byte chunks turned
-// by the row so that 8 rows of one chunk lie in different banks.
+// Tiles hold 32 rows of DP bytes.  Chunk c (16 bytes) of row r lies at a place
+// turned by r, so that the 16 rows that a product's lanes read (8 a + 4 t + 0 ..
+// 3) and the 8 of a transposing read lie in different banks (96 bytes: nearly).
+template <int DP>
+__device__ __forceinline__ int tile8_turn(int r) {
+    if constexpr (DP == 128)
+        return ((r >> 1) & 1) | ((r >> 2) & 2) | ((((r >> 4) ^ (r >> 2)) & 1) << 2);
+    if constexpr (DP == 64) return ((r >> 3) ^ ((r >> 2) & 1)) & 3;
+    return r >> 3;
+}
 template <int DP>
 __device__ __forceinline__ int tile8_off(int r, int c) {
-    const int turn = DP == 128 ? r & 7 : DP == 64 ? (r >> 1) & 3 : 0;
-    return r * DP + ((c ^ turn) << 4);
+    const int t = tile8_turn<DP>(r);
+    if constexpr (DP == 96) return r * DP + ((c + t) % 6) * 16;
+    if constexpr (DP == 32) return r * DP + ((c ^ (t & 1)) << 4);
+    return r * DP + ((c ^ t) << 4);
 }
 
-// Direct loads of 32 rows of both pools' integers and of the scales; a lane's
+// Direct loads of 32 rows of a pool's integers and of their scales; a lane's
 // place in LDS fixes its row and chunk.  Chunks past the row read its first
 // one: the queries' zeros, or columns that are not stored, meet them.
 template <int DP>
 struct CacheStage {
     static constexpr int TILE = 32 * DP, PIECES = TILE / 1024;
-    static constexpr int BYTES = 2 * TILE + 256;   // keys, values, their scales
-    static constexpr int LOADS = 2 * PIECES + 1;
+    static constexpr int BYTES = TILE + 256;   // integers, scales (twice)
+    static constexpr int LOADS = PIECES + 1;
     int off[PIECES];
     bool high[PIECES];   // rows 16 .. 31
 
     __device__ __forceinline__ void init(int lane, int Dp) {
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const int at = i * 1024 + lane * 16, r = at / DP;
-            const int turn = DP == 128 ? r & 7 : DP == 64 ? (r >> 1) & 3 : 0;
-            const int c = ((at % DP) >> 4) ^ turn;
+            const int at = i * 1024 + lane * 16, r = at / DP, p = (at % DP) >> 4;
+            const int t = tile8_turn<DP>(r);
+            const int c = DP == 96 ? (p + 6 - t) % 6 : p ^ (DP == 32 ? t & 1 : t);
             high[i] = r >= 16;
             off[i] = (r & 15) * Dp + (c * 16 < Dp ? c * 16 : 0);
         }
     }
-    // rows r0 (the first 16 keys) and r1 of the pools
-    __device__ __forceinline__ void issue(const CacheAttnArgs& x, int64_t r0, int64_t r1,
-                                          int lane, uint8_t* lds) const {
+    // rows r0 (the first 16 keys) and r1 of a pool
+    __device__ __forceinline__ void issue(const int8_t* pool, const float* scale, int Dp,
+                                          int64_t r0, int64_t r1, int lane, uint8_t* lds) const {
         typedef __attribute__((address_space(1))) void* gp;
         typedef __attribute__((address_space(3))) void* lp;
+        const int8_t* b0 = pool + r0 * Dp;
+        const int8_t* b1 = pool + r1 * Dp;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int8_t* b0 = x.pool[t] + r0 * x.Dp;
-            const int8_t* b1 = x.pool[t] + r1 * x.Dp;
-#pragma unroll
-            for (int i = 0; i < PIECES; ++i)
-                __builtin_amdgcn_global_load_lds((gp)((high[i] ? b1 : b0) + off[i]),
-                                                 (lp)(lds + t * TILE + i * 1024), 16, 0, 0);
-        }
-        // lanes 0 .. 31 the keys' scales, the others the values'
-        const float* s = (lane < 32 ? x.scales[0] : x.scales[1]) + ((lane & 16) ? r1 : r0);
-        __builtin_amdgcn_global_load_lds((gp)(s + (lane & 15)), (lp)(lds + 2 * TILE), 4, 0, 0);
+        for (int i = 0; i < PIECES; ++i)
+            __builtin_amdgcn_global_load_lds((gp)((high[i] ? b1 : b0) + off[i]),
+                                             (lp)(lds + i * 1024), 16, 0, 0);
+        const float* s = scale + ((lane & 16) ? r1 : r0) + (lane & 15);
+        __builtin_amdgcn_global_load_lds((gp)s, (lp)(lds + TILE), 4, 0, 0);
     }
 };
 
-template <int DT, int DP, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void cache_attn_kernel(CacheAttnArgs x) {
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(const i32x4& a, const i32x4& b, f32x4 c) {
+    if constexpr (DT == DT_FP16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// x over a lane and those 16, 32 and 48 away.
+__device__ __forceinline__ void both_rows(float x, float* lo, float* hi) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t r0 = r[0], r1 = r[1];
+    *lo = __builtin_bit_cast(float, r0);
+    *hi = __builtin_bit_cast(float, r1);
+}
+__device__ __forceinline__ float max_quarters(float x) {
+    float a, b;
+    both_rows(x, &a, &b);
+    return max_halves(fmaxf(a, b));
+}
+__device__ __forceinline__ float sum_quarters(float x) {
+    float a, b;
+    both_rows(x, &a, &b);
+    return sum_halves(a + b);
+}
+
+template <int DT, int DP, int RB, int NW>
+__global__ __launch_bounds__(NW * 64, RB == 1 ? 4 : 2) void cache_attn_kernel(CacheAttnArgs x) {
     const AttnArgs& a = x.a;
-    constexpr int DB = DP / 32, KS = DP / 16;
+    constexpr int DB = DP / 16, KS = DP / 32, ROWS = 16 * RB;
     using Stage = CacheStage<DP>;
+    constexpr int OWN = 2 * Stage::BYTES;   // a wave's keys and values, then 16 rows of results
+    static_assert(OWN >= 16 * DP * 4, "a wave's results fit its stages");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    lds_poison<NW * 64>(lds, NW * OWN + NW * 32 * 4);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int half = lane >> 5;
-    const int rows_tile = min(a.rows, 32);
-    // a wave's two stages, which its results reuse
-    constexpr int own = 2 * Stage::BYTES;
-    static_assert(own >= 32 * DP * 4, "a wave's results fit its stages");
-    lds_poison<NW * 64>(lds, NW * own + NW * 64 * 4);
-    uint8_t* mine = lds + wave * own;
-    float* st_m = reinterpret_cast<float*>(lds + NW * own);   // [NW][32] m, then l
-    float* st_l = st_m + NW * 32;
+    const int quarter = lane >> 4, r16 = lane & 15;
+    uint8_t* kl = lds + wave * OWN;
+    uint8_t* vl = kl + Stage::BYTES;
+    float* st_m = reinterpret_cast<float*>(lds + NW * OWN);   // [NW][16] m, then l
+    float* st_l = st_m + NW * 16;
 
     const int hr_n = a.Hk * a.row_tiles;
     CachePlace at;
@@ -240,31 +276,8 @@ __global__ __launch_bounds__(NW * 64, 2) void cache_attn_kernel(CacheAttnArgs x)
     const int begin = __builtin_amdgcn_readfirstlane((int)at.begin);
     const int end = __builtin_amdgcn_readfirstlane((int)at.end);
     const int len = __builtin_amdgcn_readfirstlane(at.len);
-    const int hk = hr / a.row_tiles, row0 = (hr - hk * a.row_tiles) * 32;
-    const int row = row0 + (lane & 31), t0 = div_g(a, row0);
-
-    // queries: k step 2 y + z, half h holds values 32 y + 16 h + 8 z .. + 7, as
-    // the keys' 16-byte chunks do
-    i32x4 qf[KS];
-    {
-        const __amdgpu_buffer_rsrc_t rs = attn_rsrc(
-            a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h + (int64_t)t0 * a.q_t);
-        const unsigned off = packed_off(a, row, t0, a.q_t, a.q_h);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const int d = 32 * (s >> 1) + 16 * half + 8 * (s & 1);
-            qf[s] = __builtin_bit_cast(i32x4, load16(rs, d < a.D ? off + 2 * d : kOut));
-        }
-    }
-    // this lane's row sees the keys before `last`
-    int last = len;
-    if (x.causal) last = len - (a.Tq - 1 - div_g(a, min(row, a.rows - 1)));
-    f32x16 acc[DB];
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
-    float m = -__builtin_inff(), l = 0.0f;
+    const int hk = hr / a.row_tiles, row0 = (hr - hk * a.row_tiles) * ROWS;
+    const int t0 = div_g(a, row0);
 
     Stage stage;
     stage.init(lane, x.Dp);
@@ -272,218 +285,316 @@ __global__ __launch_bounds__(NW * 64, 2) void cache_attn_kernel(CacheAttnArgs x)
     typedef __attribute__((address_space(4))) const int32_t* sp;
     const sp table = (sp)(x.table + b * x.table_stride);
     constexpr int STEP = NW * 32;
-    // pages of the two halves of the block at j; keys at or past the end need none
-    auto pages = [&](int j, int* id0, int* id1) {
-        *id0 = j < end ? cache_page(table, j, x.shift, x.entries, x.pages) : 0;
-        *id1 = j + 16 < end ? cache_page(table, j + 16, x.shift, x.entries, x.pages) : 0;
+    // Entries of the two halves of the block at j, and the pages they name: the
+    // loads are asked for long before their values are looked at.
+    auto entries = [&](int j, int* e0, int* e1) {
+        *e0 = table[min(j >> x.shift, x.entries - 1)];
+        *e1 = table[min((j + 16) >> x.shift, x.entries - 1)];
     };
-    auto issue = [&](int j, int id0, int id1, uint8_t* to) {
-        stage.issue(x, cache_row(id0 < 0 ? 0 : id0, a.Hk, hk, j, x.shift),
-                    cache_row(id1 < 0 ? 0 : id1, a.Hk, hk, j + 16, x.shift), lane, to);
+    auto page = [&](int e, int j) {
+        return j >> x.shift < x.entries && e >= 0 && e < x.pages ? e : -1;
     };
-    const int j0 = begin + wave * 32;
-    int id0 = 0, id1 = 0, nx0 = 0, nx1 = 0;   // the block's pages, and the next one's
-    if (j0 < end) {
-        pages(j0, &id0, &id1);
-        issue(j0, id0, id1, mine);
-        if (j0 + STEP < end) {
-            pages(j0 + STEP, &nx0, &nx1);
-            issue(j0 + STEP, nx0, nx1, mine + Stage::BYTES);
+    auto issue = [&](int which, int j, int id0, int id1) {
+        stage.issue(x.pool[which], x.scales[which], x.Dp,
+                    cache_row(id0 < 0 ? 0 : id0, a.Hk, hk, j, x.shift),
+                    cache_row(id1 < 0 ? 0 : id1, a.Hk, hk, j + 16, x.shift), lane,
+                    which ? vl : kl);
+    };
+
+    // queries: a lane reads whole 16-byte chunks of the keys, which are two k
+    // steps: steps 2 y + z of quarter f hold values 64 y + 16 f + 8 z .. + 7; a
+    // last single step 8 f .. + 7 of its 32
+    i32x4 qf[RB][KS];
+    int last[RB];   // this lane's row sees the keys before `last`
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+        const int row = row0 + 16 * i + r16;
+        const __amdgpu_buffer_rsrc_t rs = attn_rsrc(
+            a.q + (int64_t)b * a.q_b + (int64_t)hk * a.G * a.q_h + (int64_t)t0 * a.q_t);
+        const unsigned off = packed_off(a, row, t0, a.q_t, a.q_h);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int d = (KS & 1) && s == KS - 1 ? 32 * s + 8 * quarter
+                                                  : 64 * (s >> 1) + 16 * quarter + 8 * (s & 1);
+            qf[i][s] = __builtin_bit_cast(i32x4, load16(rs, d < a.D ? off + 2 * d : kOut));
         }
+        last[i] = x.causal ? len - (a.Tq - 1 - div_g(a, min(row, a.rows - 1))) : len;
     }
-    int buf = 0;
+    f32x4 acc[RB][DB];
+    float m[RB], l[RB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d) acc[i][d] = f32x4{0, 0, 0, 0};
+        m[i] = -__builtin_inff();
+        l[i] = 0.0f;
+    }
+
+    const int j0 = begin + wave * 32;
+    int id0 = 0, id1 = 0, nx0 = 0, nx1 = 0;
+    // Without a split the first block is asked for before the length is here;
+    // whatever the table says past it, the places exist.
+    if (j0 < (x.split ? end : (int)x.capacity)) {
+        entries(j0, &nx0, &nx1);
+        id0 = page(nx0, j0);
+        id1 = page(nx1, j0 + 16);
+        issue(0, j0, id0, id1);
+        issue(1, j0, id0, id1);
+    }
     for (int j = j0; j < end; j += STEP) {
-        // this block: all but the next one's loads
-        if (j + STEP < end) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Stage::LOADS) : "memory");
-        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        const uint8_t* kl = mine + buf * Stage::BYTES;
-        const uint8_t* vl = kl + Stage::TILE;
-        const float* sl = reinterpret_cast<const float*>(vl + Stage::TILE);
-        f32x16 s;
+        const bool more = j + STEP < end;
+        if (more) entries(j + STEP, &nx0, &nx1);
+        // the keys: all but the values asked for after them
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Stage::LOADS) : "memory");
+        f32x4 s[RB][2];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = 0.0f;
-        // row l % 32 of the product is key 16 (l / 16) + 8 bit 2 + 4 bit 3 + l % 4
-        const int key = (lane & 0x13) | ((lane & 4) << 1) | ((lane & 8) >> 1);
+        for (int i = 0; i < RB; ++i) s[i][0] = s[i][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int y = 0; y < DP / 32; ++y) {
-            const u32x4 kb = *reinterpret_cast<const u32x4*>(kl + tile8_off<DP>(key, 2 * y + half));
-            const i32x4 k0 = bytes_frag<DT>(kb[0], kb[1]), k1 = bytes_frag<DT>(kb[2], kb[3]);
-            s = mfma32<DT>(&k0, &qf[2 * y], s);
-            s = mfma32<DT>(&k1, &qf[2 * y + 1], s);
-        }
-        float ks[16], vs[16];
+        for (int t = 0; t < 2; ++t) {
+            const int key = 8 * (r16 >> 2) + 4 * t + (r16 & 3);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int at4 = 16 * (g >> 1) + 8 * half + 4 * (g & 1);
-            const f32x4 u = *reinterpret_cast<const f32x4*>(sl + at4);
-            const f32x4 w = *reinterpret_cast<const f32x4*>(sl + 32 + at4);
+            for (int y = 0; y < KS / 2; ++y) {
+                const u32x4 kb = *reinterpret_cast<const u32x4*>(
+                    kl + tile8_off<DP>(key, 4 * y + quarter));
+                const i32x4 k0 = bytes_frag<DT>(kb[0], kb[1]), k1 = bytes_frag<DT>(kb[2], kb[3]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ks[4 * g + i] = u[i];
-                vs[4 * g + i] = w[i];
-            }
-        }
-        if (id0 < 0 || id1 < 0) {   // no such page: its keys are NaN
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if ((i < 8 ? id0 : id1) < 0) ks[i] = vs[i] = __builtin_nanf("");
-        }
-        const int left = min(last, end) - j;
-        const bool full = __all(left >= 32);
-        float t = -__builtin_inff();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] *= ks[i] * a.c;
-        if (!full) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (16 * (i >> 3) + 8 * half + (i & 7) >= left) {
-                    s[i] = -__builtin_inff();
-                    vs[i] = 0.0f;   // may be anything there
+                for (int i = 0; i < RB; ++i) {
+                    s[i][t] = mfma16<DT>(k0, qf[i][2 * y], s[i][t]);
+                    s[i][t] = mfma16<DT>(k1, qf[i][2 * y + 1], s[i][t]);
                 }
-        }
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) t = fmaxf(fmaxf(s[i], s[i + 1]), t);
-        t = max_halves(t);
-        if (__any(t > m + kCacheSlack)) {
-            const float mn = fmaxf(m, t);
-            // rows still without a key: 2^(-inf - 0) keeps everything 0
-            const float f = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-            m = mn;
-            l *= f;
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[d][i] *= f;
-        }
-        const float ms = m == -__builtin_inff() ? 0.0f : m;
-        float sum[4] = {0, 0, 0, 0};
-        i32x4 hi[2], lo[2];
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            float p[2], q[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                p[k] = __builtin_amdgcn_exp2f(s[i + k] - ms);
-                sum[(i + k) & 3] += p[k];
-                p[k] *= vs[i + k];
             }
-            const uint32_t h = pack_out2(p[0], p[1], DT_BF16);
-            q[0] = p[0] - __builtin_bit_cast(float, h << 16);
-            q[1] = p[1] - __builtin_bit_cast(float, h & 0xffff0000u);
-            hi[i >> 3][(i >> 1) & 3] = (int)h;
-            lo[i >> 3][(i >> 1) & 3] = (int)pack_out2(q[0], q[1], DT_BF16);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        // values: lane i of 16 reads 8 bytes of row i / 2 and gets 8 rows of
-        // column i
+            if constexpr (KS & 1) {
+                const u32x2 kb = *reinterpret_cast<const u32x2*>(
+                    kl + tile8_off<DP>(key, 2 * (KS - 1) + (quarter >> 1)) + 8 * (quarter & 1));
+                const i32x4 k0 = bytes_frag<DT>(kb[0], kb[1]);
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                const int r = 16 * g + 8 * half + ((lane & 15) >> 1);
-                const u32x2 vb = read_tr8(vl + tile8_off<DP>(r, 2 * d + ((lane >> 4) & 1)) +
-                                          8 * (lane & 1));
-                const i32x4 vf = bytes_frag<DT_BF16>(vb[0], vb[1]);
-                acc[d] = mfma32<DT_BF16>(&vf, &hi[g], acc[d]);
-                acc[d] = mfma32<DT_BF16>(&vf, &lo[g], acc[d]);
+                for (int i = 0; i < RB; ++i) s[i][t] = mfma16<DT>(k0, qf[i][KS - 1], s[i][t]);
             }
-        // the stage is read: the block after the next may arrive
+        }
+        // the lane's keys are 8 quarter .. + 7: score k is register k % 4 of
+        // product k / 4
+        float ks[8];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const f32x4 u = *reinterpret_cast<const f32x4*>(kl + Stage::TILE + 32 * quarter +
+                                                            16 * g);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ks[4 * g + k] = u[k] * a.c;
+        }
+        // they are read: the next block's may arrive
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (more) {
+            nx0 = page(nx0, j + STEP);
+            nx1 = page(nx1, j + STEP + 16);
+            issue(0, j + STEP, nx0, nx1);
+        }
+        const bool bad = (quarter < 2 ? id0 : id1) < 0;   // no such page
+        if (id0 < 0 || id1 < 0) {   // its keys, as far as they count, are NaN
+#pragma unroll
+            for (int k = 0; k < 8; ++k) ks[k] = bad ? __builtin_nanf("") : ks[k];
+        }
+        float p[RB][8];
+        bool full = true;
+        int left[RB];
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            left[i] = min(last[i], end) - j - 8 * quarter;   // the lane's keys that count
+            full = full && left[i] >= 8;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) p[i][k] = s[i][k >> 2][k & 3] * ks[k];
+        }
+        full = __all(full);
+        if (!full) {
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k >= left[i]) p[i][k] = -__builtin_inff();
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            float t = fmaxf(p[i][0], p[i][1]);
+#pragma unroll
+            for (int k = 2; k < 8; k += 2) t = fmaxf(fmaxf(p[i][k], p[i][k + 1]), t);
+            t = max_quarters(t);
+            if (__any(t > m[i] + kCacheSlack)) {
+                const float mn = fmaxf(m[i], t);
+                // rows still without a key: 2^(-inf - 0) keeps everything 0
+                const float f =
+                    mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[i] - mn);
+                m[i] = mn;
+                l[i] *= f;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) acc[i][d] *= f;
+            }
+            const float ms = m[i] == -__builtin_inff() ? 0.0f : m[i];
+            float sum[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                p[i][k] = __builtin_amdgcn_exp2f(p[i][k] - ms);
+                sum[k & 1] += p[i][k];
+            }
+            l[i] += sum[0] + sum[1];
+        }
+        // the values: all but the next keys
+        if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Stage::LOADS) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        float vs[8];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const f32x4 u = *reinterpret_cast<const f32x4*>(vl + Stage::TILE + 32 * quarter +
+                                                            16 * g);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) vs[4 * g + k] = u[k];
+        }
+        if (id0 < 0 || id1 < 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) vs[k] = bad ? __builtin_nanf("") : vs[k];
+        }
+        i32x4 hi[RB], lo[RB];
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                p[i][k] *= vs[k];
+                // keys that do not count may hold anything
+                if (!full && k >= left[i]) p[i][k] = 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+                const uint32_t h = pack_out2(p[i][k], p[i][k + 1], DT_BF16);
+                hi[i][k / 2] = (int)h;
+                lo[i][k / 2] = (int)pack_out2(p[i][k] - __builtin_bit_cast(float, h << 16),
+                                              p[i][k + 1] -
+                                                  __builtin_bit_cast(float, h & 0xffff0000u),
+                                              DT_BF16);
+            }
+        }
+        // values: lane i of 16 reads 8 bytes of row i / 2 of the quarter's 8 and
+        // gets its 8 rows of column i
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+            const u32x2 vb = read_tr8(vl + tile8_off<DP>(8 * quarter + (r16 >> 1), d) +
+                                      8 * (lane & 1));
+            const i32x4 vf = bytes_frag<DT_BF16>(vb[0], vb[1]);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                acc[i][d] = mfma16<DT_BF16>(vf, hi[i], acc[i][d]);
+                acc[i][d] = mfma16<DT_BF16>(vf, lo[i], acc[i][d]);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (more) issue(1, j + STEP, nx0, nx1);
         id0 = nx0;
         id1 = nx1;
-        if (j + 2 * STEP < end) {
-            pages(j + 2 * STEP, &nx0, &nx1);
-            issue(j + 2 * STEP, nx0, nx1, mine + buf * Stage::BYTES);
-        }
-        buf ^= 1;
     }
-    // join of the waves: each wave's rows as floats [rows][DP] over its stages
-    l = sum_halves(l);
-    float* po = reinterpret_cast<float*>(mine);
-    const int r32 = lane & 31;
-    if (r32 < rows_tile) {
+    // join of the waves, 16 rows at a time: each wave's as floats [16][DP] over
+    // its stages, once nothing is under way to them
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    float* po = reinterpret_cast<float*>(kl);
+    const int per = a.D / 4;
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+    for (int i = 0; i < RB; ++i) {
+        const int n = min(16, a.rows - row0 - 16 * i);
+        if (i > 0) __syncthreads();
+        const float ls = sum_quarters(l[i]);
+        if (r16 < n) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<f32x4*>(po + r32 * DP + 32 * d + 8 * g + 4 * half) =
-                    f32x4{acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]};
-        if (half == 0) {
-            st_m[wave * 32 + r32] = m;
-            st_l[wave * 32 + r32] = l;
-        }
-    }
-    __syncthreads();
-    const int per = a.D / 4, n = min(32, a.rows - row0);
-    for (int e = threadIdx.x; e < n * per; e += NW * 64) {
-        const int r = e / per, d = (e - r * per) * 4;
-        float mm = -__builtin_inff();
-#pragma unroll
-        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, st_m[w * 32 + r]);
-        const float ms = mm == -__builtin_inff() ? 0.0f : mm;
-        float ll = 0.0f;
-        f32x4 o = {0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float f = __builtin_amdgcn_exp2f(st_m[w * 32 + r] - ms);
-            ll = __builtin_fmaf(st_l[w * 32 + r], f, ll);
-            const f32x4 v = *reinterpret_cast<const f32x4*>(
-                reinterpret_cast<const float*>(lds + w * own) + r * DP + d);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], f, o[i]);
-        }
-        if (parts > 1) {
-            const int64_t to = (int64_t)blockIdx.x * rows_tile + r;
-            *reinterpret_cast<f32x4*>(a.part + to * a.D + d) = o;
-            if (d == 0) {
-                a.stat[to * 2] = mm;
-                a.stat[to * 2 + 1] = ll;
+            for (int d = 0; d < DB; ++d)
+                *reinterpret_cast<f32x4*>(po + r16 * DP + 16 * d + 4 * quarter) = acc[i][d];
+            if (quarter == 0) {
+                st_m[wave * 16 + r16] = m[i];
+                st_l[wave * 16 + r16] = ls;
             }
-            continue;
         }
-        cache_attn_out<DT>(a, b, hk, row0 + r, d, o, mm, ll);
+        __syncthreads();
+        for (int e = threadIdx.x; e < n * per; e += NW * 64) {
+            const int r = e / per, d = (e - r * per) * 4;
+            float mm = -__builtin_inff();
+#pragma unroll
+            for (int w = 0; w < NW; ++w) mm = fmaxf(mm, st_m[w * 16 + r]);
+            const float ms = mm == -__builtin_inff() ? 0.0f : mm;
+            float ll = 0.0f;
+            f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float f = __builtin_amdgcn_exp2f(st_m[w * 16 + r] - ms);
+                ll = __builtin_fmaf(st_l[w * 16 + r], f, ll);
+                const f32x4 v = *reinterpret_cast<const f32x4*>(
+                    reinterpret_cast<const float*>(lds + w * OWN) + r * DP + d);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = __builtin_fmaf(v[k], f, o[k]);
+            }
+            const int row = row0 + 16 * i + r;
+            if (parts > 1) {
+                const int64_t to = (int64_t)blockIdx.x * min(a.rows, ROWS) + 16 * i + r;
+                *reinterpret_cast<f32x4*>(a.part + to * a.D + d) = o;
+                if (d == 0) {
+                    a.stat[to * 2] = mm;
+                    a.stat[to * 2 + 1] = ll;
+                }
+            } else {
+                cache_attn_out<DT>(a, b, hk, row, d, o, mm, ll);
+            }
+        }
     }
 }
 
 // Join of the parts of a sequence that several workgroups read: a workgroup a
-// (sequence, key head, row tile), 32 lanes a row, 4 values a lane, parts in
-// order.
+// row, its eight groups of 32 lanes (4 values a lane) sum every eighth part,
+// and the eight sums are added in order through LDS.
 template <int DT>
 __global__ __launch_bounds__(256) void cache_attn_join_kernel(CacheAttnArgs x) {
+    __shared__ __attribute__((aligned(16))) f32x4 part[8][32];
+    __shared__ __attribute__((aligned(16))) float sum[8];
+    lds_poison<256>(reinterpret_cast<uint8_t*>(part), sizeof(part));
+    lds_poison<256>(reinterpret_cast<uint8_t*>(sum), sizeof(sum));
     const AttnArgs& a = x.a;
-    const int lane = threadIdx.x & 63;
-    const int hr_n = a.Hk * a.row_tiles, b = blockIdx.x / hr_n, hr = blockIdx.x - b * hr_n;
+    const int lane = threadIdx.x & 63, g = threadIdx.x >> 5, d = (threadIdx.x & 31) * 4;
+    const int rows_tile = min(a.rows, x.tile), hr_n = a.Hk * a.row_tiles;
+    const int br = (int)(blockIdx.x / rows_tile), r = (int)blockIdx.x - br * rows_tile;
+    const int b = br / hr_n, hr = br - b * hr_n;
+    const int hk = hr / a.row_tiles, row = (hr - hk * a.row_tiles) * x.tile + r;
+    if (row >= a.rows) return;
     CacheDivision div;
     div.init(x, lane);
     CachePlace at;
     div.find(x, lane, 0, hr_n, b, &at);
     if (at.parts <= 1) return;   // written where it was read
-    const int hk = hr / a.row_tiles, row0 = (hr - hk * a.row_tiles) * 32;
-    const int rows_tile = min(a.rows, 32), n = min(32, a.rows - row0);
     const int64_t slot = at.slot0 + (int64_t)hr * at.parts;
-    const int d = (threadIdx.x & 31) * 4;
-    for (int r = threadIdx.x >> 5; r < n; r += 8) {
-        float mm = -__builtin_inff();
-        for (int s = threadIdx.x & 31; s < at.parts; s += 32)
-            mm = fmaxf(mm, a.stat[((slot + s) * rows_tile + r) * 2]);
+    const float* stat = a.stat + (slot * rows_tile + r) * 2;
+    const float* from = a.part + (slot * rows_tile + r) * a.D + d;
+    const int64_t pitch = (int64_t)rows_tile * a.D;
+    float mm = -__builtin_inff();
+    for (int s = lane; s < at.parts; s += 64)
+        mm = fmaxf(mm, stat[(int64_t)s * rows_tile * 2]);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) mm = fmaxf(mm, __shfl_xor(mm, o, 64));
-        const float ms = mm == -__builtin_inff() ? 0.0f : mm;
-        float ll = 0.0f;
-        f32x4 o = {0, 0, 0, 0};
-        for (int s = 0; s < at.parts; ++s) {
-            const int64_t from = (slot + s) * rows_tile + r;
-            const float f = __builtin_amdgcn_exp2f(a.stat[from * 2] - ms);
-            ll = __builtin_fmaf(a.stat[from * 2 + 1], f, ll);
-            if (d < a.D) {
-                const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + from * a.D + d);
+    for (int o = 1; o < 64; o <<= 1) mm = fmaxf(mm, __shfl_xor(mm, o, 64));
+    const float ms = mm == -__builtin_inff() ? 0.0f : mm;
+    float ll = 0.0f;
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = g; s < at.parts; s += 8) {
+        const float f = __builtin_amdgcn_exp2f(stat[(int64_t)s * rows_tile * 2] - ms);
+        ll = __builtin_fmaf(stat[(int64_t)s * rows_tile * 2 + 1], f, ll);
+        if (d < a.D) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(from + s * pitch);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], f, o[i]);
-            }
+            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], f, o[i]);
         }
-        if (d < a.D) cache_attn_out<DT>(a, b, hk, row0 + r, d, o, mm, ll);
     }
+    part[g][threadIdx.x & 31] = o;
+    if (d == 0) sum[g] = ll;
+    __syncthreads();
+    if (g != 0 || d >= a.D) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        ll += sum[i];
+        o += part[i][threadIdx.x];
+    }
+    cache_attn_out<DT>(a, b, hk, row, d, o, mm, ll);
 }
 
 }  // namespace igc

@@ -430,7 +430,8 @@ int32_t run_io(const igc_kv_io* p, bool write, void* stream) {
 
 // ------------------------------------------------------------ attention over it
 struct CacheAttnPlan {
-    int64_t row_tiles, slots, groups;   // slots of cache_plan.hpp; workgroups
+    int64_t tile, row_tiles;            // rows a workgroup
+    int64_t slots, groups;              // slots of cache_plan.hpp; workgroups
     int64_t capacity;
     bool split;
     int64_t part_floats, stat_floats;
@@ -462,7 +463,8 @@ CacheAttnPlan cache_attn_plan(const igc_cache_attn* p) {
     CacheAttnPlan x{};
     const igc_kv_cache& c = p->cache;
     const int64_t rows = c.kv_heads ? p->q_len * (p->q_heads / c.kv_heads) : 0;
-    x.row_tiles = ceil_div(rows, 32);
+    x.tile = rows <= 16 ? 16 : 32;
+    x.row_tiles = ceil_div(rows, x.tile);
     x.capacity = p->table_entries * c.page_tokens;
     const int64_t hr = c.kv_heads * x.row_tiles;
     x.slots = hr ? kCacheFill * kNumCUs / hr : 0;
@@ -470,7 +472,7 @@ CacheAttnPlan cache_attn_plan(const igc_cache_attn* p) {
     if (!x.split) x.slots = p->batch;
     x.groups = hr * (x.split ? cache_slots_bound(x.slots, p->batch, x.capacity) : p->batch);
     if (x.split) {
-        const int64_t n = x.groups * (rows < 32 ? rows : 32);
+        const int64_t n = x.groups * (rows < x.tile ? rows : x.tile);
         x.part_floats = n * c.head_dim;
         x.stat_floats = n * 2;
     }
@@ -499,7 +501,7 @@ int32_t check_cache_attn(const igc_cache_attn* p, Tensor* q, Tensor* o, CacheAtt
     if (!aligned(p->lens, 4) || !aligned(p->lse, 4)) return IGC_DECLINE_ALIGNMENT;
     *plan = cache_attn_plan(p);
     if (!launchable(plan->groups, kCacheWaves * 64) ||
-        p->batch * c.kv_heads * plan->row_tiles >= kLim31 / 256)
+        !launchable(p->batch * c.kv_heads * plan->row_tiles, 32 * 256))
         return IGC_DECLINE_SIZE_LIMIT;
     const size_t lb = (size_t)(p->batch * p->q_heads * p->q_len) * 4, bb = (size_t)p->batch * 4;
     const size_t ws = cache_attn_ws(*plan);
@@ -644,6 +646,7 @@ int32_t cache_attn_fwd(const igc_cache_attn* args, void* stream) {
     x.shift = log2_exact(c.page_tokens);
     x.Dp = (int)cache_pitch(c);
     x.causal = args->causal != 0;
+    x.tile = (int)plan.tile;
     x.split = plan.split;
     const hipStream_t st = (hipStream_t)stream;
     Workspace w;

@@ -31,15 +31,21 @@ hipError_t launch_io(const CacheArgs& a, bool write, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int DT, int DP>
+template <int DT, int DP, int RB>
 hipError_t launch_attn(const CacheAttnArgs& x, unsigned groups, hipStream_t stream) {
-    auto kern = cache_attn_kernel<DT, DP, kCacheWaves>;
-    constexpr size_t lds = (size_t)kCacheWaves * (2 * CacheStage<DP>::BYTES + 64 * 4);
+    auto kern = cache_attn_kernel<DT, DP, RB, kCacheWaves>;
+    constexpr size_t lds = (size_t)kCacheWaves * (2 * CacheStage<DP>::BYTES + 32 * 4);
     static LdsAttr attr;
     const hipError_t e = ensure_lds(attr, (const void*)kern, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3(groups), dim3(kCacheWaves * 64), lds, stream, x);
     return hipGetLastError();
+}
+
+template <int DT, int DP>
+hipError_t launch_attn(const CacheAttnArgs& x, unsigned groups, hipStream_t stream) {
+    return x.tile == 16 ? launch_attn<DT, DP, 1>(x, groups, stream)
+                        : launch_attn<DT, DP, 2>(x, groups, stream);
 }
 
 }  // namespace
@@ -77,8 +83,9 @@ hipError_t launch_cache_attn(const CacheAttnArgs& x, unsigned groups, hipStream_
     else e = launch_attn<DT, 128>(x, groups, stream);
     if (e != hipSuccess || !x.split) return e;
     hipLaunchKernelGGL(cache_attn_join_kernel<DT>,
-                       dim3((unsigned)((int64_t)x.a.B * x.a.Hk * x.a.row_tiles)), dim3(256), 0,
-                       stream, x);
+                       dim3((unsigned)((int64_t)x.a.B * x.a.Hk * x.a.row_tiles *
+                                       (x.a.rows < x.tile ? x.a.rows : x.tile))),
+                       dim3(256), 0, stream, x);
     return hipGetLastError();
 }
 

@@ -195,7 +195,7 @@ int32_t kv_cache_read_check(const igc_kv_io* args);
  * order: results do not change from run to run.
  * Limits: as cross_attn_fwd for q and out; the table's capacity below
  * 2^31 - 4096, batch * q_heads below 2^31, batch * kv_heads times the tiles of
- * 32 rows (q_len * q_heads / kv_heads) below 2^23.
+ * 32 rows (q_len * q_heads / kv_heads) below 2^19.
  */
 typedef struct igc_cache_attn {
     igc_kv_cache cache;
