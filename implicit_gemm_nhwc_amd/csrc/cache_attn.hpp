@@ -78,49 +78,61 @@ struct CachePlace {
     int b, hr, part, parts;
     int64_t begin, end;
     int len;
-    int64_t slot0;         // slot of part 0
+    int slot0;             // slot of part 0 of the sequence's first (key head, row tile)
 };
+
+// Sum of x over the lanes up to this one.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+    // within rows of 16 lanes, then the rows before
+#define IGC_STEP(ctrl, rows) \
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, rows, 0xf, false)
+    IGC_STEP(0x111, 0xf);   // row_shr:1
+    IGC_STEP(0x112, 0xf);
+    IGC_STEP(0x114, 0xf);
+    IGC_STEP(0x118, 0xf);
+    IGC_STEP(0x142, 0xa);   // row_bcast:15 to rows 1 and 3
+    IGC_STEP(0x143, 0xc);   // row_bcast:31 to rows 2 and 3
+#undef IGC_STEP
+    return x;
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
+}
 
 // Division of the work, by whole waves: every wave forms it.
 struct CacheDivision {
-    int64_t chunk;
+    uint32_t chunk;
+    int first;             // the lane's length, of the first 64 sequences
     __device__ __forceinline__ int len(const CacheAttnArgs& x, int b) const {
-        return cache_len(x.lens[b], x.capacity);
+        return b < x.a.B ? cache_len(x.lens[b], x.capacity) : 0;
     }
     __device__ __forceinline__ void init(const CacheAttnArgs& x, int lane) {
-        int64_t total = 0;
-        for (int b = lane; b < x.a.B; b += 64) total += cache_units(len(x, b));
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) total += __shfl_xor(total, o, 64);
-        chunk = cache_chunk(total, x.slots, x.a.B);
+        first = len(x, lane);
+        uint32_t total = lane_value(wave_scan(cache_units(first)), 63);
+        for (int base = 64; base < x.a.B; base += 64)
+            total += lane_value(wave_scan(cache_units(len(x, base + lane))), 63);
+        chunk = cache_chunk(total, (uint32_t)x.slots, (uint32_t)x.a.B);
     }
-    // parts of sequence `b` and of those before it; returns the first
-    // sequence whose parts reach past `slot` (in parts, not workgroups) when
-    // b < 0
-    __device__ __forceinline__ bool find(const CacheAttnArgs& x, int lane, int64_t w, int hr_n,
+    // The sequence that workgroup w works on (b < 0), or sequence b: its
+    // parts, length and first slot.  False for workgroups past the last part.
+    __device__ __forceinline__ bool find(const CacheAttnArgs& x, int lane, uint32_t w, int hr_n,
                                          int b, CachePlace* o) const {
-        int64_t before = 0;
+        uint32_t before = 0;
         for (int base = 0; base < x.a.B; base += 64) {
-            const int mine = base + lane;
-            const int n = mine < x.a.B ? len(x, mine) : 0;
-            int64_t k = mine < x.a.B ? cache_parts(n, chunk) : 0, sum = k;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int64_t up = __shfl_up(sum, d, 64);
-                if (lane >= d) sum += up;
-            }
-            const uint64_t here = b >= 0 ? (b >= base && b < base + 64 ? 1ull << (b - base) : 0)
+            const int n = base ? len(x, base + lane) : first;
+            const uint32_t k = base + lane < x.a.B ? cache_parts(n, chunk) : 0;
+            const uint32_t sum = wave_scan(k);
+            const uint64_t here = b >= 0 ? (b < base + 64 ? 1ull << (b - base) : 0)
                                          : __ballot(w < (before + sum) * hr_n && k > 0);
             if (here) {
                 const int f = __builtin_ctzll(here);
                 o->b = base + f;
-                o->parts = (int)__shfl(k, f, 64);
-                o->len = __shfl(n, f, 64);
-                before += __shfl(sum, f, 64) - o->parts;
-                o->slot0 = before * hr_n;
+                o->parts = (int)lane_value(k, f);
+                o->len = (int)lane_value((uint32_t)n, f);
+                o->slot0 = (int)((before + lane_value(sum, f) - o->parts) * hr_n);
                 return true;
             }
-            before += __shfl(sum, 63, 64);
+            before += lane_value(sum, 63);
         }
         return false;
     }
@@ -257,11 +269,11 @@ __global__ __launch_bounds__(NW * 64, RB == 1 ? 4 : 2) void cache_attn_kernel(Ca
         CacheDivision div;
         div.init(x, lane);
         if (!div.find(x, lane, blockIdx.x, hr_n, -1, &at)) return;   // all waves
-        const int r = (int)((int64_t)blockIdx.x - at.slot0);
+        const int r = (int)blockIdx.x - at.slot0;
         at.hr = r / at.parts;
         at.part = r - at.hr * at.parts;
-        at.begin = at.part * div.chunk * kCacheUnit;
-        at.end = at.begin + div.chunk * kCacheUnit;
+        at.begin = (int64_t)at.part * div.chunk * kCacheUnit;
+        at.end = at.begin + (int64_t)div.chunk * kCacheUnit;
         if (at.end > at.len) at.end = at.len;
     } else {
         at.b = blockIdx.x / hr_n;
@@ -563,7 +575,7 @@ __global__ __launch_bounds__(256) void cache_attn_join_kernel(CacheAttnArgs x) {
     CachePlace at;
     div.find(x, lane, 0, hr_n, b, &at);
     if (at.parts <= 1) return;   // written where it was read
-    const int64_t slot = at.slot0 + (int64_t)hr * at.parts;
+    const int64_t slot = at.slot0 + hr * at.parts;
     const float* stat = a.stat + (slot * rows_tile + r) * 2;
     const float* from = a.part + (slot * rows_tile + r) * a.D + d;
     const int64_t pitch = (int64_t)rows_tile * a.D;

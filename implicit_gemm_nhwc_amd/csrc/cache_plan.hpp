@@ -37,22 +37,26 @@ IGC_HD inline int cache_len(int len, int64_t capacity) {
 // only, so c comes from them there: with `slots` workgroups a (key head, row
 // tile) over all sequences, c = ceil(sum n_b / (slots - B)) leaves at most
 // `slots` of them, of equal length but for each sequence's last.  slots < 2 B:
-// one workgroup each.
+// one workgroup each.  With slots up to 512, B is at most 256 where there is
+// a division, and sum n_b stays below 2^32.
 constexpr int kCacheUnit = 256;    // keys a round of a workgroup's waves
 constexpr int kCacheLeast = 2;     // units a split at least
+constexpr int kCacheMostSlots = 512;
 
-IGC_HD inline int64_t cache_units(int len) { return ((int64_t)len + kCacheUnit - 1) / kCacheUnit; }
+IGC_HD inline uint32_t cache_units(int len) {
+    return ((uint32_t)len + (kCacheUnit - 1)) / kCacheUnit;
+}
 
 IGC_HD inline bool cache_splits(int64_t slots, int64_t batch) { return slots >= 2 * batch; }
 
 // c from the sum of the units.
-IGC_HD inline int64_t cache_chunk(int64_t total, int64_t slots, int64_t batch) {
-    const int64_t c = (total + (slots - batch) - 1) / (slots - batch);
+IGC_HD inline uint32_t cache_chunk(uint32_t total, uint32_t slots, uint32_t batch) {
+    const uint32_t per = slots - batch, c = total / per + (total % per != 0);
     return c < kCacheLeast ? kCacheLeast : c;
 }
 
-IGC_HD inline int64_t cache_parts(int len, int64_t chunk) {
-    const int64_t n = (cache_units(len) + chunk - 1) / chunk;
+IGC_HD inline uint32_t cache_parts(int len, uint32_t chunk) {
+    const uint32_t n = (cache_units(len) + (chunk - 1)) / chunk;
     return n < 1 ? 1 : n;
 }
 

@@ -22,9 +22,9 @@ int64_t row(int id, int heads, int head, int64_t p, int shift) {
 }
 int len(int n, int64_t capacity) { return igc::cache_len(n, capacity); }
 int splits(int64_t slots, int64_t b) { return igc::cache_splits(slots, b); }
-int64_t units(int n) { return igc::cache_units(n); }
-int64_t chunk(int64_t total, int64_t slots, int64_t b) { return igc::cache_chunk(total, slots, b); }
-int64_t parts(int n, int64_t chunk) { return igc::cache_parts(n, chunk); }
+uint32_t units(int n) { return igc::cache_units(n); }
+uint32_t chunk(uint32_t total, uint32_t slots, uint32_t b) { return igc::cache_chunk(total, slots, b); }
+uint32_t parts(int n, uint32_t chunk) { return igc::cache_parts(n, chunk); }
 int64_t bound(int64_t slots, int64_t b, int64_t cap) { return igc::cache_slots_bound(slots, b, cap); }
 }
 """
@@ -43,10 +43,11 @@ def plan(tmp_path_factory):
     L.row.argtypes, L.row.restype = [ctypes.c_int] * 3 + [i64, ctypes.c_int], i64
     L.len.argtypes = [ctypes.c_int, i64]
     L.splits.argtypes = [i64, i64]
-    L.units.argtypes, L.units.restype = [ctypes.c_int], i64
-    for n in ("chunk", "bound"):
-        getattr(L, n).argtypes, getattr(L, n).restype = [i64] * 3, i64
-    L.parts.argtypes, L.parts.restype = [ctypes.c_int, i64], i64
+    u32 = ctypes.c_uint32
+    L.units.argtypes, L.units.restype = [ctypes.c_int], u32
+    L.chunk.argtypes, L.chunk.restype = [u32] * 3, u32
+    L.bound.argtypes, L.bound.restype = [i64] * 3, i64
+    L.parts.argtypes, L.parts.restype = [ctypes.c_int, u32], u32
     return L
 
 
@@ -85,10 +86,10 @@ def test_division(plan):
             assert room == b
             continue
         total = sum(plan.units(n) for n in lens)
+        assert total < 1 << 32
         c = plan.chunk(total, slots, b)
         assert c >= 2 and (c == 2 or (c - 1) * (slots - b) < total)
         parts = [plan.parts(n, c) for n in lens]
-        assert sum(parts) <= min(slots, room) or sum(parts) <= room
         assert sum(parts) <= room
         for n, k in zip(lens, parts):
             assert k >= 1
