@@ -261,7 +261,7 @@ int32_t check_quant(const igc_quantize_rows* p, Rows* x, Rows* q) {
 LinForm lin_form(const igc_linear_i8* p) {
     if (p->m <= kFewRows) return {0, 1, ceil_div(p->n, 16), kFewWaves * 64};
     for (int tile : {256, 128}) {
-        const LinForm f{tile, ceil_div(p->m, tile), ceil_div(p->n, tile), tile == 256 ? 512 : 256};
+        const LinForm f{tile, ceil_div(p->m, tile), ceil_div(p->n, tile), 256};
         if (f.tiles_m * f.tiles_n >= kNumCUs) return f;
     }
     return {64, ceil_div(p->m, 64), ceil_div(p->n, 64), 256};

@@ -16,15 +16,15 @@ hipError_t launch_few(const LinArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int DT, int B, int WM, int WN>
+template <int DT, int B>
 hipError_t launch_tile(const LinArgs& a, hipStream_t stream) {
-    auto kern = linear_i8_tile_kernel<DT, B, B, WM, WN>;
-    constexpr size_t lds = 4 * (size_t)B * kLinKT;
+    auto kern = linear_i8_tile_kernel<DT, B>;
+    constexpr size_t lds = 2 * (size_t)kLinStages * B * kLinKT;
     static LdsAttr attr;
     const hipError_t e = ensure_lds(attr, (const void*)kern, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)), dim3(WM * WN * 64),
-                       lds, stream, a);
+    hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)), dim3(256), lds,
+                       stream, a);
     return hipGetLastError();
 }
 
@@ -32,9 +32,9 @@ hipError_t launch_tile(const LinArgs& a, hipStream_t stream) {
 
 template <int DT>
 hipError_t launch_linear_i8(const LinArgs& a, int tile, hipStream_t stream) {
-    if (tile == 256) return launch_tile<DT, 256, 2, 4>(a, stream);
-    if (tile == 128) return launch_tile<DT, 128, 2, 2>(a, stream);
-    if (tile == 64) return launch_tile<DT, 64, 2, 2>(a, stream);
+    if (tile == 256) return launch_tile<DT, 256>(a, stream);
+    if (tile == 128) return launch_tile<DT, 128>(a, stream);
+    if (tile == 64) return launch_tile<DT, 64>(a, stream);
     if (a.M <= 16) return launch_few<DT, 1>(a, stream);
     if (a.M <= 32) return launch_few<DT, 2>(a, stream);
     return launch_few<DT, 4>(a, stream);

@@ -6,8 +6,8 @@
 // owns one row of y and neighbouring columns.  The integer sums are exact; they
 // are scaled in fp32 and rounded once.
 //
-// The tile kernel stages 128 k of its rows and columns in LDS by direct loads,
-// double buffered; the few-rows kernel, which the weights' bytes bound, takes
+// The tile kernel stages 64 k of its rows and columns in LDS by direct loads,
+// three stages deep; the few-rows kernel, which the weights' bytes bound, takes
 // 16 columns a workgroup, gives each wave a part of k and reads both operands
 // straight into registers.
 #pragma once
@@ -134,113 +134,196 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_i8_few_kernel(LinArgs a
 }
 
 // ---------------------------------------------------------------------------
-// Tiles of BM rows of x and BN of w, WM x WN waves.
-constexpr int kLinKT = 128;   // k a tile, bytes
-template <int DT, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64) void linear_i8_tile_kernel(LinArgs a) {
-    constexpr int NW = WM * WN, MB = BM / WM / 32, NB = BN / WN / 32;
-    constexpr int XT = BM * kLinKT, WT = BN * kLinKT;
-    constexpr int XP = XT / 1024 / NW, WP = WT / 1024 / NW;   // loads a wave
-    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];   // 2 x {x, w}
-    lds_poison<NW * 64>(lds, 2 * (XT + WT));
+// Square tiles of B rows of x and B of w, four waves of a quarter each.  A
+// stage is 64 k of all rows; kLinStages of them are under way or being read,
+// because a stage takes more than one of its times to arrive.  A step is 32 k:
+// the fragments of the next one are read while its products run, and a stage's
+// last step reads the next stage's first, so that the matrix cores see no
+// seam.  One barrier a stage: behind it the next stage is whole, and the one
+// just read may be overwritten.
+constexpr int kLinKT = 64, kLinStages = 3;
+
+template <int DT, int B>
+__global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(LinArgs a) {
+    constexpr int NW = 4, MB = B / 64;   // blocks of 32 a wave, each way
+    constexpr int T = B * kLinKT, P = T / 1024 / NW;   // bytes, loads a wave of one operand
+    constexpr int NS = kLinStages;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];   // NS x {x, w}
+    lds_poison<NW * 64>(lds, NS * 2 * T);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int wm = wave / WN, wn = wave % WN, half = lane >> 5;
+    const int wm = wave >> 1, wn = wave & 1, half = lane >> 5;
 
     // an XCD's run of tiles goes through bands of 8 tiles of x, column by
     // column: the workgroups that run at once share both operands in its L2
     const int tile = xcd_remap(blockIdx.x, gridDim.x);
     const int band = tile / (8 * a.tiles_n), rows = min(8, a.tiles_m - 8 * band);
     const int in = tile - band * 8 * a.tiles_n;
-    const int m0 = (8 * band + in % rows) * BM, n0 = in / rows * BN;
-
+    const int m0 = (8 * band + in % rows) * B, n0 = in / rows * B;
     const __amdgpu_buffer_rsrc_t xr = lin_rsrc(
-        a.x + m0 * a.x_p, lin_bytes(min(BM, a.M - m0), a.x_p, a.K16));
+        a.x + m0 * a.x_p, lin_bytes(min(B, a.M - m0), a.x_p, a.K16));
     const __amdgpu_buffer_rsrc_t wr = lin_rsrc(
-        a.w + n0 * a.w_p, lin_bytes(min(BN, a.N - n0), a.w_p, a.K16));
-    // a piece is 8 rows; the 16-byte chunk c of row r lies at c ^ (r % 8)
-    const int chunk = (lane & 7) ^ (lane >> 3);
-    const unsigned xo = (unsigned)((lane >> 3) * a.x_p) + 16 * chunk;
-    const unsigned wo = (unsigned)((lane >> 3) * a.w_p) + 16 * chunk;
-    auto issue = [&](int k, uint8_t* to) {
-        typedef __attribute__((address_space(3))) void* lp;
-        const bool in_k = k + 16 * chunk < a.K;   // w's bytes past K meet zeros of x
-#pragma unroll
-        for (int i = 0; i < XP; ++i) {
-            const int p = wave * XP + i;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                xr, (lp)(to + p * 1024), 16, in_k ? xo + (unsigned)(8 * p * a.x_p) + k : kOut, 0,
-                0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < WP; ++i) {
-            const int p = wave * WP + i;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                wr, (lp)(to + XT + p * 1024), 16, wo + (unsigned)(8 * p * a.w_p) + k, 0, 0, 0);
+        a.w + n0 * a.w_p, lin_bytes(min(B, a.N - n0), a.w_p, a.K16));
+
+    // a load is 16 rows; the 16-byte chunk c of row r lies at c ^ (r / 4 % 4),
+    // which spreads a chunk of 16 rows over all banks
+    const int chunk = (lane & 3) ^ (lane >> 4);
+    const unsigned xo = (unsigned)((16 * wave * P + (lane >> 2)) * a.x_p) + 16 * chunk;
+    const unsigned wo = (unsigned)((16 * wave * P + (lane >> 2)) * a.w_p) + 16 * chunk;
+    const unsigned x16 = (unsigned)(16 * a.x_p), w16 = (unsigned)(16 * a.w_p);
+    typedef __attribute__((address_space(3))) void* lp;
+    auto issue_x = [&](int k, uint8_t* to, int i) {
+        const unsigned at = k + 16 * chunk < a.K ? xo + k : kOut;   // zeros past K
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lp)(to + (wave * P + i) * 1024), 16,
+                                                 at + i * x16, 0, 0, 0);
+    };
+    auto issue_w = [&](int k, uint8_t* to, int i) {   // past K anything: it meets zeros
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lp)(to + T + (wave * P + i) * 1024), 16,
+                                                 wo + k + i * w16, 0, 0, 0);
+    };
+    // This wave's part of the stage at k is here: all of it, for all waves, is.
+    // (A bare barrier: __syncthreads would wait for the later stages too.)
+    auto barrier = [&] {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    auto arrived = [&](int k, uint8_t* at) {
+        barrier();
+        if (a.K - k < kLinKT && a.K > k && a.K != a.K16) {
+            // x's bytes past K in its last chunk become zeros
+            for (int r = threadIdx.x; r < B; r += NW * 64) {
+                i32x4* c = reinterpret_cast<i32x4*>(
+                    at + r * kLinKT + ((((a.K - k) >> 4) ^ (r >> 2 & 3)) << 4));
+                *c = lin_clear(*c, (a.K - k) & 15);
+            }
+            barrier();
         }
     };
-    i32x16 acc[MB][NB];
+    i32x4 xf[2][MB], wf[2][MB];
+    // rows of a block start at multiples of 32
+    const int turn = lane >> 2 & 3;
+    const uint8_t* xl = lds + (wm * MB * 32 + (lane & 31)) * kLinKT;
+    const uint8_t* wl = lds + T + (wn * MB * 32 + (lane & 31)) * kLinKT;
+    auto read = [&](int buf, int s, int set, int i) {
+        const int c = buf * 2 * T + (((2 * s + half) ^ turn) << 4);   // buf: the stage's place
+        wf[set][i] = *reinterpret_cast<const i32x4*>(wl + c + i * 32 * kLinKT);
+        xf[set][i] = *reinterpret_cast<const i32x4*>(xl + c + i * 32 * kLinKT);
+    };
+    i32x16 acc[MB][MB];
+    // Products of one step, and between them the reads of the next one and a
+    // stage's loads of one operand (P = MB): in a burst the loads would hold up
+    // the products behind them.
+    auto step = [&](int set, int next_buf, int next_s, auto load) {
+        static_assert(P == MB, "a load a row of products");
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            read(next_buf, next_s, set ^ 1, i);
+            load(i);
+#pragma unroll
+            for (int j = 0; j < MB; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[set][j], xf[set][i],
+                                                                  acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    int buf = 0, old = NS - 1;   // the stage being read, and the one before it
+    if (a.K > 0) {   // stages past K are loaded too (zeros), and not read
+#pragma unroll
+        for (int n = 0; n < NS - 1; ++n)
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                issue_x(n * kLinKT, lds + n * 2 * T, i);
+                issue_w(n * kLinKT, lds + n * 2 * T, i);
+            }
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * 2 * P) : "memory");
+        arrived(0, lds);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            issue_x((NS - 1) * kLinKT, lds + (NS - 1) * 2 * T, i);
+            read(0, 0, 0, i);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
+        for (int j = 0; j < MB; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-    if (a.K > 0) issue(0, lds);
-    int buf = 0;
     for (int k = 0; k < a.K; k += kLinKT) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        uint8_t* xl = lds + buf * (XT + WT);
-        const uint8_t* wl = xl + XT;
-        if (k + kLinKT < a.K) {
-            issue(k + kLinKT, lds + (buf ^ 1) * (XT + WT));
-        } else if (a.K != a.K16) {
-            // x's bytes past K in its last chunk become zeros
-            for (int r = threadIdx.x; r < BM; r += NW * 64) {
-                i32x4* c = reinterpret_cast<i32x4*>(
-                    xl + r * kLinKT + ((((a.K - k) >> 4) ^ (r & 7)) << 4));
-                *c = lin_clear(*c, (a.K - k) & 15);
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int s = 0; s < kLinKT / 32; ++s) {
-            i32x4 xf[MB], wf[NB];
-            const int c = 2 * s + half;
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int r = (wn * NB + j) * 32 + (lane & 31);
-                wf[j] = *reinterpret_cast<const i32x4*>(wl + r * kLinKT + ((c ^ (r & 7)) << 4));
-            }
-#pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                const int r = (wm * MB + i) * 32 + (lane & 31);
-                xf[i] = *reinterpret_cast<const i32x4*>(xl + r * kLinKT + ((c ^ (r & 7)) << 4));
-            }
-#pragma unroll
-            for (int i = 0; i < MB; ++i)
-#pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[j], xf[i], acc[i][j], 0,
-                                                                      0, 0);
-        }
-        buf ^= 1;
+        step(0, buf, 1, [&](int i) { issue_w(k + (NS - 1) * kLinKT, lds + old * 2 * T, i); });
+        // the last step's fragments and the next stage
+        asm volatile("s_waitcnt lgkmcnt(0) vmcnt(%0)" ::"n"((NS - 2) * 2 * P) : "memory");
+        old = buf;
+        buf = buf + 1 < NS ? buf + 1 : 0;
+        arrived(k + kLinKT, lds + buf * 2 * T);
+        step(1, buf, 0, [&](int i) { issue_x(k + NS * kLinKT, lds + old * 2 * T, i); });
     }
-    // register 4 g + r of half h is column 8 g + 4 h + r of the block
+    // nothing may be under way to LDS when the workgroup ends
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // Scales and bias of the columns go through LDS, and the results too, 32
+    // rows of a wave at a time, so that whole lines are stored.
+    barrier();
+    float* col = reinterpret_cast<float*>(lds);   // [2][B]
+    for (int c = threadIdx.x; c < B; c += NW * 64) {
+        const int n = min(n0 + c, a.N - 1);
+        col[c] = a.ws[n];
+        col[B + c] = a.bias ? a.bias[n] : 0.0f;
+    }
+    __syncthreads();
+    constexpr int CH = MB * 4, RL = 64 / CH;   // 16-byte chunks of a row; rows a store
+    uint8_t* out = lds + 2 * B * 4 + wave * (32 * CH * 16);
+    const bool inner = m0 + B <= a.M && n0 + B <= a.N;
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-        const int m = m0 + (wm * MB + i) * 32 + (lane & 31);
-        if (m < a.M) {
+        const int mb = m0 + (wm * MB + i) * 32, nb = n0 + wn * MB * 32;
+        const int r = lane & 31;
+        const float xs = a.xs[min(mb + r, a.M - 1)];
+        // register 4 g + e of half h is column 8 g + 4 h + e of a block; the
+        // halves exchange groups, so that each lane holds 8 neighbouring
+        // columns: half h the groups h and 2 + h
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
+        for (int j = 0; j < MB; ++j)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int n = n0 + (wn * NB + j) * 32 + 8 * g + 4 * half;
-                    const int v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1],
-                                      acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-                    if (n < a.N) lin_store4<DT>(a, m, n, v);
+            for (int gg = 0; gg < 2; ++gg) {
+                const float* c = col + (wn * MB + j) * 32 + 16 * gg + 4 * half;
+                uint32_t v[4];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const f32x4 ws = *reinterpret_cast<const f32x4*>(c + 8 * g);
+                    const f32x4 bs = *reinterpret_cast<const f32x4*>(c + B + 8 * g);
+                    float f[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        f[e] = __builtin_fmaf((float)acc[i][j][8 * gg + 4 * g + e] * xs, ws[e],
+                                              bs[e]);
+                    v[2 * g] = pack_out2(f[0], f[1], DT);
+                    v[2 * g + 1] = pack_out2(f[2], f[3], DT);
                 }
+                const auto p = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+                const auto q = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+                const int ch = 4 * j + 2 * gg + half;
+                *reinterpret_cast<u32x4*>(out + (r * CH + (ch ^ (r & (CH - 1)))) * 16) =
+                    u32x4{p[0], q[0], p[1], q[1]};
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's own rows
+#pragma unroll
+        for (int t = 0; t < 32 / RL; ++t) {
+            const int row = t * RL + lane / CH, ch = lane % CH;
+            const u32x4 o = *reinterpret_cast<const u32x4*>(
+                out + (row * CH + (ch ^ (row & (CH - 1)))) * 16);
+            const int m = mb + row, n = nb + 8 * ch;
+            uint8_t* y = a.y + (int64_t)m * a.y_p + 2 * (int64_t)n;
+            if (inner) {
+                *reinterpret_cast<u32x4h*>(y) = o;
+            } else if (m < a.M) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (n + e < a.N)
+                        *reinterpret_cast<uint16_t*>(y + 2 * e) =
+                            (uint16_t)(o[e / 2] >> (16 * (e & 1)));
+            }
         }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
 
