@@ -15,20 +15,40 @@ namespace igc {
 constexpr int kLnMaxChannels = 16384;
 
 // Form of the layer norm kernels for C channels: lanes a row, chunks of 8
-// values a lane, threads a workgroup.
+// values a lane, threads a workgroup.  Two or three chunks a lane leave the
+// fewest lanes without work (154 MB: 54 to 58 us forward and 92 to 96 backward
+// wherever the row fills them; 768 channels on 32 lanes x 3 58 and 95, on 64 x 2
+// 73 and 103; 512 on 32 x 2 54 and 94, on 64 x 1 62 and 109, on 16 x 4 58 and
+// 104).  Past 2048 channels a workgroup takes a row (4096: 65 and 104; 8192:
+// 74 and 122).
 struct LnForm {
     int lanes, chunks, threads;
 };
 constexpr LnForm ln_form(int c) {
     if (c <= 64) return {8, 1, 256};
-    if (c <= 128) return {16, 1, 256};
-    if (c <= 256) return {32, 1, 256};
-    if (c <= 512) return {64, 1, 256};
-    if (c <= 1024) return {64, 2, 256};
-    if (c <= 2048) return {64, 4, 256};
+    if (c <= 2048) {
+        int lanes = 8;
+        while (lanes * 16 < c) lanes *= 2;   // two chunks a lane
+        if (lanes > 8 && lanes * 12 >= c) return {lanes / 2, 3, 256};
+        return lanes > 64 ? LnForm{64, 4, 256} : LnForm{lanes, 2, 256};
+    }
     if (c <= 4096) return {256, 2, 256};
+    if (c <= 6144) return {256, 3, 256};
     if (c <= 8192) return {256, 4, 256};
     return {512, 4, 512};
+}
+// What ln_form returns.
+#define IGC_LN_FORMS(F) \
+    F(8, 1, 256) F(8, 2, 256) F(8, 3, 256) F(16, 2, 256) \
+    F(16, 3, 256) F(32, 2, 256) F(32, 3, 256) F(64, 2, 256) \
+    F(64, 3, 256) F(64, 4, 256) F(256, 2, 256) \
+    F(256, 3, 256) F(256, 4, 256) F(512, 4, 512)
+
+// Workgroups a CU of the backward pass: with four chunks (three on many lanes)
+// the registers hold two well (2048 channels: 96 us, three 109; 1536: 92 and
+// 97; 320 on 16 x 3 101 and 95).
+constexpr int ln_bwd_fill(const LnForm& f) {
+    return f.chunks == 4 || (f.chunks == 3 && f.lanes >= 32 && f.lanes <= 64) ? 2 : 3;
 }
 
 template <int DT>

@@ -140,7 +140,7 @@ int32_t check_ln_shape(const igc_layer_norm* p) {
 int64_t ln_blocks(const igc_layer_norm* p) {
     const LnForm f = ln_form((int)p->channels);
     const int64_t tiles = ceil_div(ln_rows(p), f.threads / f.lanes);
-    const int64_t rounds = ceil_div(tiles, 3 * kNumCUs);
+    const int64_t rounds = ceil_div(tiles, ln_bwd_fill(f) * kNumCUs);
     return rounds ? ceil_div(tiles, rounds) : 0;
 }
 

@@ -54,15 +54,13 @@ template <int DT>
 hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t stream) {
     if (a.C > kLnMaxChannels) return launch_quant<DT, 512, 4, 512, true>(a, stream);
     const LnForm f = ln_form(a.C);
-    if (f.lanes == 8) return launch_quant<DT, 8, 1, 256>(a, stream);
-    if (f.lanes == 16) return launch_quant<DT, 16, 1, 256>(a, stream);
-    if (f.lanes == 32) return launch_quant<DT, 32, 1, 256>(a, stream);
-    if (f.lanes == 64 && f.chunks == 1) return launch_quant<DT, 64, 1, 256>(a, stream);
-    if (f.lanes == 64 && f.chunks == 2) return launch_quant<DT, 64, 2, 256>(a, stream);
-    if (f.lanes == 64) return launch_quant<DT, 64, 4, 256>(a, stream);
-    if (f.lanes == 256 && f.chunks == 2) return launch_quant<DT, 256, 2, 256>(a, stream);
-    if (f.lanes == 256) return launch_quant<DT, 256, 4, 256>(a, stream);
-    return launch_quant<DT, 512, 4, 512>(a, stream);
+    hipError_t e = hipErrorInvalidValue;
+#define IGC_FORM(LANES, CHUNKS, THREADS)        \
+    if (f.lanes == LANES && f.chunks == CHUNKS) \
+        e = launch_quant<DT, LANES, CHUNKS, THREADS>(a, stream);
+    IGC_LN_FORMS(IGC_FORM)
+#undef IGC_FORM
+    return e;
 }
 
 template <int DT>

@@ -29,16 +29,12 @@ template <int DT>
 hipError_t launch_layer_norm(const LnArgs& a, bool backward, hipStream_t stream) {
     if (a.rows > 0) {
         const LnForm f = ln_form(a.C);
-        hipError_t e;
-        if (f.lanes == 8) e = launch<DT, 8, 1, 256>(a, backward, stream);
-        else if (f.lanes == 16) e = launch<DT, 16, 1, 256>(a, backward, stream);
-        else if (f.lanes == 32) e = launch<DT, 32, 1, 256>(a, backward, stream);
-        else if (f.lanes == 64 && f.chunks == 1) e = launch<DT, 64, 1, 256>(a, backward, stream);
-        else if (f.lanes == 64 && f.chunks == 2) e = launch<DT, 64, 2, 256>(a, backward, stream);
-        else if (f.lanes == 64) e = launch<DT, 64, 4, 256>(a, backward, stream);
-        else if (f.lanes == 256 && f.chunks == 2) e = launch<DT, 256, 2, 256>(a, backward, stream);
-        else if (f.lanes == 256) e = launch<DT, 256, 4, 256>(a, backward, stream);
-        else e = launch<DT, 512, 4, 512>(a, backward, stream);
+        hipError_t e = hipErrorInvalidValue;
+#define IGC_FORM(LANES, CHUNKS, THREADS)           \
+    if (f.lanes == LANES && f.chunks == CHUNKS)    \
+        e = launch<DT, LANES, CHUNKS, THREADS>(a, backward, stream);
+        IGC_LN_FORMS(IGC_FORM)
+#undef IGC_FORM
         if (e != hipSuccess) return e;
     }
     if (!backward || !(a.dw || a.db)) return hipSuccess;
