@@ -348,9 +348,13 @@ int32_t check_table(const int32_t* table, int64_t batch, int64_t stride, int64_t
     return IGC_OK;
 }
 
-// Lane groups that a launch of kv_cache_write / read takes for keys or values.
-int64_t io_items(const igc_kv_io* p) {
-    return p->batch * p->tokens * ceil_div(p->cache.kv_heads, kCacheHeads);
+// Runs of tokens that a workgroup of kv_cache_write / read takes, a sequence;
+// workgroups of a launch.
+int64_t io_runs(const igc_kv_io* p) {
+    return ceil_div(p->tokens, cache_run(qk_lanes((int)p->cache.head_dim)));
+}
+int64_t io_groups(const igc_kv_io* p) {
+    return p->batch * io_runs(p) * 2 * ceil_div(p->cache.kv_heads, kCacheHeads);
 }
 
 int32_t check_io(const igc_kv_io* p, bool write, Tensor t[2]) {
@@ -363,8 +367,7 @@ int32_t check_io(const igc_kv_io* p, bool write, Tensor t[2]) {
     const igc_kv_cache& c = p->cache;
     const int64_t hc = ceil_div(c.kv_heads, kCacheHeads);
     if (hc && p->batch * p->tokens > ((int64_t)1 << 40) / hc) return IGC_DECLINE_SIZE_LIMIT;
-    const int64_t per = kCacheThreads / qk_lanes((int)c.head_dim);
-    if (!launchable(2 * ceil_div(io_items(p), per), kCacheThreads)) return IGC_DECLINE_SIZE_LIMIT;
+    if (!launchable(io_groups(p), kCacheThreads)) return IGC_DECLINE_SIZE_LIMIT;
     const igc_attn_view* v[2] = {&p->k, &p->v};
     for (int i = 0; i < 2; ++i)
         if ((r = check_view(*v[i], p->batch, p->tokens, c.kv_heads, c.head_dim, !write,
@@ -372,7 +375,7 @@ int32_t check_io(const igc_kv_io* p, bool write, Tensor t[2]) {
             return r;
     size_t tb;
     if ((r = check_table(p->table, p->batch, p->table_stride, p->table_entries, &tb))) return r;
-    if (io_items(p) == 0) return IGC_OK;
+    if (io_groups(p) == 0) return IGC_OK;
     if (!p->start) return IGC_DECLINE_NULL_POINTER;
     if (!aligned(p->start, 4) || !aligned(p->lens, 4)) return IGC_DECLINE_ALIGNMENT;
     const size_t bb = (size_t)p->batch * 4;
@@ -395,7 +398,7 @@ int32_t check_io(const igc_kv_io* p, bool write, Tensor t[2]) {
 int32_t run_io(const igc_kv_io* p, bool write, void* stream) {
     Tensor t[2];
     if (check_io(p, write, t) != IGC_OK) return 0;
-    if (io_items(p) == 0) return 1;
+    if (io_groups(p) == 0) return 1;
     const igc_kv_cache& c = p->cache;
     CacheArgs a{};
     a.pool[0] = c.k;
@@ -418,7 +421,7 @@ int32_t run_io(const igc_kv_io* p, bool write, void* stream) {
     a.D = (int)c.head_dim;
     a.Dp = (int)cache_pitch(c);
     a.hc = (int)ceil_div(c.kv_heads, kCacheHeads);
-    a.items = io_items(p);
+    a.runs = (int)io_runs(p);
     a.entries = (int)p->table_entries;
     a.pages = (int)c.pages;
     a.shift = log2_exact(c.page_tokens);

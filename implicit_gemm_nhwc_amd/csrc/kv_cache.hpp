@@ -3,9 +3,11 @@
 // Pages hold [kv heads][page tokens][D rounded up to 16] integers and
 // [kv heads][page tokens] scales: the rows that one head's attention walks lie
 // side by side.  Both kernels are bound by HBM.  LPR lanes of 8 values take a
-// row; a lane group takes the same token of up to four heads, neighbouring
-// groups neighbouring tokens, so that a wave reads whole heads of a token and
-// writes runs of a page.
+// row; a lane group takes a token of up to four heads, a workgroup a run of
+// tokens of them.  Workgroups that follow one another take the other heads of
+// the same tokens, and then their values: together they go through whole rows
+// of the 16-bit tensors (16 x 4096 tokens written and read, 8 heads of 128: 151
+// us; keys first, and heads by fours, 162).
 #pragma once
 
 #include "cache_plan.hpp"
@@ -23,28 +25,34 @@ struct CacheArgs {
     const int32_t* lens;   // tokens of each sequence, or null (T)
     int64_t table_stride;
     int B, T, H, D, Dp;
-    int hc;                // lane groups a token: ceil(H / kCacheHeads)
-    int64_t items;         // B * hc * T
+    int hc;                // workgroups a run of tokens: ceil(H / kCacheHeads)
+    int runs;              // runs of tokens a sequence
     int entries, pages, shift;
 };
 
 constexpr int kCacheHeads = 4, kCacheThreads = 256;
 
-// What a lane group works on: heads h0 .. h0 + nh - 1 of token t of sequence b,
-// at position p of page `id` (-1: none).  `given` is false for tokens past the
-// sequence's length.
+// Tokens a workgroup (of lpr lanes a row).
+constexpr int cache_run(int lpr) { return kCacheThreads / lpr; }
+
+// What a lane group works on: heads h0 .. h0 + nh - 1 of the keys (0) or values
+// of token t of sequence b, at position p of page `id` (-1: none).  `given` is
+// false for tokens past the sequence's length.
 struct CacheItem {
-    int b, t, h0, nh, id;
+    int which, b, t, h0, nh, id;
     int64_t p;
     bool given;
 };
-__device__ __forceinline__ CacheItem cache_item(const CacheArgs& a, int64_t item) {
+template <int LPR>
+__device__ __forceinline__ CacheItem cache_item(const CacheArgs& a) {
     CacheItem x;
-    const bool live = item < a.items;
-    const int64_t at = live ? item : 0, bh = at / a.T;
-    x.t = (int)(at - bh * a.T);
-    x.b = (int)(bh / a.hc);
-    x.h0 = (int)(bh - (int64_t)x.b * a.hc) * kCacheHeads;
+    const int kv = blockIdx.x / a.hc, run = kv >> 1;
+    x.which = kv & 1;
+    x.h0 = (int)(blockIdx.x - kv * a.hc) * kCacheHeads;
+    x.b = run / a.runs;
+    x.t = (run - x.b * a.runs) * cache_run(LPR) + threadIdx.x / LPR;
+    const bool live = x.t < a.T;
+    if (!live) x.t = 0;
     x.nh = live ? min(kCacheHeads, a.H - x.h0) : 0;
     x.given = x.t < (a.lens ? a.lens[x.b] : a.T);
     x.p = (int64_t)a.start[x.b] + x.t;
@@ -55,22 +63,24 @@ __device__ __forceinline__ CacheItem cache_item(const CacheArgs& a, int64_t item
 
 template <int DT, int LPR>
 __global__ __launch_bounds__(kCacheThreads) void kv_cache_write_kernel(CacheArgs a) {
-    const int which = blockIdx.y, c = (int)(threadIdx.x % LPR) * 8;
-    const CacheItem x = cache_item(
-        a, (int64_t)blockIdx.x * (kCacheThreads / LPR) + threadIdx.x / LPR);
-    // the rows of a wave are summed up together: no lane leaves before that
-    const int nh = x.id >= 0 && c < a.D ? x.nh : 0;
+    const int c = (int)(threadIdx.x % LPR) * 8;
+    const CacheItem x = cache_item<LPR>(a);
+    const int which = x.which;
+    // The rows are asked for before the page is known, all at once: where there
+    // is none to take, the group's first, which exists.
+    const int nr = x.given && c < a.D ? x.nh : 0;
+    if (!__any(nr > 0)) return;   // whole waves: the maxima are theirs
     const uint8_t* src = a.t[which] + x.b * a.t_b[which] + x.t * a.t_t[which] +
-                         x.h0 * a.t_h[which] + 2 * c;
+                         x.h0 * a.t_h[which] + (c < a.D ? 2 * c : 0);
     u32x4 raw[kCacheHeads];
 #pragma unroll
     for (int i = 0; i < kCacheHeads; ++i)
-        raw[i] = i < nh ? *reinterpret_cast<const u32x4*>(src + i * a.t_h[which])
-                        : u32x4{0, 0, 0, 0};
+        raw[i] = *reinterpret_cast<const u32x4*>(src + (i < nr ? i : 0) * a.t_h[which]);
+    const int nh = x.id >= 0 ? nr : 0;
 #pragma unroll
     for (int i = 0; i < kCacheHeads; ++i) {
         float v[8];
-        unpack8<DT>(raw[i], v);
+        unpack8<DT>(i < nr ? raw[i] : u32x4{0, 0, 0, 0}, v);
         const RowScale rs = row_scale(row_top<LPR>(top_bits(v, 0), nullptr));
         if (i < nh) {
             const int64_t row = cache_row(x.id, a.H, x.h0 + i, x.p, a.shift);
@@ -84,22 +94,27 @@ __global__ __launch_bounds__(kCacheThreads) void kv_cache_write_kernel(CacheArgs
 // where its position or page does not exist.
 template <int DT, int LPR>
 __global__ __launch_bounds__(kCacheThreads) void kv_cache_read_kernel(CacheArgs a) {
-    const int which = blockIdx.y, c = (int)(threadIdx.x % LPR) * 8;
-    const CacheItem x = cache_item(
-        a, (int64_t)blockIdx.x * (kCacheThreads / LPR) + threadIdx.x / LPR);
+    const int c = (int)(threadIdx.x % LPR) * 8;
+    const CacheItem x = cache_item<LPR>(a);
+    const int which = x.which;
     if (c >= a.D) return;
     u32x2 raw[kCacheHeads];
     float scale[kCacheHeads];
+    if (a.pages > 0) {   // a page 0 exists
 #pragma unroll
-    for (int i = 0; i < kCacheHeads; ++i) {
-        raw[i] = u32x2{0, 0};
-        scale[i] = x.given ? __builtin_nanf("") : 0.0f;
-        if (x.id >= 0 && i < x.nh) {
-            const int64_t row = cache_row(x.id, a.H, x.h0 + i, x.p, a.shift);
+        for (int i = 0; i < kCacheHeads; ++i) {
+            const int64_t row = x.id >= 0 && i < x.nh
+                                    ? cache_row(x.id, a.H, x.h0 + i, x.p, a.shift) : 0;
             raw[i] = *reinterpret_cast<const u32x2*>(a.pool[which] + row * a.Dp + c);
             scale[i] = a.scale[which][row];
         }
     }
+#pragma unroll
+    for (int i = 0; i < kCacheHeads; ++i)
+        if (x.id < 0) {
+            raw[i] = u32x2{0, 0};
+            scale[i] = x.given ? __builtin_nanf("") : 0.0f;
+        }
     uint8_t* dst = a.t[which] + x.b * a.t_b[which] + x.t * a.t_t[which] + x.h0 * a.t_h[which] +
                    2 * c;
 #pragma unroll

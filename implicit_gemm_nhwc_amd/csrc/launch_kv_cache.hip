@@ -20,8 +20,7 @@ hipError_t launch_quant(const QuantArgs& a, hipStream_t stream) {
 
 template <int DT, int LPR>
 hipError_t launch_io(const CacheArgs& a, bool write, hipStream_t stream) {
-    constexpr int PER = kCacheThreads / LPR;
-    const dim3 grid((unsigned)((a.items + PER - 1) / PER), 2);
+    const dim3 grid((unsigned)((int64_t)a.B * a.runs * 2 * a.hc));
     if (write)
         hipLaunchKernelGGL((kv_cache_write_kernel<DT, LPR>), grid, dim3(kCacheThreads), 0, stream,
                            a);

@@ -77,6 +77,42 @@ __device__ __forceinline__ void ln_weights(const float* w, int c, int C, float n
     for (int j = 0; j < 8; ++j) v[j] = w && c + j < C ? w[c + j] : none;
 }
 
+// f(x, y) with y the value of a partner lane whose group of O lanes differs in
+// bit log2(O) from this one's, for values that all lanes of a group share (so
+// that any lane of the other group will do): lane permutations of the vector
+// unit, without a trip through LDS.
+template <int O, typename F>
+__device__ __forceinline__ uint32_t with_group(uint32_t x, F f) {
+    static_assert(O <= 32, "within a wave");
+    if constexpr (O == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        const uint32_t a = r[0], b = r[1];
+        return f(a, b);
+    } else if constexpr (O == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        const uint32_t a = r[0], b = r[1];
+        return f(a, b);
+    } else {
+        // quad_perm 1 0 3 2, 2 3 0 1; half rows and rows mirrored
+        constexpr int ctrl = O == 1 ? 0xb1 : O == 2 ? 0x4e : O == 4 ? 0x141 : 0x140;
+        return f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, 0xf, 0xf, true));
+    }
+}
+// f over the N lanes of a group, for every lane.
+template <int N, int O = 1, typename F>
+__device__ __forceinline__ uint32_t over_lanes(uint32_t x, F f) {
+    if constexpr (O < N) return over_lanes<N, 2 * O>(with_group<O>(x, f), f);
+    return x;
+}
+template <int N>
+__device__ __forceinline__ float sum_lanes(float x) {
+    return __builtin_bit_cast(
+        float, over_lanes<N>(__builtin_bit_cast(uint32_t, x), [](uint32_t a, uint32_t b) {
+            return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a) +
+                                                    __builtin_bit_cast(float, b));
+        }));
+}
+
 // Sums over the lanes of a row.  Rows of more than a wave add the waves' sums
 // in order through LDS; consecutive sums use the two slots in turn, so that
 // one barrier each is enough.
@@ -91,11 +127,8 @@ struct RowSum {
     }
     template <int N = 2>
     __device__ __forceinline__ void add(float& x, float& y) {
-#pragma unroll
-        for (int o = 1; o < (LPR < 64 ? LPR : 64); o <<= 1) {
-            x += __shfl_xor(x, o, 64);
-            if constexpr (N > 1) y += __shfl_xor(y, o, 64);
-        }
+        x = sum_lanes<(LPR < 64 ? LPR : 64)>(x);
+        if constexpr (N > 1) y = sum_lanes<(LPR < 64 ? LPR : 64)>(y);
         if constexpr (LPR > 64) {
             float* s = lds + slot * 2 * NW;
             slot ^= 1;

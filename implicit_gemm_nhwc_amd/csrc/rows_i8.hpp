@@ -68,9 +68,8 @@ __device__ __forceinline__ u32x2 row_bytes(const float* v, const RowScale& s) {
 // Maximum over the lanes of a row (RowSum's way).
 template <int LPR>
 __device__ __forceinline__ uint32_t row_top(uint32_t top, uint32_t* lds) {
-#pragma unroll
-    for (int o = 1; o < (LPR < 64 ? LPR : 64); o <<= 1)
-        top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
+    top = over_lanes<(LPR < 64 ? LPR : 64)>(top,
+                                            [](uint32_t a, uint32_t b) { return max(a, b); });
     if constexpr (LPR > 64) {
         if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = top;
         __syncthreads();

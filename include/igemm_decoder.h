@@ -158,7 +158,8 @@ typedef struct igc_kv_cache {
  * position or the page does not exist.
  * Limits: batch, tokens below 2^31; a launch holds one group of 4 to 16 lanes
  * (head_dim / 8, rounded up to a power of two) for every four heads of a
- * token, of keys and of values, and fewer than 2^32 threads.
+ * token, of keys and of values, a sequence's tokens rounded up to a workgroup
+ * of 256 lanes, and fewer than 2^32 threads.
  */
 typedef struct igc_kv_io {
     igc_kv_cache cache;
