@@ -62,7 +62,7 @@ template <int DT>
 hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t stream);
 
 // Form of the product: at most kFewRows rows of x, or square tiles.
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 32;
 struct LinForm {
     int tile;         // 0: few rows
     int64_t tiles_m, tiles_n;

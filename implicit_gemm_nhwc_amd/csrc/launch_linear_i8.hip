@@ -16,10 +16,10 @@ hipError_t launch_few(const LinArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int DT, int B>
+template <int DT, int B, int NS>
 hipError_t launch_tile(const LinArgs& a, hipStream_t stream) {
-    auto kern = linear_i8_tile_kernel<DT, B>;
-    constexpr size_t lds = 2 * (size_t)kLinStages * B * kLinKT;
+    auto kern = linear_i8_tile_kernel<DT, B, NS>;
+    constexpr size_t lds = LinTile<B, NS>::LDS;
     static LdsAttr attr;
     const hipError_t e = ensure_lds(attr, (const void*)kern, lds);
     if (e != hipSuccess) return e;
@@ -32,12 +32,12 @@ hipError_t launch_tile(const LinArgs& a, hipStream_t stream) {
 
 template <int DT>
 hipError_t launch_linear_i8(const LinArgs& a, int tile, hipStream_t stream) {
-    if (tile == 256) return launch_tile<DT, 256>(a, stream);
-    if (tile == 128) return launch_tile<DT, 128>(a, stream);
-    if (tile == 64) return launch_tile<DT, 64>(a, stream);
-    if (a.M <= 16) return launch_few<DT, 1>(a, stream);
-    if (a.M <= 32) return launch_few<DT, 2>(a, stream);
-    return launch_few<DT, 4>(a, stream);
+    if (tile == 256) return launch_tile<DT, 256, 3>(a, stream);
+    if (tile == 128) return launch_tile<DT, 128, 3>(a, stream);
+    if (tile == 64)
+        return (int64_t)a.tiles_m * a.tiles_n > kNumCUs ? launch_tile<DT, 64, 2>(a, stream)
+                                                        : launch_tile<DT, 64, 3>(a, stream);
+    return a.M <= 16 ? launch_few<DT, 1>(a, stream) : launch_few<DT, 2>(a, stream);
 }
 
 template hipError_t launch_linear_i8<IGC_DT>(const LinArgs&, int, hipStream_t);

@@ -6,8 +6,8 @@
 // owns one row of y and neighbouring columns.  The integer sums are exact; they
 // are scaled in fp32 and rounded once.
 //
-// The tile kernel stages 64 k of its rows and columns in LDS by direct loads,
-// three stages deep; the few-rows kernel, which the weights' bytes bound, takes
+// The tile kernel stages its rows and columns in LDS by direct loads; the
+// few-rows kernel, which the weights' bytes bound, takes
 // 16 columns a workgroup, gives each wave a part of k and reads both operands
 // straight into registers.
 #pragma once
@@ -46,17 +46,27 @@ __device__ __forceinline__ i32x4 lin_clear(i32x4 v, int left) {
     return v;
 }
 
-// Columns n .. n + 3 of row m.
+// Scales and bias of columns n .. n + 3 of row m (zeros past N).
+struct LinScales {
+    float xs;
+    f32x4 ws, bs;
+    __device__ __forceinline__ void load(const LinArgs& a, int m, int n) {
+        xs = a.xs[min(m, a.M - 1)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = min(n + i, a.N - 1);
+            ws[i] = a.ws[c];
+            bs[i] = a.bias ? a.bias[c] : 0.0f;
+        }
+    }
+};
 template <int DT>
-__device__ __forceinline__ void lin_store4(const LinArgs& a, int m, int n, const int* acc) {
+__device__ __forceinline__ void lin_store4(const LinArgs& a, int m, int n, const i32x4& acc,
+                                           const LinScales& sc) {
     typedef uint32_t u32x2h __attribute__((ext_vector_type(2), aligned(2)));
-    const float xs = a.xs[m];
     float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = min(n + i, a.N - 1);
-        v[i] = (float)acc[i] * xs * a.ws[c] + (a.bias ? a.bias[c] : 0.0f);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf((float)acc[i] * sc.xs, sc.ws[i], sc.bs[i]);
     const u32x2 o = {pack_out2(v[0], v[1], DT), pack_out2(v[2], v[3], DT)};
     uint8_t* y = a.y + (int64_t)m * a.y_p + 2 * (int64_t)n;
     if (n + 4 <= a.N) {
@@ -100,6 +110,12 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_i8_few_kernel(LinArgs a
                                                              ? woff + k + 64 * s : kOut));
     };
     load_w(k0, w);
+    // what the results need is asked for before the sums begin: result lane l
+    // has row l % 16 of x, columns 4 (l / 16) .. + 3
+    static_assert(MT <= kFewWaves, "a thread a result");
+    const int rt = threadIdx.x >> 6, m = 16 * rt + (lane & 15), n = n0 + 4 * (lane >> 4);
+    LinScales sc;
+    if (rt < MT) sc.load(a, m, n);
     for (int k = k0; k < a.K; k += STEP) {
         load_w(k + STEP, nw);
 #pragma unroll
@@ -119,37 +135,42 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_i8_few_kernel(LinArgs a
 #pragma unroll
     for (int t = 0; t < MT; ++t) *reinterpret_cast<i32x4*>(part[wave][t][lane]) = acc[t];
     __syncthreads();
-    // result: lane l has row l % 16 of x, columns 4 (l / 16) .. + 3
-    for (int e = threadIdx.x; e < MT * 64; e += kFewWaves * 64) {
-        const int t = e >> 6, l = e & 63, m = 16 * t + (l & 15), n = n0 + 4 * (l >> 4);
-        i32x4 s = *reinterpret_cast<const i32x4*>(part[0][t][l]);
+    if (rt >= MT) return;
+    i32x4 s = *reinterpret_cast<const i32x4*>(part[0][rt][lane]);
 #pragma unroll
-        for (int v = 1; v < kFewWaves; ++v)
-            s += *reinterpret_cast<const i32x4*>(part[v][t][l]);
-        if (m < a.M && n < a.N) {
-            const int v[4] = {s[0], s[1], s[2], s[3]};
-            lin_store4<DT>(a, m, n, v);
-        }
-    }
+    for (int v = 1; v < kFewWaves; ++v) s += *reinterpret_cast<const i32x4*>(part[v][rt][lane]);
+    if (m < a.M && n < a.N) lin_store4<DT>(a, m, n, s, sc);
 }
 
 // ---------------------------------------------------------------------------
 // Square tiles of B rows of x and B of w, four waves of a quarter each.  A
-// stage is 64 k of all rows; kLinStages of them are under way or being read,
-// because a stage takes more than one of its times to arrive.  A step is 32 k:
-// the fragments of the next one are read while its products run, and a stage's
-// last step reads the next stage's first, so that the matrix cores see no
-// seam.  One barrier a stage: behind it the next stage is whole, and the one
-// just read may be overwritten.
-constexpr int kLinKT = 64, kLinStages = 3;
+// stage is KT k of all rows; NS of them are under way or being read.  A step is
+// 32 k: the fragments of the next one are read while its products run, and a
+// stage's last step reads the next stage's first, so that the matrix cores see
+// no seam.  One barrier a stage: behind it the next stage is whole, and the one
+// just read may be overwritten.  A barrier costs as much as several products of
+// a small tile, which therefore takes long stages (64 rows x 4096 x 4096 in
+// tiles of 64: 12.2 us in stages of 64 k, 10.6 of 128, 8.7 of 256; in tiles of
+// 128, 1024 rows: 23.6 of 64 and 22.5 of 128).  Where tiles of 64 are more
+// than the CUs, two stages let two workgroups share one (512 rows: 15.5 us,
+// three stages 17.4; 64 rows 10.3 and 8.7).
+template <int B, int NS>
+struct LinTile {
+    static constexpr int KT = B == 256 ? 64 : B == 128 ? 128 : 256;
+    static constexpr int T = B * KT;   // bytes of one operand's stage
+    static constexpr int LDS = NS * 2 * T;
+};
 
-template <int DT, int B>
+template <int DT, int B, int NS>
 __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(LinArgs a) {
     constexpr int NW = 4, MB = B / 64;   // blocks of 32 a wave, each way
-    constexpr int T = B * kLinKT, P = T / 1024 / NW;   // bytes, loads a wave of one operand
-    constexpr int NS = kLinStages;
+    constexpr int KT = LinTile<B, NS>::KT, T = LinTile<B, NS>::T;
+    constexpr int STEPS = KT / 32, CH = KT / 16;   // 16-byte chunks of a row
+    constexpr int P = T / 1024 / NW, PR = 1024 / KT;   // loads a wave of one operand; their rows
+    static_assert(2 * P == STEPS * MB && STEPS % 2 == 0, "MB loads a step");
+    static_assert(P * PR % 16 == 0, "a wave's rows start at a multiple of 16");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];   // NS x {x, w}
-    lds_poison<NW * 64>(lds, NS * 2 * T);
+    lds_poison<NW * 64>(lds, LinTile<B, NS>::LDS);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave >> 1, wn = wave & 1, half = lane >> 5;
 
@@ -164,21 +185,24 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(L
     const __amdgpu_buffer_rsrc_t wr = lin_rsrc(
         a.w + n0 * a.w_p, lin_bytes(min(B, a.N - n0), a.w_p, a.K16));
 
-    // a load is 16 rows; the 16-byte chunk c of row r lies at c ^ (r / 4 % 4),
-    // which spreads a chunk of 16 rows over all banks
-    const int chunk = (lane & 3) ^ (lane >> 4);
-    const unsigned xo = (unsigned)((16 * wave * P + (lane >> 2)) * a.x_p) + 16 * chunk;
-    const unsigned wo = (unsigned)((16 * wave * P + (lane >> 2)) * a.w_p) + 16 * chunk;
-    const unsigned x16 = (unsigned)(16 * a.x_p), w16 = (unsigned)(16 * a.w_p);
+    // Chunk c of row r lies at c ^ turn(r), which spreads a chunk of 16 rows over
+    // all banks.
+    auto turn = [](int r) { return r / (256 / KT) & (CH - 1); };
+    const int lrow = lane / CH;   // the lane's row in a load
+    const unsigned xo = (unsigned)((wave * P * PR + lrow) * a.x_p);
+    const unsigned wo = (unsigned)((wave * P * PR + lrow) * a.w_p);
+    const unsigned xr1 = (unsigned)(PR * a.x_p), wr1 = (unsigned)(PR * a.w_p);
     typedef __attribute__((address_space(3))) void* lp;
-    auto issue_x = [&](int k, uint8_t* to, int i) {
-        const unsigned at = k + 16 * chunk < a.K ? xo + k : kOut;   // zeros past K
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lp)(to + (wave * P + i) * 1024), 16,
-                                                 at + i * x16, 0, 0, 0);
-    };
-    auto issue_w = [&](int k, uint8_t* to, int i) {   // past K anything: it meets zeros
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lp)(to + T + (wave * P + i) * 1024), 16,
-                                                 wo + k + i * w16, 0, 0, 0);
+    // load l of the 2 P of the stage at k
+    auto issue = [&](int k, uint8_t* to, int l) {
+        const int i = l < P ? l : l - P;
+        const int at = k + 16 * ((lane % CH) ^ turn(i * PR + lrow));
+        if (l < P)   // zeros past K
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lp)(to + (wave * P + i) * 1024), 16,
+                                                     at < a.K ? xo + i * xr1 + at : kOut, 0, 0, 0);
+        else         // past K anything: it meets zeros
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lp)(to + T + (wave * P + i) * 1024), 16,
+                                                     wo + i * wr1 + at, 0, 0, 0);
     };
     // This wave's part of the stage at k is here: all of it, for all waves, is.
     // (A bare barrier: __syncthreads would wait for the later stages too.)
@@ -189,36 +213,43 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(L
     };
     auto arrived = [&](int k, uint8_t* at) {
         barrier();
-        if (a.K - k < kLinKT && a.K > k && a.K != a.K16) {
+        if (a.K - k < KT && a.K > k && a.K != a.K16) {
             // x's bytes past K in its last chunk become zeros
             for (int r = threadIdx.x; r < B; r += NW * 64) {
                 i32x4* c = reinterpret_cast<i32x4*>(
-                    at + r * kLinKT + ((((a.K - k) >> 4) ^ (r >> 2 & 3)) << 4));
+                    at + r * KT + ((((a.K - k) >> 4) ^ turn(r)) << 4));
                 *c = lin_clear(*c, (a.K - k) & 15);
             }
             barrier();
         }
     };
+    // what the results need: a thread's column, a lane's rows
+    const int my_col = min(n0 + (int)threadIdx.x % B, a.N - 1);
+    const float my_ws = a.ws[my_col], my_bs = a.bias ? a.bias[my_col] : 0.0f;
+    float xs[MB];
+    auto row_scales = [&] {
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+            xs[i] = a.xs[min(m0 + (wm * MB + i) * 32 + (lane & 31), a.M - 1)];
+    };
+    if constexpr (B < 256) row_scales();   // the large tile has no registers for them yet
     i32x4 xf[2][MB], wf[2][MB];
     // rows of a block start at multiples of 32
-    const int turn = lane >> 2 & 3;
-    const uint8_t* xl = lds + (wm * MB * 32 + (lane & 31)) * kLinKT;
-    const uint8_t* wl = lds + T + (wn * MB * 32 + (lane & 31)) * kLinKT;
-    auto read = [&](int buf, int s, int set, int i) {
-        const int c = buf * 2 * T + (((2 * s + half) ^ turn) << 4);   // buf: the stage's place
-        wf[set][i] = *reinterpret_cast<const i32x4*>(wl + c + i * 32 * kLinKT);
-        xf[set][i] = *reinterpret_cast<const i32x4*>(xl + c + i * 32 * kLinKT);
+    const uint8_t* xl = lds + (wm * MB * 32 + (lane & 31)) * KT;
+    const uint8_t* wl = lds + T + (wn * MB * 32 + (lane & 31)) * KT;
+    auto read = [&](int buf, int s, int set, int i) {   // buf: the stage's place
+        const int c = buf * 2 * T + (((2 * s + half) ^ turn(lane & 31)) << 4);
+        wf[set][i] = *reinterpret_cast<const i32x4*>(wl + c + i * 32 * KT);
+        xf[set][i] = *reinterpret_cast<const i32x4*>(xl + c + i * 32 * KT);
     };
     i32x16 acc[MB][MB];
     // Products of one step, and between them the reads of the next one and a
-    // stage's loads of one operand (P = MB): in a burst the loads would hold up
-    // the products behind them.
-    auto step = [&](int set, int next_buf, int next_s, auto load) {
-        static_assert(P == MB, "a load a row of products");
+    // few loads: in a burst the loads would hold up the products behind them.
+    auto step = [&](int set, int next_buf, int next_s, int k, uint8_t* to, int first) {
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
             read(next_buf, next_s, set ^ 1, i);
-            load(i);
+            issue(k, to, first + i);
 #pragma unroll
             for (int j = 0; j < MB; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[set][j], xf[set][i],
@@ -231,15 +262,12 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(L
 #pragma unroll
         for (int n = 0; n < NS - 1; ++n)
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                issue_x(n * kLinKT, lds + n * 2 * T, i);
-                issue_w(n * kLinKT, lds + n * 2 * T, i);
-            }
+            for (int l = 0; l < 2 * P; ++l) issue(n * KT, lds + n * 2 * T, l);
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * 2 * P) : "memory");
         arrived(0, lds);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            issue_x((NS - 1) * kLinKT, lds + (NS - 1) * 2 * T, i);
+        for (int i = 0; i < MB; ++i) {
+            issue((NS - 1) * KT, lds + (NS - 1) * 2 * T, i);
             read(0, 0, 0, i);
         }
     }
@@ -249,14 +277,17 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(L
         for (int j = 0; j < MB; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-    for (int k = 0; k < a.K; k += kLinKT) {
-        step(0, buf, 1, [&](int i) { issue_w(k + (NS - 1) * kLinKT, lds + old * 2 * T, i); });
+    for (int k = 0; k < a.K; k += KT) {
+        uint8_t* to = lds + old * 2 * T;
+#pragma unroll
+        for (int s = 0; s < STEPS - 1; ++s)
+            step(s & 1, buf, s + 1, k + (NS - 1) * KT, to, (s + 1) * MB);
         // the last step's fragments and the next stage
         asm volatile("s_waitcnt lgkmcnt(0) vmcnt(%0)" ::"n"((NS - 2) * 2 * P) : "memory");
         old = buf;
         buf = buf + 1 < NS ? buf + 1 : 0;
-        arrived(k + kLinKT, lds + buf * 2 * T);
-        step(1, buf, 0, [&](int i) { issue_x(k + NS * kLinKT, lds + old * 2 * T, i); });
+        arrived(k + KT, lds + buf * 2 * T);
+        step(1, buf, 0, k + NS * KT, lds + old * 2 * T, 0);
     }
     // nothing may be under way to LDS when the workgroup ends
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -264,20 +295,20 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(L
     // rows of a wave at a time, so that whole lines are stored.
     barrier();
     float* col = reinterpret_cast<float*>(lds);   // [2][B]
-    for (int c = threadIdx.x; c < B; c += NW * 64) {
-        const int n = min(n0 + c, a.N - 1);
-        col[c] = a.ws[n];
-        col[B + c] = a.bias ? a.bias[n] : 0.0f;
+    static_assert(B <= NW * 64, "a column a thread");
+    if ((int)threadIdx.x < B) {
+        col[threadIdx.x] = my_ws;
+        col[B + threadIdx.x] = my_bs;
     }
+    if constexpr (B == 256) row_scales();
     __syncthreads();
-    constexpr int CH = MB * 4, RL = 64 / CH;   // 16-byte chunks of a row; rows a store
-    uint8_t* out = lds + 2 * B * 4 + wave * (32 * CH * 16);
+    constexpr int OC = MB * 4, RL = 64 / OC;   // 16-byte chunks of a row; rows a store
+    uint8_t* out = lds + 2 * B * 4 + wave * (32 * OC * 16);
     const bool inner = m0 + B <= a.M && n0 + B <= a.N;
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
         const int mb = m0 + (wm * MB + i) * 32, nb = n0 + wn * MB * 32;
         const int r = lane & 31;
-        const float xs = a.xs[min(mb + r, a.M - 1)];
         // register 4 g + e of half h is column 8 g + 4 h + e of a block; the
         // halves exchange groups, so that each lane holds 8 neighbouring
         // columns: half h the groups h and 2 + h
@@ -294,7 +325,7 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(L
                     float f[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        f[e] = __builtin_fmaf((float)acc[i][j][8 * gg + 4 * g + e] * xs, ws[e],
+                        f[e] = __builtin_fmaf((float)acc[i][j][8 * gg + 4 * g + e] * xs[i], ws[e],
                                               bs[e]);
                     v[2 * g] = pack_out2(f[0], f[1], DT);
                     v[2 * g + 1] = pack_out2(f[2], f[3], DT);
@@ -302,15 +333,15 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(L
                 const auto p = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
                 const auto q = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
                 const int ch = 4 * j + 2 * gg + half;
-                *reinterpret_cast<u32x4*>(out + (r * CH + (ch ^ (r & (CH - 1)))) * 16) =
+                *reinterpret_cast<u32x4*>(out + (r * OC + (ch ^ (r & (OC - 1)))) * 16) =
                     u32x4{p[0], q[0], p[1], q[1]};
             }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's own rows
 #pragma unroll
         for (int t = 0; t < 32 / RL; ++t) {
-            const int row = t * RL + lane / CH, ch = lane % CH;
+            const int row = t * RL + lane / OC, ch = lane % OC;
             const u32x4 o = *reinterpret_cast<const u32x4*>(
-                out + (row * CH + (ch ^ (row & (CH - 1)))) * 16);
+                out + (row * OC + (ch ^ (row & (OC - 1)))) * 16);
             const int m = mb + row, n = nb + 8 * ch;
             uint8_t* y = a.y + (int64_t)m * a.y_p + 2 * (int64_t)n;
             if (inner) {
