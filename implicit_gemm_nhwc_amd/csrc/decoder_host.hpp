@@ -19,8 +19,8 @@ constexpr int kLnMaxChannels = 16384;
 // fewest lanes without work (154 MB: 54 to 58 us forward and 92 to 96 backward
 // wherever the row fills them; 768 channels on 32 lanes x 3 58 and 95, on 64 x 2
 // 73 and 103; 512 on 32 x 2 54 and 94, on 64 x 1 62 and 109, on 16 x 4 58 and
-// 104).  Past 2048 channels a workgroup takes a row (4096: 65 and 104; 8192:
-// 74 and 122).
+// 104).  Past 2048 channels a workgroup takes a row (4096: 65 and 100; 8192: 65
+// and 100, on 256 x 4 76 and 111; 16384: 71 and 116).
 struct LnForm {
     int lanes, chunks, threads;
 };
@@ -34,21 +34,23 @@ constexpr LnForm ln_form(int c) {
     }
     if (c <= 4096) return {256, 2, 256};
     if (c <= 6144) return {256, 3, 256};
-    if (c <= 8192) return {256, 4, 256};
-    return {512, 4, 512};
+    if (c <= 8192) return {512, 2, 512};
+    return c <= 12288 ? LnForm{512, 3, 512} : LnForm{512, 4, 512};
 }
 // What ln_form returns.
 #define IGC_LN_FORMS(F) \
     F(8, 1, 256) F(8, 2, 256) F(8, 3, 256) F(16, 2, 256) \
     F(16, 3, 256) F(32, 2, 256) F(32, 3, 256) F(64, 2, 256) \
     F(64, 3, 256) F(64, 4, 256) F(256, 2, 256) \
-    F(256, 3, 256) F(256, 4, 256) F(512, 4, 512)
+    F(256, 3, 256) F(512, 2, 512) F(512, 3, 512) F(512, 4, 512)
 
-// Workgroups a CU of the backward pass: with four chunks (three on many lanes)
-// the registers hold two well (2048 channels: 96 us, three 109; 1536: 92 and
-// 97; 320 on 16 x 3 101 and 95).
+// Workgroups a CU of the backward pass, as the registers allow: with four
+// chunks (three on many lanes) two (2048 channels: 96 us, three 109; 1536: 92
+// and 97; 320 on 16 x 3 101 and 95), with a row a workgroup two of 256 threads
+// (4096: 100, three 108) or one of 512 (8192: 100, two 117).
 constexpr int ln_bwd_fill(const LnForm& f) {
-    return f.chunks == 4 || (f.chunks == 3 && f.lanes >= 32 && f.lanes <= 64) ? 2 : 3;
+    if (f.lanes > 64) return f.lanes == 256 ? 2 : 1;
+    return f.chunks == 4 || (f.chunks == 3 && f.lanes >= 32) ? 2 : 3;
 }
 
 template <int DT>

@@ -228,22 +228,45 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(LnArgs a) {
     }
     const int rounds = (int)(((int64_t)a.rows + (int64_t)a.blocks * PER - 1) /
                              ((int64_t)a.blocks * PER));
-    for (int k = 0; k < rounds; ++k) {
-        const int64_t at = ((int64_t)k * a.blocks + blockIdx.x) * PER + threadIdx.x / LPR;
+    // A workgroup that takes one row at a time asks for the next one's values
+    // before it sums up this one's; where waves have rows of their own, the
+    // other waves' requests fill the gap.
+    constexpr bool AHEAD = LPR > 64;
+    auto row_of = [&](int k) { return ((int64_t)k * a.blocks + blockIdx.x) * PER + threadIdx.x / LPR; };
+    auto load = [&](const uint8_t* p, const int64_t* s, int64_t at, u32x4 (&to)[NC]) {
         const bool live = at < a.rows;
-        const int row = live ? (int)at : 0;
-        const uint8_t* x = a.x + ln_row(a, a.x_s, row);
-        const uint8_t* g = a.dy + ln_row(a, a.g_s, row);
-        u32x4 rx[NC], rg[NC];
+        const uint8_t* x = p + ln_row(a, s, live ? (int)at : 0);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int c = c0 + i * LPR * 8, left = live ? a.C - c : 0;
-            rx[i] = ln_load<DT>(x + 2 * c, left);
-            rg[i] = ln_load<DT>(g + 2 * c, left);
+            const int c = c0 + i * LPR * 8;
+            to[i] = ln_load<DT>(x + 2 * c, live ? a.C - c : 0);
+        }
+    };
+    u32x4 rx[NC], rg[NC], ng[NC];
+    if constexpr (AHEAD) {
+        load(a.x, a.x_s, row_of(0), rx);
+        load(a.dy, a.g_s, row_of(0), ng);
+    }
+    for (int k = 0; k < rounds; ++k) {
+        const int64_t at = row_of(k);
+        const bool live = at < a.rows;
+        const int row = live ? (int)at : 0;
+        if constexpr (!AHEAD) {
+            load(a.x, a.x_s, at, rx);
+            load(a.dy, a.g_s, at, rg);
         }
         float v[NC][8];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) unpack8<DT>(rx[i], v[i]);
+        for (int i = 0; i < NC; ++i) {
+            unpack8<DT>(rx[i], v[i]);
+            if constexpr (AHEAD) rg[i] = ng[i];
+        }
+        if constexpr (AHEAD) {
+            if (k + 1 < rounds) {
+                load(a.x, a.x_s, row_of(k + 1), rx);
+                load(a.dy, a.g_s, row_of(k + 1), ng);
+            }
+        }
         float r = ln_stats<LPR, NC>(sum, v, c0, a.C, a.inv_c, a.eps);
         if (!live) r = 0.0f;   // eps = 0 gives infinity there
         float s = 0.0f, q = 0.0f;

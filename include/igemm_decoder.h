@@ -49,7 +49,7 @@ extern "C" {
  *   weight, bias  fp32 [C] or NULL
  * Limits: C from 1 to 16384, fewer than 2^31 rows, strides below 2^40; a launch
  * holds fewer than 2^32 threads (a row takes 8 to 64 of them up to 2048
- * channels, 256 up to 8192, 512 past that).  Rows
+ * channels, 256 up to 6144, 512 past that).  Rows
  * whose squares overflow fp32 (magnitudes past 1e19 / sqrt(C)) give 0 or NaN.
  */
 typedef struct igc_layer_norm {

@@ -8,8 +8,10 @@ d = e (|x - mean| + 32 A); the variance by 2 d sigma + 32 e sigma^2, so that r
 is off by a factor (32 A r + 32) e, and xh by
   X = e (33 A r + |xh|) + |xh| (33 A r + 32) e.
 The gradients add their own sums (32 e of the magnitudes) and what X moves.
-A weight's gradient adds a lane's rounds (rows / 768), a workgroup's groups of
-lanes (32 at most), 768 / 64 partials a lane and a tree of 6.
+A weight's gradient adds a lane's rounds, a workgroup's groups of lanes, 1 / 64
+of the workgroups' partials a lane and a tree of 6: with a row a workgroup rows /
+256 + 8 + 6, otherwise rows / 2048 + 32 + 12 + 6, both under rows / 768 + 64 up to
+19000 rows.
 """
 import os
 
@@ -98,6 +100,9 @@ CASES = [
     (HF, (4000,), 777, True, 0.3),
     (BF, (1600,), 4096, False, 0.0),
     (HF, (2000,), 8200, True, 0.0),
+    (BF, (1100,), 6000, True, 0.0),
+    (HF, (700,), 7000, True, 0.3),
+    (BF, (600,), 12289, True, 0.0),
 ]
 
 
