@@ -42,7 +42,13 @@ struct CacheAttnArgs {
     int split;             // whether workgroups share a sequence (then a join follows)
 };
 
-constexpr int kCacheWaves = 8;   // a workgroup
+// Waves a workgroup: eight, of which two workgroups share a CU where sequences
+// are split; sixteen where a workgroup of at most 16 rows reads a whole
+// sequence of more than one round of eight.
+constexpr int kCacheWaves = 8;
+inline bool cache_whole(bool split, int64_t capacity) {
+    return !split && capacity > 32 * kCacheWaves;
+}
 // The running maximum follows the true one only when a row exceeds it by
 // 2^kCacheSlack: it only guards the range.
 constexpr float kCacheSlack = 8.0f;
@@ -111,7 +117,22 @@ struct CacheDivision {
         uint32_t total = lane_value(wave_scan(cache_units(first)), 63);
         for (int base = 64; base < x.a.B; base += 64)
             total += lane_value(wave_scan(cache_units(len(x, base + lane))), 63);
-        chunk = cache_chunk(total, (uint32_t)x.slots, (uint32_t)x.a.B);
+        chunk = cache_chunk(total, (uint32_t)(x.slots - x.a.B));
+        uint32_t low = cache_chunk(total, (uint32_t)x.slots);   // chunk fits; below low nothing does
+        for (int i = 0; i < kCacheBisect && low < chunk; ++i) {
+            const uint32_t mid = low + (chunk - low) / 2;
+            if (parts(x, lane, mid) <= (uint32_t)x.slots) chunk = mid;
+            else low = mid + 1;
+        }
+    }
+    __device__ __forceinline__ uint32_t parts(const CacheAttnArgs& x, int lane,
+                                              uint32_t c) const {
+        uint32_t n = 0;
+        for (int base = 0; base < x.a.B; base += 64)
+            n += lane_value(wave_scan(base + lane < x.a.B
+                                          ? cache_parts(base ? len(x, base + lane) : first, c) : 0),
+                            63);
+        return n;
     }
     // The sequence that workgroup w works on (b < 0), or sequence b: its
     // parts, length and first slot.  False for workgroups past the last part.
@@ -555,14 +576,16 @@ __global__ __launch_bounds__(NW * 64, RB == 1 ? 4 : 2) void cache_attn_kernel(Ca
 }
 
 // Join of the parts of a sequence that several workgroups read: a workgroup a
-// row, its eight groups of 32 lanes (4 values a lane) sum every eighth part,
-// and the eight sums are added in order through LDS.
+// row, its eight groups of 32 lanes (4 values a lane) take every eighth part,
+// and the eight results are added in order through LDS.  A part's statistics
+// and values are asked for together: the groups follow a running maximum of
+// their own.
 template <int DT>
 __global__ __launch_bounds__(256) void cache_attn_join_kernel(CacheAttnArgs x) {
     __shared__ __attribute__((aligned(16))) f32x4 part[8][32];
-    __shared__ __attribute__((aligned(16))) float sum[8];
+    __shared__ __attribute__((aligned(16))) float st[2][8];
     lds_poison<256>(reinterpret_cast<uint8_t*>(part), sizeof(part));
-    lds_poison<256>(reinterpret_cast<uint8_t*>(sum), sizeof(sum));
+    lds_poison<256>(reinterpret_cast<uint8_t*>(st), sizeof(st));
     const AttnArgs& a = x.a;
     const int lane = threadIdx.x & 63, g = threadIdx.x >> 5, d = (threadIdx.x & 31) * 4;
     const int rows_tile = min(a.rows, x.tile), hr_n = a.Hk * a.row_tiles;
@@ -577,34 +600,54 @@ __global__ __launch_bounds__(256) void cache_attn_join_kernel(CacheAttnArgs x) {
     if (at.parts <= 1) return;   // written where it was read
     const int64_t slot = at.slot0 + hr * at.parts;
     const float* stat = a.stat + (slot * rows_tile + r) * 2;
-    const float* from = a.part + (slot * rows_tile + r) * a.D + d;
+    const float* from = a.part + (slot * rows_tile + r) * a.D + (d < a.D ? d : 0);
     const int64_t pitch = (int64_t)rows_tile * a.D;
-    float mm = -__builtin_inff();
-    for (int s = lane; s < at.parts; s += 64)
-        mm = fmaxf(mm, stat[(int64_t)s * rows_tile * 2]);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) mm = fmaxf(mm, __shfl_xor(mm, o, 64));
-    const float ms = mm == -__builtin_inff() ? 0.0f : mm;
-    float ll = 0.0f;
+    float mm = -__builtin_inff(), ll = 0.0f;
     f32x4 o = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int s = g; s < at.parts; s += 8) {
-        const float f = __builtin_amdgcn_exp2f(stat[(int64_t)s * rows_tile * 2] - ms);
-        ll = __builtin_fmaf(stat[(int64_t)s * rows_tile * 2 + 1], f, ll);
-        if (d < a.D) {
-            const f32x4 v = *reinterpret_cast<const f32x4*>(from + s * pitch);
+    auto scale = [](float from, float to) {   // 2^(from - to), parts without a key left out
+        return from == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(from - to);
+    };
+    constexpr int U = 4;   // parts asked for at once
+    for (int s0 = g; s0 < at.parts; s0 += 8 * U) {
+        float m[U], l[U];
+        f32x4 v[U];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], f, o[i]);
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + 8 * u;
+            const int64_t i = s < at.parts ? s : s0;
+            m[u] = stat[i * rows_tile * 2];
+            l[u] = stat[i * rows_tile * 2 + 1];
+            v[u] = *reinterpret_cast<const f32x4*>(from + i * pitch);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s0 + 8 * u >= at.parts) break;
+            const float n = fmaxf(mm, m[u]), f = scale(mm, n), k = scale(m[u], n);
+            mm = n;
+            ll = __builtin_fmaf(l[u], k, ll * f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[u][i], k, o[i] * f);
         }
     }
     part[g][threadIdx.x & 31] = o;
-    if (d == 0) sum[g] = ll;
+    if (d == 0) {
+        st[0][g] = mm;
+        st[1][g] = ll;
+    }
     __syncthreads();
     if (g != 0 || d >= a.D) return;
+    mm = st[0][0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        ll += sum[i];
-        o += part[i][threadIdx.x];
+    for (int i = 1; i < 8; ++i) mm = fmaxf(mm, st[0][i]);
+    ll = 0.0f;
+    o = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float k = scale(st[0][i], mm);
+        ll = __builtin_fmaf(st[1][i], k, ll);
+        const f32x4 v = part[i][threadIdx.x];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(v[e], k, o[e]);
     }
     cache_attn_out<DT>(a, b, hk, row, d, o, mm, ll);
 }

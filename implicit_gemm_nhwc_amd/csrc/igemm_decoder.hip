@@ -471,7 +471,7 @@ CacheAttnPlan cache_attn_plan(const igc_cache_attn* p) {
     x.capacity = p->table_entries * c.page_tokens;
     const int64_t hr = c.kv_heads * x.row_tiles;
     x.slots = hr ? kCacheFill * kNumCUs / hr : 0;
-    x.split = cache_splits(x.slots, p->batch) && x.capacity > 4 * kCacheUnit;
+    x.split = cache_splits(x.slots, p->batch) && x.capacity > 1024;
     if (!x.split) x.slots = p->batch;
     x.groups = hr * (x.split ? cache_slots_bound(x.slots, p->batch, x.capacity) : p->batch);
     if (x.split) {
@@ -503,7 +503,7 @@ int32_t check_cache_attn(const igc_cache_attn* p, Tensor* q, Tensor* o, CacheAtt
     if (p->batch && p->q_len && p->q_heads && !p->lens) return IGC_DECLINE_NULL_POINTER;
     if (!aligned(p->lens, 4) || !aligned(p->lse, 4)) return IGC_DECLINE_ALIGNMENT;
     *plan = cache_attn_plan(p);
-    if (!launchable(plan->groups, kCacheWaves * 64) ||
+    if (!launchable(plan->groups, 2 * kCacheWaves * 64) ||
         !launchable(p->batch * c.kv_heads * plan->row_tiles, 32 * 256))
         return IGC_DECLINE_SIZE_LIMIT;
     const size_t lb = (size_t)(p->batch * p->q_heads * p->q_len) * 4, bb = (size_t)p->batch * 4;

@@ -23,7 +23,10 @@ int64_t row(int id, int heads, int head, int64_t p, int shift) {
 int len(int n, int64_t capacity) { return igc::cache_len(n, capacity); }
 int splits(int64_t slots, int64_t b) { return igc::cache_splits(slots, b); }
 uint32_t units(int n) { return igc::cache_units(n); }
-uint32_t chunk(uint32_t total, uint32_t slots, uint32_t b) { return igc::cache_chunk(total, slots, b); }
+uint32_t chunk(uint32_t total, uint32_t per) { return igc::cache_chunk(total, per); }
+int bisect() { return igc::kCacheBisect; }
+int unit() { return igc::kCacheUnit; }
+int least() { return igc::kCacheLeast; }
 uint32_t parts(int n, uint32_t chunk) { return igc::cache_parts(n, chunk); }
 int64_t bound(int64_t slots, int64_t b, int64_t cap) { return igc::cache_slots_bound(slots, b, cap); }
 }
@@ -45,7 +48,7 @@ def plan(tmp_path_factory):
     L.splits.argtypes = [i64, i64]
     u32 = ctypes.c_uint32
     L.units.argtypes, L.units.restype = [ctypes.c_int], u32
-    L.chunk.argtypes, L.chunk.restype = [u32] * 3, u32
+    L.chunk.argtypes, L.chunk.restype = [u32] * 2, u32
     L.bound.argtypes, L.bound.restype = [i64] * 3, i64
     L.parts.argtypes, L.parts.restype = [ctypes.c_int, u32], u32
     return L
@@ -87,15 +90,21 @@ def test_division(plan):
             continue
         total = sum(plan.units(n) for n in lens)
         assert total < 1 << 32
-        c = plan.chunk(total, slots, b)
-        assert c >= 2 and (c == 2 or (c - 1) * (slots - b) < total)
+        c, low = plan.chunk(total, slots - b), plan.chunk(total, slots)
+        for _ in range(plan.bisect()):
+            if low < c:
+                mid = low + (c - low) // 2
+                if sum(plan.parts(n, mid) for n in lens) <= slots:
+                    c = mid
+                else:
+                    low = mid + 1
         parts = [plan.parts(n, c) for n in lens]
-        assert sum(parts) <= room
+        assert c >= plan.least() and sum(parts) <= room
         for n, k in zip(lens, parts):
             assert k >= 1
             at = 0
             for i in range(k):
-                lo, hi = i * c * 256, min((i + 1) * c * 256, n)
+                lo, hi = i * c * plan.unit(), min((i + 1) * c * plan.unit(), n)
                 assert lo == at and (hi > lo or n == 0)
                 at = max(hi, at)
             assert at == n
