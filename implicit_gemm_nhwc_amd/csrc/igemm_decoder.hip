@@ -471,7 +471,7 @@ CacheAttnPlan cache_attn_plan(const igc_cache_attn* p) {
     x.capacity = p->table_entries * c.page_tokens;
     const int64_t hr = c.kv_heads * x.row_tiles;
     x.slots = hr ? kCacheFill * kNumCUs / hr : 0;
-    x.split = cache_splits(x.slots, p->batch) && x.capacity > 1024;
+    x.split = p->batch > 0 && cache_splits(x.slots, p->batch) && x.capacity > 1024;
     if (!x.split) x.slots = p->batch;
     x.groups = hr * (x.split ? cache_slots_bound(x.slots, p->batch, x.capacity) : p->batch);
     if (x.split) {

@@ -223,16 +223,18 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(L
             barrier();
         }
     };
-    // what the results need: a thread's column, a lane's rows
-    const int my_col = min(n0 + (int)threadIdx.x % B, a.N - 1);
-    const float my_ws = a.ws[my_col], my_bs = a.bias ? a.bias[my_col] : 0.0f;
-    float xs[MB];
-    auto row_scales = [&] {
+    // What the results need: a thread's column, a lane's rows.  The large tile
+    // has no registers for it before its sums are done.
+    float my_ws, my_bs, xs[MB];
+    auto scales = [&] {
+        const int c = min(n0 + (int)threadIdx.x % B, a.N - 1);
+        my_ws = a.ws[c];
+        my_bs = a.bias ? a.bias[c] : 0.0f;
 #pragma unroll
         for (int i = 0; i < MB; ++i)
             xs[i] = a.xs[min(m0 + (wm * MB + i) * 32 + (lane & 31), a.M - 1)];
     };
-    if constexpr (B < 256) row_scales();   // the large tile has no registers for them yet
+    if constexpr (B < 256) scales();
     i32x4 xf[2][MB], wf[2][MB];
     // rows of a block start at multiples of 32
     const uint8_t* xl = lds + (wm * MB * 32 + (lane & 31)) * KT;
@@ -296,11 +298,11 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(L
     barrier();
     float* col = reinterpret_cast<float*>(lds);   // [2][B]
     static_assert(B <= NW * 64, "a column a thread");
+    if constexpr (B == 256) scales();
     if ((int)threadIdx.x < B) {
         col[threadIdx.x] = my_ws;
         col[B + threadIdx.x] = my_bs;
     }
-    if constexpr (B == 256) row_scales();
     __syncthreads();
     constexpr int OC = MB * 4, RL = 64 / OC;   // 16-byte chunks of a row; rows a store
     uint8_t* out = lds + 2 * B * 4 + wave * (32 * OC * 16);
@@ -335,6 +337,7 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void linear_i8_tile_kernel(L
                 const int ch = 4 * j + 2 * gg + half;
                 *reinterpret_cast<u32x4*>(out + (r * OC + (ch ^ (r & (OC - 1)))) * 16) =
                     u32x4{p[0], q[0], p[1], q[1]};
+                __builtin_amdgcn_sched_barrier(0);   // a block's sums at a time: no spills
             }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's own rows
 #pragma unroll

@@ -206,6 +206,8 @@ def test_empty_extents():
     for b, tq, hq in ((0, 1, 4), (2, 0, 4), (2, 1, 0)):
         q = torch.zeros(b, tq, hq, 32, dtype=BF, device=DEV)
         assert igc.cache_attention(q, cache, table[:b], n[:b]).shape == q.shape
+        long = torch.zeros(b, 200, dtype=torch.int32, device=DEV)
+        assert igc.cache_attention(q, cache, long, n[:b]).shape == q.shape
     q = _q(BF, 2, 1, 4, 32)
     out = igc.cache_attention(q, cache, table[:, :0], n)
     assert (out == 0).all()
