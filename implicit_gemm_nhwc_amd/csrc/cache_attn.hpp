@@ -308,14 +308,15 @@ __global__ __launch_bounds__(NW * 64, RB == 1 ? 4 : 2) void cache_attn_kernel(Ca
     const int parts = __builtin_amdgcn_readfirstlane(at.parts);
     const int begin = __builtin_amdgcn_readfirstlane((int)at.begin);
     const int end = __builtin_amdgcn_readfirstlane((int)at.end);
-    const int len = __builtin_amdgcn_readfirstlane(at.len);
+    // the length as given places the new tokens, also past the table
+    typedef __attribute__((address_space(4))) const int32_t* sp;
+    const int given = max(((sp)x.lens)[b], 0);
     const int hk = hr / a.row_tiles, row0 = (hr - hk * a.row_tiles) * ROWS;
     const int t0 = div_g(a, row0);
 
     Stage stage;
     stage.init(lane, x.Dp);
     // scalar loads: a vector load's wait would be one for the stages in flight
-    typedef __attribute__((address_space(4))) const int32_t* sp;
     const sp table = (sp)(x.table + b * x.table_stride);
     constexpr int STEP = NW * 32;
     // Entries of the two halves of the block at j, and the pages they name: the
@@ -351,7 +352,7 @@ __global__ __launch_bounds__(NW * 64, RB == 1 ? 4 : 2) void cache_attn_kernel(Ca
                                                   : 64 * (s >> 1) + 16 * quarter + 8 * (s & 1);
             qf[i][s] = __builtin_bit_cast(i32x4, load16(rs, d < a.D ? off + 2 * d : kOut));
         }
-        last[i] = x.causal ? len - (a.Tq - 1 - div_g(a, min(row, a.rows - 1))) : len;
+        last[i] = x.causal ? given - (a.Tq - 1 - div_g(a, min(row, a.rows - 1))) : given;
     }
     f32x4 acc[RB][DB];
     float m[RB], l[RB];

@@ -179,9 +179,9 @@ int32_t kv_cache_read_check(const igc_kv_io* args);
 /*
  * Attention of new tokens over the cache.  q, out [batch, q_len, q_heads,
  * head_dim], kv_heads dividing q_heads; lens int32 [batch]: the tokens that a
- * sequence holds, at positions 0 .. lens[b] - 1 (limited to what its row of
- * the table reaches; a negative length is 0).  With causal != 0 the new tokens
- * are the last q_len of them: token i attends to positions below
+ * sequence holds, at positions 0 .. lens[b] - 1 (a negative length is 0;
+ * positions past the table are not attended to).  With causal != 0 the new
+ * tokens are the last q_len of the lens[b]: token i attends to positions below
  * lens[b] - (q_len - 1 - i).  With the values held, k_j and v_j, and as in
  * cross_attn_fwd:
  *   s_j = scale * q . k_j,  lse = log sum_j exp(s_j),  out = sum_j p_j v_j

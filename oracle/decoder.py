@@ -100,10 +100,11 @@ def cache_attention(q, kq, ks, vq, vs, table, lens, *, causal=True, scale=None):
          "n": torch.zeros(b, tq).long()}
     for i in range(b):
         row = table[i].tolist()
-        n = min(max(int(lens[i]), 0), len(row) * tokens)
+        given = max(int(lens[i]), 0)
+        n = min(given, len(row) * tokens)
         k, v = cache_rows(kq, ks, row, n, d), cache_rows(vq, vs, row, n, d)
         for t in range(tq):
-            m = n - (tq - 1 - t) if causal else n
+            m = min(given - (tq - 1 - t) if causal else given, n)
             if m <= 0:
                 continue
             r["n"][i, t] = m

@@ -119,3 +119,9 @@ def test_cache_attention_is_attention_to_what_it_holds():
         want = attention.cross_attention(q[:, t:t + 1], k, v, kv_lens=lens - (3 - t), scale=0.1)
         assert torch.allclose(r["out"][:, t:t + 1], want["out"], atol=1e-13)
     assert (r["out"][1, 0] == 0).all() and (r["out"][1, 1] != 0).any() and (r["out"][2] == 0).all()
+    # a length past the table's 32 positions places the tokens all the same
+    far = oracle.cache_attention(q, kq, ks, vq, vs, table, torch.tensor([34, 3, 0]), scale=0.1)
+    near = oracle.cache_attention(q[:, :2], kq, ks, vq, vs, table, torch.tensor([32, 1, 0]), scale=0.1)
+    assert torch.equal(far["out"][0, :2], near["out"][0])
+    assert torch.equal(far["lse"][0, :, 3], near["lse"][0, :, 1] * 0 + oracle.cache_attention(
+        q[:, 3:], kq, ks, vq, vs, table, torch.tensor([32, 1, 0]), scale=0.1)["lse"][0, :, 0])

@@ -123,6 +123,14 @@ def test_lengths_past_the_table():
     want = igc.cache_attention(q, cache, table, n)
     n[0] = (1 << 31) - 1
     assert torch.equal(igc.cache_attention(q, cache, table, n), want)
+    # new tokens keep their places when some lie past the table (padding)
+    for entries, tq, lens in ((3, 6, [50, 45]), (80, 4, [1282, 1281])):
+        cache, table, n = _pool(2, entries, 1, 32, 16, lens)
+        q = _q(BF, 2, tq, 2, 32)
+        out, lse = igc.cache_attention(q, cache, table, n, return_lse=True)
+        _check(q, cache, table, n, out, lse)
+        short = n - 2
+        assert torch.equal(igc.cache_attention(q[:, :-2], cache, table, short), out[:, :-2])
 
 
 def test_pages_outside_the_pool():
