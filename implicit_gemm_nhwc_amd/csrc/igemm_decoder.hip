@@ -256,10 +256,12 @@ int32_t check_quant(const igc_quantize_rows* p, Rows* x, Rows* q) {
 }
 
 // ------------------------------------------------------------ their product
-// The largest tiles that still give every CU one; smaller ones fill the card
-// with fewer rows or columns.
+// Few rows, whose workgroups each read x again (32 rows x 4096 x 4096: 7.9 us,
+// tiles 8.7; x 8192 x 8192: 26 and 16), or the largest tiles that still give
+// every CU one; smaller ones fill the card with fewer rows or columns.
 LinForm lin_form(const igc_linear_i8* p) {
-    if (p->m <= kFewRows) return {0, 1, ceil_div(p->n, 16), kFewWaves * 64};
+    if (p->m <= 16 || (p->m <= kFewRows && p->n * p->k <= (int64_t)1 << 25))
+        return {0, 1, ceil_div(p->n, 16), kFewWaves * 64};
     for (int tile : {256, 128}) {
         const LinForm f{tile, ceil_div(p->m, tile), ceil_div(p->n, tile), 256};
         if (f.tiles_m * f.tiles_n >= kNumCUs) return f;

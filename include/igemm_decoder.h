@@ -105,8 +105,8 @@ int32_t quantize_rows_check(const igc_quantize_rows* args);
  *   y        dtype (bf16 or fp16) [m][n], any row pitch (elements) from n on,
  *            and any alignment of the type
  * Limits: k from 0 to 131071, m and n below 2^31, pitches of x and w below 2^22
- * and of y below 2^40; a launch holds fewer than 2^32 threads (at most 32 rows:
- * 512 for every 16 columns; otherwise 256 for a tile of 256 x 256, 128 x 128 or
+ * and of y below 2^40; a launch holds fewer than 2^32 threads (256 for
+ * every 16 columns of at most 32 rows, or for a tile of 256 x 256, 128 x 128 or
  * 64 x 64, the largest that fills the card).
  */
 typedef struct igc_linear_i8 {

@@ -55,7 +55,8 @@ CASES = [
     (HF, 33, 128, 64, True), (BF, 64, 5000, 129, True), (HF, 5, 131071, 18, True),
     (BF, 65, 64, 64, True), (HF, 65, 1, 3, True), (BF, 100, 127, 65, False),
     (HF, 1001, 1000, 777, True), (BF, 129, 129, 1031, True), (HF, 500, 272, 63, True),
-    (BF, 70, 20000, 200, True),
+    (BF, 70, 20000, 200, True), (BF, 20, 6000, 6001, True), (HF, 18, 1300, 500, False),
+    (BF, 520, 700, 2100, True),
     (HF, 2100, 100, 2111, True), (BF, 1920, 2048, 2048, False), (HF, 2049, 129, 2050, True),
     (BF, 4100, 200, 4200, True), (HF, 4096, 1024, 4096, False), (BF, 8193, 1030, 2300, True),
 ]
