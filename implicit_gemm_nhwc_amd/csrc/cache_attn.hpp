@@ -307,12 +307,15 @@ __global__ __launch_bounds__(NW * 64, RB == 1 ? 4 : 2) void cache_attn_kernel(Ca
     const int b = __builtin_amdgcn_readfirstlane(at.b), hr = __builtin_amdgcn_readfirstlane(at.hr);
     const int parts = __builtin_amdgcn_readfirstlane(at.parts);
     const int begin = __builtin_amdgcn_readfirstlane((int)at.begin);
-    const int end = __builtin_amdgcn_readfirstlane((int)at.end);
+    int end = __builtin_amdgcn_readfirstlane((int)at.end);
     // the length as given places the new tokens, also past the table
     typedef __attribute__((address_space(4))) const int32_t* sp;
     const int given = max(((sp)x.lens)[b], 0);
     const int hk = hr / a.row_tiles, row0 = (hr - hk * a.row_tiles) * ROWS;
     const int t0 = div_g(a, row0);
+    // keys past what the last of these rows sees are not read (a prompt of 2048
+    // tokens, 16 heads of 128 over 4 key heads: 130 -> 102 us)
+    if (x.causal) end = min(end, given - (a.Tq - 1 - div_g(a, min(row0 + ROWS, a.rows) - 1)));
 
     Stage stage;
     stage.init(lane, x.Dp);

@@ -88,6 +88,11 @@ CASES = [
     (BF, 1, 2, 1, 56, 16, 70, [(97 * i) % 1121 for i in range(100)]),   # sequences past a wave
     (HF, 1, 40, 1, 128, 256, 12, [3071, 2500]),           # two row tiles, split
     (BF, 1, 10, 10, 128, 1024, 3, [2000]),
+    # prompts: a causal row tile stops where its last row does, parts of a split
+    # may hold none of its keys
+    (BF, 300, 4, 2, 64, 64, 40, [2500, 300, 150]),
+    (HF, 1200, 2, 1, 32, 32, 40, [1280]),
+    (BF, 90, 12, 12, 128, 16, 7, [90, 112, 1]),
 ]
 
 
