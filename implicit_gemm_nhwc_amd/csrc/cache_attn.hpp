@@ -42,13 +42,7 @@ struct CacheAttnArgs {
     int split;             // whether workgroups share a sequence (then a join follows)
 };
 
-// Waves a workgroup: eight, of which two workgroups share a CU where sequences
-// are split; sixteen where a workgroup of at most 16 rows reads a whole
-// sequence of more than one round of eight.
-constexpr int kCacheWaves = 8;
-inline bool cache_whole(bool split, int64_t capacity) {
-    return !split && capacity > 32 * kCacheWaves;
-}
+constexpr int kCacheWaves = 8;   // a workgroup
 // The running maximum follows the true one only when a row exceeds it by
 // 2^kCacheSlack: it only guards the range.
 constexpr float kCacheSlack = 8.0f;
@@ -268,10 +262,10 @@ __device__ __forceinline__ float sum_quarters(float x) {
     return sum_halves(a + b);
 }
 
-template <int DT, int DP, int RB, int NW>
-__global__ __launch_bounds__(NW * 64, RB == 1 ? 4 : 2) void cache_attn_kernel(CacheAttnArgs x) {
+template <int DT, int DP, int RB>
+__global__ __launch_bounds__(kCacheWaves * 64, RB == 1 ? 4 : 2) void cache_attn_kernel(CacheAttnArgs x) {
     const AttnArgs& a = x.a;
-    constexpr int DB = DP / 16, KS = DP / 32, ROWS = 16 * RB;
+    constexpr int NW = kCacheWaves, DB = DP / 16, KS = DP / 32, ROWS = 16 * RB;
     using Stage = CacheStage<DP>;
     constexpr int OWN = 2 * Stage::BYTES;   // a wave's keys and values, then 16 rows of results
     static_assert(OWN >= 16 * DP * 4, "a wave's results fit its stages");
@@ -316,6 +310,8 @@ __global__ __launch_bounds__(NW * 64, RB == 1 ? 4 : 2) void cache_attn_kernel(Ca
     // keys past what the last of these rows sees are not read (a prompt of 2048
     // tokens, 16 heads of 128 over 4 key heads: 130 -> 102 us)
     if (x.causal) end = min(end, given - (a.Tq - 1 - div_g(a, min(row0 + ROWS, a.rows) - 1)));
+    const bool empty = x.pages == 0;   // a pool without pages: nothing to read
+    const int stop = empty ? 0 : end;
 
     Stage stage;
     stage.init(lane, x.Dp);
@@ -367,19 +363,24 @@ __global__ __launch_bounds__(NW * 64, RB == 1 ? 4 : 2) void cache_attn_kernel(Ca
         l[i] = 0.0f;
     }
 
+    if (empty) {   // rows with a key are NaN
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+            if (min(last[i], end) > begin) l[i] = __builtin_nanf("");
+    }
     const int j0 = begin + wave * 32;
     int id0 = 0, id1 = 0, nx0 = 0, nx1 = 0;
     // Without a split the first block is asked for before the length is here;
     // whatever the table says past it, the places exist.
-    if (j0 < (x.split ? end : (int)x.capacity)) {
+    if (j0 < (x.split || empty ? stop : (int)x.capacity)) {
         entries(j0, &nx0, &nx1);
         id0 = page(nx0, j0);
         id1 = page(nx1, j0 + 16);
         issue(0, j0, id0, id1);
         issue(1, j0, id0, id1);
     }
-    for (int j = j0; j < end; j += STEP) {
-        const bool more = j + STEP < end;
+    for (int j = j0; j < stop; j += STEP) {
+        const bool more = j + STEP < stop;
         if (more) entries(j + STEP, &nx0, &nx1);
         // the keys: all but the values asked for after them
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Stage::LOADS) : "memory");

@@ -40,8 +40,8 @@ IGC_HD inline int cache_len(int len, int64_t capacity) {
 // sequences of up to 4099 tokens with 5 drafts: 21.8 -> 21.2 us).  slots < 2 B:
 // one workgroup each.  With slots up to 512, B is at most 256 where there is
 // a division, and sum n_b stays below 2^32.
-constexpr int kCacheUnit = 128;    // keys: half a round of a workgroup's waves
-constexpr int kCacheLeast = 4;     // units a split at least
+constexpr int kCacheUnit = 128;   // keys: half a round of a workgroup's waves
+constexpr int kCacheLeast = 2;     // units a split at least
 constexpr int kCacheMostSlots = 512;
 constexpr int kCacheBisect = 4;
 

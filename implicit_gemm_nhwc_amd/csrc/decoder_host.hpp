@@ -77,9 +77,7 @@ hipError_t launch_linear_i8(const LinArgs& a, int tile, hipStream_t stream);
 template <int DT>
 hipError_t launch_kv_cache(const CacheArgs& a, bool write, hipStream_t stream);
 
-// Workgroups of the attention over the cache that split launches aim at, a CU.
-constexpr int kCacheFill = 2;
-static_assert(kCacheFill * kNumCUs <= kCacheMostSlots, "unit sums fit 32 bits");
+static_assert(2 * kNumCUs <= kCacheMostSlots, "unit sums of split sequences fit 32 bits");
 
 // groups: workgroups of the launch.
 template <int DT>

@@ -350,6 +350,36 @@ int32_t check_table(const int32_t* table, int64_t batch, int64_t stride, int64_t
     return IGC_OK;
 }
 
+// Whether two outputs of one shape [n0, n1, n2, d] share no element: they lie
+// apart, or have the same strides and the blocks of some inner axes of the one
+// lie between those of the other (the halves of one buffer's rows, say).
+bool outputs_apart(const Tensor& x, const Tensor& y, const int64_t n[3], int64_t d) {
+    if (!meet(x.p, x.bytes, y.p, y.bytes)) return true;
+    if (x.b != y.b || x.t != y.t || x.h != y.h) return false;
+    const uintptr_t a = (uintptr_t)x.p, b = (uintptr_t)y.p;
+    const int64_t delta = (int64_t)(a < b ? b - a : a - b);
+    struct Axis { int64_t n, s; } ax[3] = {{n[0], x.b}, {n[1], x.t}, {n[2], x.h}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (ax[j].s < ax[i].s) {
+                const Axis t = ax[i];
+                ax[i] = ax[j];
+                ax[j] = t;
+            }
+    int64_t block = 2 * d;   // bytes of the inner `i` axes
+    for (int i = 0; i < 3; ++i) {
+        if (delta >= block) {
+            int64_t both = block + delta;
+            int j = i;
+            for (; j < 3 && (ax[j].n == 1 || ax[j].s >= both); ++j)
+                both += (ax[j].n - 1) * ax[j].s;
+            if (j == 3) return true;
+        }
+        block += (ax[i].n - 1) * ax[i].s;
+    }
+    return false;
+}
+
 // Runs of tokens that a workgroup of kv_cache_write / read takes, a sequence;
 // workgroups of a launch.
 int64_t io_runs(const igc_kv_io* p) {
@@ -391,9 +421,8 @@ int32_t check_io(const igc_kv_io* p, bool write, Tensor t[2]) {
             for (int i = 0; i < 2; ++i)
                 if (meet(s.p, s.n, t[i].p, t[i].bytes)) return IGC_DECLINE_OVERLAP;
     }
-    // the two outputs may interleave in one buffer, not meet in an element:
-    // the halves of one projection are strided views of the same rows
-    if (!write && t[0].p == t[1].p) return IGC_DECLINE_OVERLAP;
+    const int64_t n[3] = {p->batch, p->tokens, c.kv_heads};
+    if (!write && !outputs_apart(t[0], t[1], n, c.head_dim)) return IGC_DECLINE_OVERLAP;
     return IGC_OK;
 }
 
@@ -464,6 +493,16 @@ int32_t check_cache_attn_shape(const igc_cache_attn* p) {
     return IGC_OK;
 }
 
+// Rows of a workgroup: 16 where that holds them all (4 x 65537 tokens, 4 rows a
+// key head: 89 us, 32 rows 106; 8 x 784: 9.6 and 12.5).  A sequence is split
+// between workgroups from 769 tokens on (8 sequences, 16 heads of 128 over 4
+// key heads, 704 tokens: 9.9 us whole and 10.2 split; 784: 10.2 both; 1024: 12.1
+// and 10.3), where the card has a workgroup a CU for three of each, or for two
+// of 32 rows, which fill a CU alone (16 x 4096 with 32 rows: 28 us, two a CU
+// 36); else two a CU that even out ragged lengths (16 x 4099 with 5 drafts: 24
+// and 26; 8 x 4099: 18.6 and 18.2), if those are 2.5 a sequence (24 x 4099: 36.7 us
+// split and 38.0 whole, 28 x 4096: 42.6 and 40.4) or long ones 2 (32 x 16000:
+// 83 and 94).
 CacheAttnPlan cache_attn_plan(const igc_cache_attn* p) {
     CacheAttnPlan x{};
     const igc_kv_cache& c = p->cache;
@@ -472,8 +511,10 @@ CacheAttnPlan cache_attn_plan(const igc_cache_attn* p) {
     x.row_tiles = ceil_div(rows, x.tile);
     x.capacity = p->table_entries * c.page_tokens;
     const int64_t hr = c.kv_heads * x.row_tiles;
-    x.slots = hr ? kCacheFill * kNumCUs / hr : 0;
-    x.split = p->batch > 0 && cache_splits(x.slots, p->batch) && x.capacity > 1024;
+    x.slots = hr ? kNumCUs / hr : 0;
+    if (x.tile == 16 && x.slots < 3 * p->batch) x.slots = hr ? 2 * kNumCUs / hr : 0;
+    const bool fair = x.tile != 16 || x.slots * 2 >= 5 * p->batch || x.capacity > 8192;
+    x.split = p->batch > 0 && cache_splits(x.slots, p->batch) && fair && x.capacity > 768;
     if (!x.split) x.slots = p->batch;
     x.groups = hr * (x.split ? cache_slots_bound(x.slots, p->batch, x.capacity) : p->batch);
     if (x.split) {
@@ -505,9 +546,8 @@ int32_t check_cache_attn(const igc_cache_attn* p, Tensor* q, Tensor* o, CacheAtt
     if (p->batch && p->q_len && p->q_heads && !p->lens) return IGC_DECLINE_NULL_POINTER;
     if (!aligned(p->lens, 4) || !aligned(p->lse, 4)) return IGC_DECLINE_ALIGNMENT;
     *plan = cache_attn_plan(p);
-    if (!launchable(plan->groups, 2 * kCacheWaves * 64) ||
-        !launchable(p->batch * c.kv_heads * plan->row_tiles, 32 * 256))
-        return IGC_DECLINE_SIZE_LIMIT;
+    // (a split leaves at most kCacheMostSlots groups, and so few rows to join)
+    if (!launchable(plan->groups, kCacheWaves * 64)) return IGC_DECLINE_SIZE_LIMIT;
     const size_t lb = (size_t)(p->batch * p->q_heads * p->q_len) * 4, bb = (size_t)p->batch * 4;
     const size_t ws = cache_attn_ws(*plan);
     const struct { const void* p; size_t n; } outs[3] = {
@@ -643,8 +683,7 @@ int32_t cache_attn_fwd(const igc_cache_attn* args, void* stream) {
     x.table = args->table;
     x.lens = args->lens;
     x.table_stride = args->table_stride;
-    // a pool without rows is read nowhere
-    x.capacity = cache_rows(c) ? plan.capacity : 0;
+    x.capacity = plan.capacity;
     x.slots = plan.slots;
     x.entries = (int)args->table_entries;
     x.pages = (int)c.pages;

@@ -30,23 +30,21 @@ hipError_t launch_io(const CacheArgs& a, bool write, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int DT, int DP, int RB, int NW>
+template <int DT, int DP, int RB>
 hipError_t launch_attn(const CacheAttnArgs& x, unsigned groups, hipStream_t stream) {
-    auto kern = cache_attn_kernel<DT, DP, RB, NW>;
-    constexpr size_t lds = (size_t)NW * (2 * CacheStage<DP>::BYTES + 32 * 4);
+    auto kern = cache_attn_kernel<DT, DP, RB>;
+    constexpr size_t lds = (size_t)kCacheWaves * (2 * CacheStage<DP>::BYTES + 32 * 4);
     static LdsAttr attr;
     const hipError_t e = ensure_lds(attr, (const void*)kern, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3(groups), dim3(NW * 64), lds, stream, x);
+    hipLaunchKernelGGL(kern, dim3(groups), dim3(kCacheWaves * 64), lds, stream, x);
     return hipGetLastError();
 }
 
 template <int DT, int DP>
 hipError_t launch_attn(const CacheAttnArgs& x, unsigned groups, hipStream_t stream) {
-    if (x.tile != 16) return launch_attn<DT, DP, 2, kCacheWaves>(x, groups, stream);
-    return cache_whole(x.split, x.capacity)
-               ? launch_attn<DT, DP, 1, 2 * kCacheWaves>(x, groups, stream)
-               : launch_attn<DT, DP, 1, kCacheWaves>(x, groups, stream);
+    return x.tile == 16 ? launch_attn<DT, DP, 1>(x, groups, stream)
+                        : launch_attn<DT, DP, 2>(x, groups, stream);
 }
 
 }  // namespace

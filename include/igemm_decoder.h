@@ -155,7 +155,8 @@ typedef struct igc_kv_cache {
  * place that one call writes twice (a page shared by sequences that both
  * write to it) holds a mix of the two rows afterwards.
  * kv_cache_read writes all of k and v: zeros at i >= lens[b], NaN where the
- * position or the page does not exist.
+ * position or the page does not exist.  k and v may interleave in one buffer,
+ * with the same strides, and not share an element.
  * Limits: batch, tokens below 2^31; a launch holds one group of 4 to 16 lanes
  * (head_dim / 8, rounded up to a power of two) for every four heads of a
  * token, of keys and of values, a sequence's tokens rounded up to a workgroup
@@ -191,12 +192,12 @@ int32_t kv_cache_read_check(const igc_kv_io* args);
  *   lse  fp32 [batch, q_heads, q_len], dense, or NULL
  * The integers enter the matrix products as they are; p_j times the value's
  * scale is held in 16 significant bits, sums in fp32.  Sequences of more than
- * 1024 tokens (by the table's capacity) may be read by several workgroups,
+ * 768 tokens (by the table's capacity) may be read by several workgroups,
  * whose results (fp32, in the workspace) a second launch joins in a fixed
  * order: results do not change from run to run.
  * Limits: as cross_attn_fwd for q and out; the table's capacity below
  * 2^31 - 4096, batch * q_heads below 2^31, batch * kv_heads times the tiles of
- * 32 rows (q_len * q_heads / kv_heads) below 2^19.
+ * 32 rows (q_len * q_heads / kv_heads) below 2^23.
  */
 typedef struct igc_cache_attn {
     igc_kv_cache cache;

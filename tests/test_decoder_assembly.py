@@ -55,7 +55,7 @@ def built(request, tmp_path_factory):
 def test_no_copy_before_a_mask_is_restored(built):
     _, code = built
     for part, least in (("layer_norm_", 50), ("quantize_rows", 28), ("kv_cache_", 12),
-                        ("cache_attn_", 24), ("linear_i8_", 10)):
+                        ("cache_attn_", 18), ("linear_i8_", 10)):
         assert sum(part in n for n in code) >= least, part
     for name, body in code.items():
         assert copies_before_a_restore(body) == [], name

@@ -175,6 +175,13 @@ def _io(**kw):
     return _cache(**kw) + D._IO.pack(*f.values())
 
 
+def _pair(h, delta, t=None, b=None):
+    """k and v of the same strides, v `delta` elements behind k."""
+    t = t or 6 * h
+    b = b or 50 * t
+    return dict(x_h=h, x_t=t, x_b=b, y_h=h, y_t=t, y_b=b, y=X + 2 * delta)
+
+
 CACHE_BAD = [
     (dict(page=8), "shape"), (dict(page=24), "shape"), (dict(page=2048), "shape"),
     (dict(pages=-1), "shape"), (dict(heads=-1), "shape"), (dict(d=0), "head_dim"),
@@ -211,9 +218,17 @@ def test_cache_refusals_of_one_direction():
         assert _reason(L.kv_cache_write_check(_io(**kw))) == "overlap"
         assert L.kv_cache_read_check(_io(**kw)) == 0
     for kw in (dict(table=X), dict(start=G + 64), dict(lens=X + 64), dict(x_t=0), dict(y_h=64),
-               dict(y=X)):
-        assert _reason(L.kv_cache_read_check(_io(**kw))) == "overlap"
+               dict(y=X), dict(y=X + 16), dict(y=X + 6 * 72 * 2), dict(y=X + 144),
+               _pair(h=144, delta=64), _pair(h=144, delta=80), _pair(h=72, t=864, delta=424),
+               _pair(h=72, t=864, delta=864), _pair(h=72, t=432, b=43200, delta=21608),
+               dict(_pair(h=72, t=864, delta=432), y_h=144)):
+        assert _reason(L.kv_cache_read_check(_io(**kw))) == "overlap", kw
         assert L.kv_cache_write_check(_io(**kw)) == 0
+    # halves of heads' rows, of tokens and of sequences; either first
+    for kw in (_pair(h=144, delta=72), _pair(h=72, t=864, delta=432), _pair(h=72, t=880, delta=440),
+               _pair(h=72, t=432, b=43200, delta=21600), _pair(h=3600, t=72, b=43200, delta=21600),
+               dict(_pair(h=144, delta=72), x=X + 144, y=X), dict(y=X + 3 * 50 * 6 * 72 * 2)):
+        assert L.kv_cache_read_check(_io(**kw)) == 0, kw
 
 
 def test_cache_accepted():
@@ -242,7 +257,7 @@ def _attn(**kw):
     (dict(scale=0.0), "scale"), (dict(scale=math.nan), "scale"), (dict(scale=1e300), "scale"),
     (dict(scale=1e-40), "scale"), (dict(b=1 << 31), "size_limit"),
     (dict(b=1 << 29), "size_limit"), (dict(tq=1 << 30), "size_limit"),
-    (dict(entries=1 << 26), "size_limit"), (dict(b=1 << 18), "size_limit"),
+    (dict(entries=1 << 26), "size_limit"), (dict(b=1 << 21), "size_limit"),
     (dict(q_t=1 << 23), "size_limit"), (dict(q_h=1 << 23), "size_limit"),
     (dict(hq=1536, q_h=(1 << 23) - 8), "size_limit"),
     (dict(q=0), "null_pointer"), (dict(o=0), "null_pointer"), (dict(lens=0), "null_pointer"),
@@ -272,7 +287,7 @@ def test_cache_attention_accepted():
 
 def test_cache_attention_workspace():
     L = igc.lib()
-    assert L.cache_attn_fwd_workspace_bytes(_attn(entries=32)) == 0      # 1024 tokens: no split
+    assert L.cache_attn_fwd_workspace_bytes(_attn(entries=24)) == 0      # 768 tokens: no split
     need = L.cache_attn_fwd_workspace_bytes(_attn())
     assert need > 0 and need % 4 == 0
     assert L.cache_attn_fwd_check(_attn(ws=WS, ws_bytes=need)) == 0

@@ -224,8 +224,17 @@ def test_empty_extents():
     q = _q(BF, 2, 1, 4, 32)
     out = igc.cache_attention(q, cache, table[:, :0], n)
     assert (out == 0).all()
+    # a pool without pages: every page of a table is outside it
     none = igc.KVCache.empty(0, 16, 2, 32, device=DEV)
-    assert (igc.cache_attention(q, none, table, n) == 0).all()
+    n[1] = 0
+    for entries in (2, 200):
+        t = torch.zeros(2, entries, dtype=torch.int32, device=DEV)
+        out, lse = igc.cache_attention(q, none, t, n, return_lse=True)
+        assert out[0].isnan().all() and lse[0].isnan().all()
+        assert (out[1] == 0).all() and torch.isinf(lse[1]).all()
+        new = _q(BF, 2, 40, 4, 32)   # the first 20 attend to nothing
+        out = igc.cache_attention(new, none, t, n)
+        assert (out[0, :20] == 0).all() and out[0, 20:].isnan().all() and (out[1] == 0).all()
 
 
 def test_graph_and_stream():
