@@ -194,17 +194,28 @@ __global__ __launch_bounds__(NT) void layer_norm_fwd_kernel(LnArgs a) {
         const int c = c0 + i * LPR * 8;
         unpack8<DT>(ln_load<DT>(x + 2 * c, live ? a.C - c : 0), v[i]);
     }
+    // Weights asked for before the sums save their round trip, and cost waves
+    // by their registers (154 MB: 64 channels 59 us, after the sums 65; 16384 65
+    // and 70; but 333 99 and 89, 4096 72 and 65).
+    constexpr bool EARLY = LPR > 64 ? NC >= 3 : NC <= 2;
+    float w[NC][8], b[NC][8];
+    auto weights = [&](int i) {
+        ln_weights(a.w, c0 + i * LPR * 8, a.C, 1.0f, w[i]);
+        ln_weights(a.b, c0 + i * LPR * 8, a.C, 0.0f, b[i]);
+    };
+    if constexpr (EARLY) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) weights(i);
+    }
     const float r = ln_stats<LPR, NC>(sum, v, c0, a.C, a.inv_c, a.eps);
     if (!live) return;
     uint8_t* y = a.out + ln_row(a, a.o_s, row);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = c0 + i * LPR * 8;
-        float w[8], b[8];
-        ln_weights(a.w, c, a.C, 1.0f, w);
-        ln_weights(a.b, c, a.C, 0.0f, b);
+        if constexpr (!EARLY) weights(i);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j] * r, w[j], b[j]);
+        for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j] * r, w[i][j], b[i][j]);
         ln_store<DT>(y + 2 * c, a.C - c, v[i]);
     }
 }
