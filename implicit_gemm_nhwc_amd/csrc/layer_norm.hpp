@@ -39,28 +39,66 @@ __device__ __forceinline__ int64_t ln_row(const LnArgs& a, const int64_t* s, int
     return i0 * s[0] + (i01 - i0 * a.n1) * s[1] + (row - i01 * a.n2) * s[2];
 }
 
-// 8 values from p (2-byte aligned), `left` of them in the row; zeros past it.
-template <int DT>
-__device__ __forceinline__ u32x4 ln_load(const uint8_t* p, int left) {
-    if (left >= 8) return u32x4(*reinterpret_cast<const u32x4h*>(p));
-    u32x4 r = {0, 0, 0, 0};
+// N chunks of 8 values of a row of C, `step` values apart from p (2-byte
+// aligned) on, `left` of them in the row; zeros past it, and only zeros unless
+// `live`.  A chunk that reaches past the row is read as its last 8 values and
+// shifted: one load for every lane (154 MB in rows of 1023: 81 us forward and 97
+// backward; value by value 102 and 205), all of them asked for before the first
+// is looked at.
+template <int N>
+__device__ __forceinline__ void ln_load(const uint8_t* p, int left, int step, int C, bool live,
+                                        u32x4 (&to)[N]) {
+    if (C < 8) {   // one chunk
 #pragma unroll
-    for (int j = 0; j < 7; ++j)
-        if (j < left)
-            r[j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + 2 * j) << (16 * (j & 1));
-    return r;
+        for (int i = 0; i < N; ++i) to[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (live && j < left)
+                to[0][j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + 2 * j)
+                                << (16 * (j & 1));
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        to[i] = u32x4(*reinterpret_cast<const u32x4h*>(
+            p + 2 * (int64_t)(i * step + min(left - i * step - 8, 0))));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        u32x4 r = to[i];
+        const int s = live ? 8 - (left - i * step) : 8;
+        if (s > 0) {
+            if (s & 4) r = u32x4{r[2], r[3], 0, 0};
+            if (s & 2) r = u32x4{r[1], r[2], r[3], 0};
+            if (s & 1)
+                r = u32x4{r[0] >> 16 | r[1] << 16, r[1] >> 16 | r[2] << 16,
+                          r[2] >> 16 | r[3] << 16, r[3] >> 16};
+            if (s >= 8) r = u32x4{0, 0, 0, 0};
+        }
+        to[i] = r;
+    }
 }
 template <int DT>
 __device__ __forceinline__ void ln_store(uint8_t* p, int left, const float* v) {
-    const u32x4 r = pack8<DT>(v);
+    typedef uint32_t u32x2h __attribute__((ext_vector_type(2), aligned(2)));
+    typedef uint32_t u32h __attribute__((aligned(2)));
+    u32x4 r = pack8<DT>(v);
     if (left >= 8) {
         *reinterpret_cast<u32x4h*>(p) = r;
         return;
     }
-#pragma unroll
-    for (int j = 0; j < 7; ++j)
-        if (j < left)
-            *reinterpret_cast<uint16_t*>(p + 2 * j) = (uint16_t)(r[j / 2] >> (16 * (j & 1)));
+    if (left <= 0) return;
+    if (left & 4) {
+        *reinterpret_cast<u32x2h*>(p) = u32x2{r[0], r[1]};
+        p += 8;
+        r[0] = r[2];
+        r[1] = r[3];
+    }
+    if (left & 2) {
+        *reinterpret_cast<u32h*>(p) = r[0];
+        p += 4;
+        r[0] = r[1];
+    }
+    if (left & 1) *reinterpret_cast<uint16_t*>(p) = (uint16_t)r[0];
 }
 // 8 of the C values of w from c on (`none` without w and past the end).
 __device__ __forceinline__ void ln_weights(const float* w, int c, int C, float none, float* v) {
@@ -188,12 +226,11 @@ __global__ __launch_bounds__(NT) void layer_norm_fwd_kernel(LnArgs a) {
     const int row = (int)(blockIdx.x * (NT / LPR) + threadIdx.x / LPR);
     const bool live = row < a.rows;   // rows of more than a wave always are
     const uint8_t* x = a.x + (live ? ln_row(a, a.x_s, row) : 0);
+    u32x4 raw[NC];
+    ln_load(x + 2 * c0, a.C - c0, LPR * 8, a.C, live, raw);
     float v[NC][8];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int c = c0 + i * LPR * 8;
-        unpack8<DT>(ln_load<DT>(x + 2 * c, live ? a.C - c : 0), v[i]);
-    }
+    for (int i = 0; i < NC; ++i) unpack8<DT>(raw[i], v[i]);
     // Weights asked for before the sums save their round trip, and cost waves
     // by their registers (154 MB: 64 channels 59 us, after the sums 65; 16384 65
     // and 70; but 333 99 and 89, 4096 72 and 65).
@@ -247,10 +284,14 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(LnArgs a) {
     auto load = [&](const uint8_t* p, const int64_t* s, int64_t at, u32x4 (&to)[NC]) {
         const bool live = at < a.rows;
         const uint8_t* x = p + ln_row(a, s, live ? (int)at : 0);
+        // a chunk at a time: together they take two registers too many for a
+        // third workgroup a CU (333 channels: 96 us, 127)
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = c0 + i * LPR * 8;
-            to[i] = ln_load<DT>(x + 2 * c, live ? a.C - c : 0);
+            u32x4 one[1];
+            ln_load(x + 2 * c, a.C - c, 0, a.C, live, one);
+            to[i] = one[0];
         }
     };
     u32x4 rx[NC], rg[NC], ng[NC];

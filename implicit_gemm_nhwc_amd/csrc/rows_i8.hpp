@@ -107,11 +107,7 @@ __global__ __launch_bounds__(NT) void quantize_rows_kernel(QuantArgs a) {
     uint32_t top = 0;
     const int segs = LONG ? (a.C + W - 1) / W : 1;
     for (int s = 0; s < segs; ++s) {
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = s * W + c0 + i * LPR * 8;
-            raw[i] = ln_load<DT>(x + 2 * c, live ? a.C - c : 0);
-        }
+        ln_load(x + 2 * (s * W + c0), a.C - (s * W + c0), LPR * 8, a.C, live, raw);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             float v[8];
@@ -123,13 +119,8 @@ __global__ __launch_bounds__(NT) void quantize_rows_kernel(QuantArgs a) {
     if (!live) return;
     uint8_t* q = a.q + i0 * a.q_s[0] + i1 * a.q_s[1] + i2 * a.q_s[2];
     for (int s = segs - 1; s >= 0; --s) {   // the last piece is still here
-        if (s < segs - 1) {
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const int c = s * W + c0 + i * LPR * 8;
-                raw[i] = ln_load<DT>(x + 2 * c, a.C - c);
-            }
-        }
+        if (s < segs - 1)
+            ln_load(x + 2 * (s * W + c0), a.C - (s * W + c0), LPR * 8, a.C, true, raw);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = s * W + c0 + i * LPR * 8, left = a.C - c;
@@ -138,10 +129,20 @@ __global__ __launch_bounds__(NT) void quantize_rows_kernel(QuantArgs a) {
             const u32x2 o = row_bytes(v, rs);
             if (left >= 8) {
                 *reinterpret_cast<u32x2*>(q + c) = o;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 7; ++j)
-                    if (j < left) q[c + j] = (uint8_t)(o[j / 4] >> (8 * (j & 3)));
+            } else if (left > 0) {
+                uint32_t w = o[0];
+                uint8_t* to = q + c;
+                if (left & 4) {
+                    *reinterpret_cast<uint32_t*>(to) = w;
+                    to += 4;
+                    w = o[1];
+                }
+                if (left & 2) {
+                    *reinterpret_cast<uint16_t*>(to) = (uint16_t)w;
+                    to += 2;
+                    w >>= 16;
+                }
+                if (left & 1) *to = (uint8_t)w;
             }
         }
     }
