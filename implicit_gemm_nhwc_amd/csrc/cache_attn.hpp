@@ -1,7 +1,7 @@
 // Attention of a few new tokens over the paged cache in 8 bits.
 //
 // Rows are the Tq * G queries that share one key head, 16 RB a workgroup; its
-// waves take blocks of 32 keys in turn.  With k_j = ks_j K_j and v_j = vs_j V_j
+// eight waves take blocks of 32 keys in turn.  With k_j = ks_j K_j and v_j = vs_j V_j
 // (integers K, V):
 //   s_j = (q . K_j) ks_j scale,  p_j = 2^(s_j log2 e - m),
 //   out = sum (p_j vs_j) V_j / sum p_j
@@ -18,8 +18,14 @@
 //
 // p vs is held as the sum of two bf16 numbers (16 bits of its own), which
 // doubles the second products but leaves the outputs as accurate as fp32
-// probabilities, for both types; the cache's bytes bound the kernel, not the
-// matrix cores.
+// probabilities, for both types; the matrix cores are busy 11 %.
+//
+// Long caches are bound by HBM: 4 sequences of 22000 to 65537 tokens, 8 key heads
+// of 128, in 75 to 80 us (369 MB, 4.6 to 4.9 TB/s), then 4.8 us for the join.  Short
+// ones by vector instructions, of which a block of 32 keys takes about 340, half
+// of them for turning 8-bit values into 16-bit ones (0.8 us a block and SIMD), and
+// by round trips: entry of the table, keys, values.  16 sequences of 4099 with 5
+// drafts, 8 heads of 80: 17 us, vector units 61 % busy.
 #pragma once
 
 #include "attn_common.hpp"
