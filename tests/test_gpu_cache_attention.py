@@ -86,7 +86,7 @@ CASES = [
     (BF, 2, 6, 2, 72, 32, 160, [5100, 0, 2049, 1, 777]),
     (HF, 4, 4, 1, 24, 16, 130, [2080, 1030]),
     (BF, 1, 2, 1, 56, 16, 70, [(97 * i) % 1121 for i in range(100)]),   # sequences past a wave
-    (HF, 1, 40, 1, 128, 256, 12, [3071, 2500]),           # two row tiles, split
+    (HF, 1, 40, 1, 128, 256, 13, [3071, 2500]),           # two row tiles, split
     (BF, 1, 10, 10, 128, 1024, 3, [2000]),
     # prompts: a causal row tile stops where its last row does, parts of a split
     # may hold none of its keys
