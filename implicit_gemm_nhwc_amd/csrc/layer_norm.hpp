@@ -43,12 +43,28 @@ __device__ __forceinline__ int64_t ln_row(const LnArgs& a, const int64_t* s, int
     return i0 * s[0] + (i01 - i0 * a.n1) * s[1] + (row - i01 * a.n2) * s[2];
 }
 
+// 8 values of a row of at least 8 from p (2-byte aligned) on, of which `left` are
+// in the row: where those are fewer, the row's last 8, which ln_trim shifts.
+__device__ __forceinline__ u32x4 ln_fetch(const uint8_t* p, int left) {
+    return u32x4(*reinterpret_cast<const u32x4h*>(p + 2 * (int64_t)min(left - 8, 0)));
+}
+__device__ __forceinline__ u32x4 ln_trim(u32x4 r, int left) {
+    const int s = 8 - left;
+    if (s > 0) {
+        if (s & 4) r = u32x4{r[2], r[3], 0, 0};
+        if (s & 2) r = u32x4{r[1], r[2], r[3], 0};
+        if (s & 1)
+            r = u32x4{r[0] >> 16 | r[1] << 16, r[1] >> 16 | r[2] << 16,
+                      r[2] >> 16 | r[3] << 16, r[3] >> 16};
+        if (s >= 8) r = u32x4{0, 0, 0, 0};
+    }
+    return r;
+}
 // N chunks of 8 values of a row of C, `step` values apart from p (2-byte
 // aligned) on, `left` of them in the row; zeros past it, and only zeros unless
-// `live`.  A chunk that reaches past the row is read as its last 8 values and
-// shifted: one load for every lane (154 MB in rows of 1023: 81 us forward and 97
-// backward; value by value 102 and 205), all of them asked for before the first
-// is looked at.
+// `live`.  One load a chunk for every lane (154 MB in rows of 1023: 81 us forward
+// and 97 backward; value by value 102 and 205), all of them asked for before the
+// first is looked at.
 template <int N>
 __device__ __forceinline__ void ln_load(const uint8_t* p, int left, int step, int C, bool live,
                                         u32x4 (&to)[N]) {
@@ -63,23 +79,9 @@ __device__ __forceinline__ void ln_load(const uint8_t* p, int left, int step, in
         return;
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        to[i] = u32x4(*reinterpret_cast<const u32x4h*>(
-            p + 2 * (int64_t)(i * step + min(left - i * step - 8, 0))));
+    for (int i = 0; i < N; ++i) to[i] = ln_fetch(p + 2 * i * step, left - i * step);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        u32x4 r = to[i];
-        const int s = live ? 8 - (left - i * step) : 8;
-        if (s > 0) {
-            if (s & 4) r = u32x4{r[2], r[3], 0, 0};
-            if (s & 2) r = u32x4{r[1], r[2], r[3], 0};
-            if (s & 1)
-                r = u32x4{r[0] >> 16 | r[1] << 16, r[1] >> 16 | r[2] << 16,
-                          r[2] >> 16 | r[3] << 16, r[3] >> 16};
-            if (s >= 8) r = u32x4{0, 0, 0, 0};
-        }
-        to[i] = r;
-    }
+    for (int i = 0; i < N; ++i) to[i] = ln_trim(to[i], live ? left - i * step : 0);
 }
 template <int DT>
 __device__ __forceinline__ void ln_store(uint8_t* p, int left, const float* v) {
@@ -293,9 +295,13 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(LnArgs a) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = c0 + i * LPR * 8;
-            u32x4 one[1];
-            ln_load(x + 2 * c, a.C - c, 0, a.C, live, one);
-            to[i] = one[0];
+            if constexpr (AHEAD) {   // trimmed in its turn (8191: 113 us, at once 166)
+                to[i] = ln_fetch(x + 2 * c, a.C - c);
+            } else {
+                u32x4 one[1];
+                ln_load(x + 2 * c, a.C - c, 0, a.C, live, one);
+                to[i] = one[0];
+            }
         }
     };
     u32x4 rx[NC], rg[NC], ng[NC];
@@ -314,8 +320,12 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(LnArgs a) {
         float v[NC][8];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
+            if constexpr (AHEAD) {
+                const int left = live ? a.C - (c0 + i * LPR * 8) : 0;
+                rx[i] = ln_trim(rx[i], left);
+                rg[i] = ln_trim(ng[i], left);
+            }
             unpack8<DT>(rx[i], v[i]);
-            if constexpr (AHEAD) rg[i] = ng[i];
         }
         if constexpr (AHEAD) {
             if (k + 1 < rounds) {
