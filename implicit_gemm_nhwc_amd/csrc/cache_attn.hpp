@@ -46,6 +46,7 @@ struct CacheAttnArgs {
     int causal;
     int tile;              // rows a workgroup: 16 or 32
     int split;             // whether workgroups share a sequence (then a join follows)
+    int fixed;             // slots of each sequence, or 0: divided by their lengths
 };
 
 constexpr int kCacheWaves = 8;   // a workgroup
@@ -86,6 +87,17 @@ struct CachePlace {
     int len;
     int slot0;             // slot of part 0 of the sequence's first (key head, row tile)
 };
+
+// The same for sequences with slots of their own, x.fixed a (key head, row
+// tile): no sums over the lengths (8 x 784: 10.2 -> 9.7 us).
+__device__ __forceinline__ void cache_fixed_place(const CacheAttnArgs& x, int b, int hr_n,
+                                                  CachePlace* o) {
+    typedef __attribute__((address_space(4))) const int32_t* sp;
+    o->b = b;
+    o->len = cache_len(((sp)x.lens)[b], x.capacity);
+    o->parts = (int)cache_parts(o->len, kCacheLeast);
+    o->slot0 = b * hr_n * x.fixed;
+}
 
 // Sum of x over the lanes up to this one.
 __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
@@ -287,14 +299,25 @@ __global__ __launch_bounds__(kCacheWaves * 64, RB == 1 ? 4 : 2) void cache_attn_
     const int hr_n = a.Hk * a.row_tiles;
     CachePlace at;
     if (x.split) {
-        CacheDivision div;
-        div.init(x, lane);
-        if (!div.find(x, lane, blockIdx.x, hr_n, -1, &at)) return;   // all waves
-        const int r = (int)blockIdx.x - at.slot0;
-        at.hr = r / at.parts;
-        at.part = r - at.hr * at.parts;
-        at.begin = (int64_t)at.part * div.chunk * kCacheUnit;
-        at.end = at.begin + (int64_t)div.chunk * kCacheUnit;
+        uint32_t chunk = kCacheLeast;
+        if (x.fixed) {
+            at.hr = (int)(blockIdx.x / (uint32_t)x.fixed);
+            at.part = (int)blockIdx.x - at.hr * x.fixed;
+            const int b = at.hr / hr_n;
+            at.hr -= b * hr_n;
+            cache_fixed_place(x, b, hr_n, &at);
+            if (at.part >= at.parts) return;   // all waves
+        } else {
+            CacheDivision div;
+            div.init(x, lane);
+            if (!div.find(x, lane, blockIdx.x, hr_n, -1, &at)) return;   // all waves
+            const int r = (int)blockIdx.x - at.slot0;
+            at.hr = r / at.parts;
+            at.part = r - at.hr * at.parts;
+            chunk = div.chunk;
+        }
+        at.begin = (int64_t)at.part * chunk * kCacheUnit;
+        at.end = at.begin + (int64_t)chunk * kCacheUnit;
         if (at.end > at.len) at.end = at.len;
     } else {
         at.b = blockIdx.x / hr_n;
@@ -604,12 +627,16 @@ __global__ __launch_bounds__(256) void cache_attn_join_kernel(CacheAttnArgs x) {
     const int b = br / hr_n, hr = br - b * hr_n;
     const int hk = hr / a.row_tiles, row = (hr - hk * a.row_tiles) * x.tile + r;
     if (row >= a.rows) return;
-    CacheDivision div;
-    div.init(x, lane);
     CachePlace at;
-    div.find(x, lane, 0, hr_n, b, &at);
+    if (x.fixed) {
+        cache_fixed_place(x, b, hr_n, &at);
+    } else {
+        CacheDivision div;
+        div.init(x, lane);
+        div.find(x, lane, 0, hr_n, b, &at);
+    }
     if (at.parts <= 1) return;   // written where it was read
-    const int64_t slot = at.slot0 + hr * at.parts;
+    const int64_t slot = at.slot0 + hr * (x.fixed ? x.fixed : at.parts);
     const float* stat = a.stat + (slot * rows_tile + r) * 2;
     const float* from = a.part + (slot * rows_tile + r) * a.D + (d < a.D ? d : 0);
     const int64_t pitch = (int64_t)rows_tile * a.D;

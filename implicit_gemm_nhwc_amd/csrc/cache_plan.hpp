@@ -63,13 +63,24 @@ IGC_HD inline uint32_t cache_parts(int len, uint32_t chunk) {
     return n < 1 ? 1 : n;
 }
 
+// Splits of the smallest size that a sequence as long as the table makes.
+IGC_HD inline int64_t cache_most(int64_t capacity) {
+    const int64_t units = (capacity + kCacheUnit - 1) / kCacheUnit;
+    const int64_t most = (units + kCacheLeast - 1) / kCacheLeast;
+    return most < 1 ? 1 : most;
+}
+
+// Whether there is room for that many of every sequence: then each has its own
+// slots, and no division is needed.
+IGC_HD inline bool cache_fixed(int64_t slots, int64_t batch, int64_t capacity) {
+    const int64_t most = cache_most(capacity);
+    return most < slots / batch + 1 && most * batch <= slots;
+}
+
 // Workgroups a (key head, row tile) that a launch needs room for.
 IGC_HD inline int64_t cache_slots_bound(int64_t slots, int64_t batch, int64_t capacity) {
     if (!cache_splits(slots, batch)) return batch;
-    const int64_t units = (capacity + kCacheUnit - 1) / kCacheUnit;
-    int64_t most = (units + kCacheLeast - 1) / kCacheLeast;
-    if (most < 1) most = 1;
-    return most < slots / batch + 1 && most * batch < slots ? most * batch : slots;
+    return cache_fixed(slots, batch, capacity) ? cache_most(capacity) * batch : slots;
 }
 
 }  // namespace igc

@@ -694,6 +694,8 @@ int32_t cache_attn_fwd(const igc_cache_attn* args, void* stream) {
     x.causal = args->causal != 0;
     x.tile = (int)plan.tile;
     x.split = plan.split;
+    x.fixed = plan.split && cache_fixed(plan.slots, args->batch, plan.capacity)
+                  ? (int)cache_most(plan.capacity) : 0;
     const hipStream_t st = (hipStream_t)stream;
     Workspace w;
     hipError_t e = w.take(args->workspace, cache_attn_ws(plan), st);

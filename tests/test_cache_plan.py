@@ -28,6 +28,8 @@ int bisect() { return igc::kCacheBisect; }
 int unit() { return igc::kCacheUnit; }
 int least() { return igc::kCacheLeast; }
 uint32_t parts(int n, uint32_t chunk) { return igc::cache_parts(n, chunk); }
+int fixed(int64_t slots, int64_t b, int64_t cap) { return igc::cache_fixed(slots, b, cap); }
+int64_t most(int64_t cap) { return igc::cache_most(cap); }
 int64_t bound(int64_t slots, int64_t b, int64_t cap) { return igc::cache_slots_bound(slots, b, cap); }
 }
 """
@@ -49,6 +51,7 @@ def plan(tmp_path_factory):
     u32 = ctypes.c_uint32
     L.units.argtypes, L.units.restype = [ctypes.c_int], u32
     L.chunk.argtypes, L.chunk.restype = [u32] * 2, u32
+    L.fixed.argtypes, L.most.argtypes, L.most.restype = [i64] * 3, [i64], i64
     L.bound.argtypes, L.bound.restype = [i64] * 3, i64
     L.parts.argtypes, L.parts.restype = [ctypes.c_int, u32], u32
     return L
@@ -88,6 +91,12 @@ def test_division(plan):
         if not plan.splits(slots, b):
             assert room == b
             continue
+        if plan.fixed(slots, b, cap):
+            # slots of their own hold every sequence's smallest splits
+            assert room == b * plan.most(cap) <= slots
+            assert all(plan.parts(n, plan.least()) <= plan.most(cap) for n in lens + [cap])
+        else:
+            assert room == slots < b * plan.most(cap)
         total = sum(plan.units(n) for n in lens)
         assert total < 1 << 32
         c, low = plan.chunk(total, slots - b), plan.chunk(total, slots)
