@@ -497,9 +497,9 @@ int32_t check_cache_attn_shape(const igc_cache_attn* p) {
 
 // Rows of a workgroup: 16 where that holds them all (4 x 65537 tokens, 4 rows a
 // key head: 89 us, 32 rows 106; 8 x 784: 9.6 and 12.5).  A sequence is split
-// between workgroups from 769 tokens on (8 sequences, 16 heads of 128 over 4
-// key heads, 704 tokens: 9.9 us whole and 10.2 split; 784: 10.2 both; 1024: 12.1
-// and 10.3), where the card has a workgroup a CU for three of each, or for two
+// between workgroups from 641 tokens on (8 sequences, 16 heads of 128 over 4
+// key heads, 640 tokens: 8.6 us whole and 9.4 split; 704: 9.8 and 9.4; 768: 10.1
+// and 9.5), where the card has a workgroup a CU for three of each, or for two
 // of 32 rows, which fill a CU alone (16 x 4096 with 32 rows: 28 us, two a CU
 // 36); else two a CU that even out ragged lengths (16 x 4099 with 5 drafts: 24
 // and 26; 8 x 4099: 18.6 and 18.2), if those are 2.5 a sequence (24 x 4099: 36.7 us
@@ -516,7 +516,7 @@ CacheAttnPlan cache_attn_plan(const igc_cache_attn* p) {
     x.slots = hr ? kNumCUs / hr : 0;
     if (x.tile == 16 && x.slots < 3 * p->batch) x.slots = hr ? 2 * kNumCUs / hr : 0;
     const bool fair = x.tile != 16 || x.slots * 2 >= 5 * p->batch || x.capacity > 8192;
-    x.split = p->batch > 0 && cache_splits(x.slots, p->batch) && fair && x.capacity > 768;
+    x.split = p->batch > 0 && cache_splits(x.slots, p->batch) && fair && x.capacity > 640;
     if (!x.split) x.slots = p->batch;
     x.groups = hr * (x.split ? cache_slots_bound(x.slots, p->batch, x.capacity) : p->batch);
     if (x.split) {

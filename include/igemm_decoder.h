@@ -192,7 +192,7 @@ int32_t kv_cache_read_check(const igc_kv_io* args);
  *   lse  fp32 [batch, q_heads, q_len], dense, or NULL
  * The integers enter the matrix products as they are; p_j times the value's
  * scale is held in 16 significant bits, sums in fp32.  Sequences of more than
- * 768 tokens (by the table's capacity) may be read by several workgroups,
+ * 640 tokens (by the table's capacity) may be read by several workgroups,
  * whose results (fp32, in the workspace) a second launch joins in a fixed
  * order: results do not change from run to run.
  * Limits: as cross_attn_fwd for q and out; the table's capacity below

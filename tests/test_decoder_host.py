@@ -287,7 +287,7 @@ def test_cache_attention_accepted():
 
 def test_cache_attention_workspace():
     L = igc.lib()
-    assert L.cache_attn_fwd_workspace_bytes(_attn(entries=24)) == 0      # 768 tokens: no split
+    assert L.cache_attn_fwd_workspace_bytes(_attn(entries=20)) == 0      # 640 tokens: no split
     need = L.cache_attn_fwd_workspace_bytes(_attn())
     assert need > 0 and need % 4 == 0
     assert L.cache_attn_fwd_check(_attn(ws=WS, ws_bytes=need)) == 0
