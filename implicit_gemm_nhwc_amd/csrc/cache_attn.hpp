@@ -64,12 +64,18 @@ __device__ __forceinline__ u32x2 read_tr8(const uint8_t* __restrict__ p) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lp)(bp)p));
 }
 
-// Four values of a packed row's result, and the row's lse.
+// Four values of a packed row's result, and the row's lse; given: the
+// sequence's length as given, not negative.  l is 0 without a key, and where all
+// scores are -inf, which is NaN: the largest finite score would add 1 or more.
 template <int DT>
-__device__ __forceinline__ void cache_attn_out(const AttnArgs& a, int b, int hk, int row, int d,
-                                               const f32x4& o, float m, float l) {
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays NaN
+__device__ __forceinline__ void cache_attn_out(const CacheAttnArgs& x, int b, int hk, int row,
+                                               int d, int given, const f32x4& o, float m,
+                                               float l) {
+    const AttnArgs& a = x.a;
     const int tok = div_g(a, row), g = row - tok * a.G;
+    const int seen = given - (x.causal ? a.Tq - 1 - tok : 0);
+    if (l == 0.0f && seen > 0 && x.capacity > 0) l = __builtin_nanf("");
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays NaN
     uint8_t* dst = a.out + (int64_t)b * a.o_b + (int64_t)tok * a.o_t +
                    ((int64_t)hk * a.G + g) * a.o_h + d * 2;
     *reinterpret_cast<u32x2*>(dst) =
@@ -603,7 +609,7 @@ __global__ __launch_bounds__(kCacheWaves * 64, RB == 1 ? 4 : 2) void cache_attn_
                     a.stat[to * 2 + 1] = ll;
                 }
             } else {
-                cache_attn_out<DT>(a, b, hk, row, d, o, mm, ll);
+                cache_attn_out<DT>(x, b, hk, row, d, given, o, mm, ll);
             }
         }
     }
@@ -687,7 +693,7 @@ __global__ __launch_bounds__(256) void cache_attn_join_kernel(CacheAttnArgs x) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(v[e], k, o[e]);
     }
-    cache_attn_out<DT>(a, b, hk, row, d, o, mm, ll);
+    cache_attn_out<DT>(x, b, hk, row, d, max(x.lens[b], 0), o, mm, ll);
 }
 
 }  // namespace igc

@@ -187,8 +187,9 @@ int32_t kv_cache_read_check(const igc_kv_io* args);
  * cross_attn_fwd:
  *   s_j = scale * q . k_j,  lse = log sum_j exp(s_j),  out = sum_j p_j v_j
  * A row that attends to nothing has out = 0 and lse = -inf; one that attends
- * to a page outside the pool is NaN.  Positions that a row does not attend to
- * never enter its sums, whatever the pool holds there.
+ * to a page outside the pool is NaN, and so is one whose scores are all -inf.
+ * Positions that a row does not attend to never enter its sums, whatever the
+ * pool holds there.
  *   lse  fp32 [batch, q_heads, q_len], dense, or NULL
  * The integers enter the matrix products as they are; p_j times the value's
  * scale is held in 16 significant bits, sums in fp32.  Sequences of more than

@@ -182,6 +182,68 @@ def test_extreme_scores_and_scales():
         _check(q, cache, table, n, out, None, scale=0.5)
 
 
+def _edge(entries, hk, tq, lens, page=16, d=64, dt=BF):
+    """Pool, table, lengths and queries of four heads a key head."""
+    cache, table, n = _pool(len(lens), entries, hk, d, page, lens)
+    return cache, table, n, _q(dt, len(lens), tq, 4 * hk, d)
+
+
+# whole sequences, slots of their own, a division by lengths; one and two row tiles
+EDGES = [(3, 2, 1, [1, 40, 0]), (4, 2, 3, [2, 61, 64]), (100, 2, 2, [1600, 700, 1]),
+         (300, 16, 1, [4800, 1, 300]), (60, 4, 9, [950, 8, 640])]
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("edge", EDGES, ids=str)
+def test_rows_whose_scores_are_all_minus_infinity_are_nan(edge, dt):
+    """An infinite value of a query makes each of its row's scores infinite; the
+    row is NaN by the definition, and zeros are what a row without a key has.
+    Rows beside it keep their bits."""
+    cache, table, n, q = _edge(*edge, dt=dt)
+    cache.k[..., 5].copy_(cache.k[..., 5].abs().clamp(1, 127))
+    b, tq, hq, _ = q.shape
+    want, lse0 = igc.cache_attention(q, cache, table, n, return_lse=True)
+    for value in (-torch.inf, torch.inf, torch.nan):
+        for rows in ((slice(None), slice(None), slice(1, None, 3)), (slice(None), 0), (0,)):
+            hit = torch.zeros(b, tq, hq, dtype=torch.bool, device=DEV)
+            hit[rows] = True
+            bad = q.clone()
+            bad[..., 5] = torch.where(hit, value, bad[..., 5].float()).to(dt)
+            for causal in (True, False):
+                first = n[:, None] - (torch.arange(tq - 1, -1, -1, device=DEV) if causal else 0)
+                hit_now = hit & (first > 0)[..., None]
+                if not causal:
+                    want_now, lse_now = igc.cache_attention(q, cache, table, n, causal=False,
+                                                            return_lse=True)
+                else:
+                    want_now, lse_now = want, lse0
+                out, lse = igc.cache_attention(bad, cache, table, n, causal=causal,
+                                               return_lse=True)
+                hit_lse = hit_now.transpose(1, 2)
+                assert out[hit_now].isnan().all() and lse[hit_lse].isnan().all()
+                assert torch.equal(out[~hit_now], want_now[~hit_now])
+                assert torch.equal(lse[~hit_lse], lse_now[~hit_lse])
+
+
+@pytest.mark.parametrize("edge", [(8, 2, 1, [128, 100, 70]), (100, 2, 2, [1600, 700, 90]),
+                                  (300, 16, 1, [4800, 80, 300]), (60, 4, 9, [950, 80, 640])],
+                         ids=str)
+def test_keys_of_minus_infinity_beside_finite_ones(edge):
+    """Scores past fp32's range, of whole blocks, waves and splits: as scores of
+    -1000 would, they leave the others their weights, to the bit."""
+    cache, table, n, q = _edge(*edge)
+    cache.k[..., 5] = -100
+    place = torch.arange(32, 64, device=DEV)
+    cache.k[table.long()[:, place // 16], :, (place % 16), 5] = 0
+    for causal in (True, False):
+        got = []
+        for value in (1e38, 1e5):
+            q[..., 5] = value
+            got.append(igc.cache_attention(q, cache, table, n, causal=causal, return_lse=True))
+        assert torch.isfinite(got[0][0]).all()
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_strides_guards_and_workspace():
     cache, table, n = _pool(3, 70, 2, 80, 16, [1100, 40, 1117])
     dense = _q(BF, 3, 3, 8, 80)
