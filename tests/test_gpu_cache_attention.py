@@ -110,6 +110,72 @@ def test_against_the_oracle(case):
             assert torch.equal(igc.cache_attention(q, cache, table, n, causal=causal), out)
 
 
+# the sequences of these share what room there is by their lengths, past a wave's
+# 64 of them too; one and two row tiles, one and several key heads
+DIVIDED = [
+    (BF, 1, 2, 1, 128, 16, 128, [2048, 0, 1, 300, 129, 2047, 7, 256] + [0, 1, 640, 90] * 23),
+    (HF, 2, 4, 2, 64, 32, 22, [704, 703, 0, 1, 257] * 20),
+    (BF, 1, 3, 1, 40, 16, 44, [(97 * i) % 705 for i in range(200)]),
+    (HF, 8, 4, 1, 32, 32, 35, [1120, 5, 0, 900, 256] * 14),
+    (BF, 1, 32, 32, 64, 64, 64, [4096, 1, 2300]),
+    (HF, 5, 32, 32, 80, 16, 256, [4095, 3, 0]),
+    (BF, 5, 24, 8, 128, 128, 64, [8192, 4100, 129]),
+]
+
+
+def _divided(q_shape, cache, entries, dt):
+    """Whether a call's workspace holds fewer parts than every sequence's own
+    slots would take (256 keys a part at least)."""
+    b, tq, hq, d = q_shape
+    rows, most = tq * hq // cache.kv_heads, -(-(entries * cache.k.shape[2]) // 256)
+    a_part = cache.kv_heads * (rows if rows <= 16 else -(-rows // 32) * min(rows, 32)) * (d + 2) * 4
+    room, rest = divmod(igc.cache_attn_fwd_workspace_bytes(q_shape, cache, entries, dt), a_part)
+    assert rest == 0
+    return b < room < b * most
+
+
+@pytest.mark.parametrize("case", DIVIDED, ids=lambda c: f"{len(c[7])}x{c[1]}-{c[2]}.{c[3]}.{c[4]}-{c[5]}")
+def test_division_by_lengths(case):
+    print(f"cache attention, divided {case[:7]}", flush=True)
+    dt, tq, hq, hk, d, page, entries, lens = case
+    cache, table, n = _pool(len(lens), entries, hk, d, page, lens)
+    q = _q(dt, len(lens), tq, hq, d)
+    assert _divided(q.shape, cache, entries, dt)
+    out, lse = igc.cache_attention(q, cache, table, n, return_lse=True)
+    _check(q, cache, table, n, out, lse)
+    full = igc.cache_attention(q, cache, table, n, causal=False)
+    if tq == 1:
+        assert torch.equal(full, out)
+    for again in range(2):
+        assert torch.equal(igc.cache_attention(q, cache, table, n), out)
+        with igc.using_library(igc.POISON_LIB_PATH):
+            assert torch.equal(igc.cache_attention(q, cache, table, n), out)
+            assert torch.equal(igc.cache_attention(q, cache, table, n, causal=False), full)
+
+
+def test_a_captured_launch_divides_anew():
+    """Between the replays of a graph the lengths change, and with them the
+    division: each replay's bits are an eager call's, and each is checked."""
+    cache, table, n = _pool(4, 100, 16, 64, 16, [1600, 1600, 1600, 1600])
+    q = _q(HF, 4, 2, 32, 64)
+    assert _divided(q.shape, cache, 100, HF)
+    igc.cache_attention(q, cache, table, n)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = igc.cache_attention(q, cache, table, n, return_lse=True)
+    for i, lens in enumerate(([1600, 0, 3, 700], [0, 0, 0, 0], [1, 1600, 1600, 2], [5, 1, 0, 1599])):
+        q.copy_(torch.randn(q.shape, device=DEV))
+        n.copy_(torch.tensor(lens, dtype=torch.int32))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        a, b = igc.cache_attention(q, cache, table, n, return_lse=True)
+        torch.cuda.synchronize()
+        assert torch.equal(a, out) and torch.equal(b, lse)
+        _check(q, cache, table, n, out, lse)
+
+
 def test_rows_that_attend_to_nothing():
     cache, table, n = _pool(3, 2, 2, 64, 16, [0, 2, 5])
     q = _q(BF, 3, 4, 4, 64)

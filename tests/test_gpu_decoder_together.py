@@ -102,3 +102,19 @@ def test_graphs_replayed_in_turn():
             assert _same(s.run(), w)   # eager, behind the replay
             torch.cuda.synchronize()
             assert _same(got, w)
+
+
+# steps whose attention divides the card by the sequences' lengths
+DIVIDED = [(5, 1, 32, 24, 4096), (6, 3, 40, 16, 2048), (7, 1, 4, 128, 65536)]
+
+
+@pytest.mark.parametrize("run", [test_threads_on_streams_of_their_own, test_graphs_replayed_in_turn])
+def test_with_divisions_by_lengths(run, monkeypatch):
+    for seed, tokens, heads, d, capacity in DIVIDED:
+        cache = igc.KVCache.empty(1, 32, heads, d, device=DEV)
+        need = igc.cache_attn_fwd_workspace_bytes((3, tokens, heads, d), cache, capacity // 32,
+                                                  torch.bfloat16)
+        room = need // (heads * tokens * (d + 2) * 4)
+        assert 3 < room < 3 * (capacity // 256)   # parts, of 256 keys at least
+    monkeypatch.setitem(globals(), "STEPS", DIVIDED)
+    run()
