@@ -10,7 +10,8 @@ import subprocess
 import pytest
 
 import implicit_gemm_nhwc_amd as igc
-from test_attn_assembly import HELD, OBJDUMP, copies_before_a_restore, under_a_lane_branch
+from test_attn_assembly import (HELD, OBJDUMP, copies_before_a_restore, kernels,
+                                under_a_lane_branch)
 
 NAMES = rb"layer_norm_|quantize_rows|kv_cache_|cache_attn_|linear_i8_"
 
@@ -105,3 +106,37 @@ def test_product_loops_do_not_drain_their_loads(built):
             stages = int(re.search(r"kernelILi\dELi\d+ELi(\d+)E", name).group(1))
             assert len(waits) <= (1 if stages == 2 else 0), (name, waits)
     assert seen >= 4
+
+
+LABEL = re.compile(r"^[0-9a-f]+ (<L\d+>:)$")
+
+
+def _labels(body):
+    """A listing's lines with labels bare: it prints their addresses before them,
+    and a rule that looks for `<` at a line's start sees none of those."""
+    return [LABEL.sub(r"\1", x) for x in body]
+
+
+def test_labels_are_seen():
+    lost = ["s_and_saveexec_b64 s[0:1], vcc", "s_cbranch_execz L1", "v_add_f32_e32 v1, v2, v3",
+            "0000000000001a40 <L1>:", "v_accvgpr_write_b32 a3, v1", "s_or_b64 exec, exec, s[0:1]"]
+    assert copies_before_a_restore(_labels(lost)) == [(lost[5], [lost[4]])]
+
+
+@pytest.mark.parametrize("lib", ["LIB_PATH", "POISON_LIB_PATH"])
+def test_no_copy_where_a_branch_of_an_attention_kernel_arrives(lib, tmp_path):
+    """The rule on the places where skipping lanes arrive, over the attention and
+    norm kernels with their labels bare."""
+    if not os.path.exists(OBJDUMP):
+        pytest.skip("no llvm-objdump")
+    if not os.path.exists(getattr(igc, lib)):
+        import __graft_entry__
+        __graft_entry__.build()
+    code = {n: _labels(b) for n, b in kernels(getattr(igc, lib), str(tmp_path)).items()}
+    jumps = {n: {x.split()[-1] for x in b if x.startswith("s_cbranch_execz")}
+             for n, b in code.items()}
+    assert sum(map(bool, jumps.values())) > 100   # kernels with such branches
+    for name, body in code.items():
+        places = {x[1:].split(">")[0] for x in body if x.startswith("<")}
+        assert jumps[name] <= places, name
+        assert copies_before_a_restore(body) == [], name
