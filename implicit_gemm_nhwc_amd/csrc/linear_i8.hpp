@@ -49,7 +49,8 @@ __device__ __forceinline__ i32x4 lin_clear(i32x4 v, int left) {
     return v;
 }
 
-// Scales and bias of columns n .. n + 3 of row m (zeros past N).
+// Scales and bias of columns n .. n + 3 of row m (past N the last column's, past
+// M the last row's; such results are not stored).
 struct LinScales {
     float xs;
     f32x4 ws, bs;

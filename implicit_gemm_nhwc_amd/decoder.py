@@ -294,8 +294,9 @@ def linear_i8(x, x_scale, w, w_scale, *, bias=None, dtype=torch.bfloat16, stream
     """The product of rows in 8 bits: x int8 [..., k] with x_scale fp32 [...]
     and w int8 [n, k] with w_scale fp32 [n] (quantize_rows of the tokens and of
     the weights) give dtype [..., n]: (x w^T) x_scale w_scale + bias (fp32 [n]
-    or None).  The integer sums are exact.  Rows start at multiples of 16 bytes,
-    which their last 16-byte piece may reach past k."""
+    or None).  The integer sums are exact; x_scale times a sum has to stay below
+    2^128 (an x_scale up to 2^96 always does).  Rows start at multiples of 16
+    bytes, which their last 16-byte piece may reach past k."""
     device = _device(x, "x")
     if _fast is not None and stream is None:
         r = _fast.linear_i8(_entries(), x, x_scale, w, w_scale, bias, dtype,
@@ -416,12 +417,13 @@ def kv_cache_write_check(cache, k, v, table, start, *, lens=None) -> int:
 
 
 def kv_cache_write(cache, k, v, table, start, *, lens=None, stream=None):
-    """Quantise k and v (bf16 or fp16 [batch, tokens, kv_heads, D], any
-    strides) into the cache: token i < lens[b] (int32 [batch]; None: all) of
-    sequence b goes to position start[b] + i (int32 [batch]), which is token
-    p % page_tokens of page table[b, p // page_tokens].  Positions past the
-    table and pages outside the pool are left out.  The page of a place must
-    not be written twice in one call."""
+    """Quantise k and v (bf16 or fp16 [batch, tokens, kv_heads, D], pointers and
+    strides multiples of 16 bytes, the values of a head adjacent) into the
+    cache: token i < lens[b] (int32 [batch]; None: all) of sequence b goes to
+    position start[b] + i (int32 [batch]), which is token p % page_tokens of
+    page table[b, p // page_tokens].  Positions past the table and pages
+    outside the pool are left out.  The page of a place must not be written
+    twice in one call."""
     device = _pool(cache)
     if _fast is not None and stream is None and device == _current_gpu():
         if _fast.kv_cache_write(_entries(), cache.packed, k, v, table, start, lens,
@@ -529,9 +531,11 @@ def cache_attention(q, cache, table, lens, *, causal=True, scale=None, return_ls
     the places that table (int32 [batch, entries]) gives its positions.  The
     new tokens are the last tq of them (kv_cache_write puts them there first)
     and causal lets token i attend up to its own position only.  scale
-    defaults to 1 / sqrt(D).  A row that attends to nothing gives 0.  Returns
-    out, dense like q, and with return_lse also the fp32 statistics [batch,
-    hq, tq].  No gradients: the cache is for inference."""
+    defaults to 1 / sqrt(D).  A row that attends to nothing gives 0, one whose
+    scores are all -inf (an infinite query) NaN.  q's pointer and strides are
+    multiples of 16 bytes, the values of a head adjacent.  Returns out, dense
+    like q, and with return_lse also the fp32 statistics [batch, hq, tq].  No
+    gradients: the cache is for inference."""
     device = _pool(cache)
     if _fast is not None and stream is None and device == _current_gpu():
         r = _fast.cache_attention(_entries(), q, cache.packed, table, lens, causal, scale,

@@ -57,8 +57,10 @@ typedef struct igc_attn_view {
  *   valid:  j < min(kv_lens[b], kv_len)  and  key_mask[b][j] != 0
  *   s_j = scale * q . k_j,   lse = log sum_j exp(s_j),   p_j = exp(s_j - lse)
  *   out = sum_j p_j v_j
- * A row without a valid key has out = 0 and lse = -inf.  The key and value
- * rows of keys that are not valid never enter a sum (they may hold NaN).
+ * A row without a valid key has out = 0 and lse = -inf, and so has one whose
+ * scores are all -inf in fp32 (an infinite query can make them so).  The key
+ * and value rows of keys that are not valid never enter a sum (they may hold
+ * NaN).
  *   q, out   [batch, q_len, q_heads, head_dim];  k, v [batch, kv_len,
  *            kv_heads, head_dim], kv_heads dividing q_heads
  *   lse      fp32 [batch, q_heads, q_len], dense, or NULL when no backward

@@ -97,7 +97,9 @@ int32_t quantize_rows_check(const igc_quantize_rows* args);
  * Product of rows in 8 bits: for x int8 [m][k] with a scale a row (a token) and
  * w int8 [n][k] with a scale a row (an output channel),
  *   y[i][j] = (sum_k x[i][k] w[j][k]) x_scale[i] w_scale[j] + bias[j]
- * The integer sums are exact; scales and bias enter in fp32.
+ * The integer sums are exact; scales and bias enter in fp32, x_scale first: a
+ * sum times x_scale that passes 2^128 is infinite, whatever w_scale is (an
+ * x_scale up to 2^96, rows of values up to 2^102, never does).
  *   x, w     pointers and row pitches (bytes) are multiples of 16; a row's last
  *            16-byte piece is read whole, its bytes past k do not matter.
  *            Every int8 value is allowed, -128 too
@@ -192,10 +194,12 @@ int32_t kv_cache_read_check(const igc_kv_io* args);
  * pool holds there.
  *   lse  fp32 [batch, q_heads, q_len], dense, or NULL
  * The integers enter the matrix products as they are; p_j times the value's
- * scale is held in 16 significant bits, sums in fp32.  Sequences of more than
- * 640 tokens (by the table's capacity) may be read by several workgroups,
- * whose results (fp32, in the workspace) a second launch joins in a fixed
- * order: results do not change from run to run.
+ * scale is held in 16 significant bits, sums in fp32.  Scores, q . K_j of the
+ * integers (queries up to 2^113) and sums of p_j v_j (values up to 2^119 /
+ * lens[b]) have to stay within fp32's range; past it rows are infinite or NaN.
+ * Sequences of more than 640 tokens (by the table's capacity) may be read by
+ * several workgroups, whose results (fp32, in the workspace) a second launch
+ * joins in a fixed order: results do not change from run to run.
  * Limits: as cross_attn_fwd for q and out; the table's capacity below
  * 2^31 - 4096, batch * q_heads below 2^31, batch * kv_heads times the tiles of
  * 32 rows (q_len * q_heads / kv_heads) below 2^23.
