@@ -21,11 +21,11 @@
 // probabilities, for both types; the matrix cores are busy 11 %.
 //
 // Long caches are bound by HBM: 4 sequences of 22000 to 65537 tokens, 8 key heads
-// of 128, in 75 to 80 us (369 MB, 4.6 to 4.9 TB/s), then 4.8 us for the join.  Short
+// of 128, in 76 to 82 us (369 MB, 4.5 to 4.9 TB/s), then 5.0 us for the join.  Short
 // ones by vector instructions, of which a block of 32 keys takes about 340, half
 // of them for turning 8-bit values into 16-bit ones (0.8 us a block and SIMD), and
 // by round trips: entry of the table, keys, values.  16 sequences of 4099 with 5
-// drafts, 8 heads of 80: 17 us, vector units 61 % busy.
+// drafts, 8 heads of 80: 17 to 19 us, vector units 61 % busy.
 #pragma once
 
 #include "attn_common.hpp"
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(kCacheWaves * 64, RB == 1 ? 4 : 2) void cache_attn_
     const int hk = hr / a.row_tiles, row0 = (hr - hk * a.row_tiles) * ROWS;
     const int t0 = div_g(a, row0);
     // keys past what the last of these rows sees are not read (a prompt of 2048
-    // tokens, 16 heads of 128 over 4 key heads: 130 -> 102 us)
+    // tokens, 16 heads of 128 over 4 key heads: 130 -> 102 us, 97 now)
     if (x.causal) end = min(end, given - (a.Tq - 1 - div_g(a, min(row0 + ROWS, a.rows) - 1)));
     const bool empty = x.pages == 0;   // a pool without pages: nothing to read
     const int stop = empty ? 0 : end;

@@ -256,11 +256,13 @@ int32_t check_quant(const igc_quantize_rows* p, Rows* x, Rows* q) {
 }
 
 // ------------------------------------------------------------ their product
-// Few rows, whose workgroups each read x again (32 rows x 4096 x 4096: 7.9 us,
-// tiles 8.7; x 8192 x 8192: 26 and 16), or the largest tiles that still give
-// every CU one (4096 x 4096 x 4096: 72 us in tiles of 256, 96 in tiles of 128; 2048
+// Few rows, whose workgroups each read x again (32 rows x 4096 x 4096: 8.4 us,
+// tiles 10.5; x 8192 x 8192: 25 and 20), or the largest tiles that still give
+// every CU one (4096 x 4096 x 4096: 72 us in tiles of 256, 90 in tiles of 128; 2048
 // x 4096 x 4096: 55 and 44; 2048 x 2048 x 4096: 23 us in tiles of 128, 34 in tiles
-// of 64; 1024 x 1024 x 4096: 19 and 11).
+// of 64; 1024 x 1024 x 4096: 19 and 11).  What the rule does not see: few columns
+// of a long k (32 rows x 300 x 131056: 115 us as few rows, 186 in tiles) and a
+// last round of few tiles (4352 x 4096 x 4096: 111 us in tiles of 256, 101 of 128).
 LinForm lin_form(const igc_linear_i8* p) {
     if (p->m <= 16 || (p->m <= kFewRows && p->n * p->k <= (int64_t)1 << 25))
         return {0, 1, ceil_div(p->n, 16), kFewWaves * 64};
@@ -496,15 +498,18 @@ int32_t check_cache_attn_shape(const igc_cache_attn* p) {
 }
 
 // Rows of a workgroup: 16 where that holds them all (4 x 65537 tokens, 4 rows a
-// key head: 89 us, 32 rows 106; 8 x 784: 9.6 and 12.5).  A sequence is split
-// between workgroups from 641 tokens on (8 sequences, 16 heads of 128 over 4
-// key heads, 640 tokens: 8.6 us whole and 9.4 split; 704: 9.8 and 9.4; 768: 10.1
-// and 9.5), where the card has a workgroup a CU for three of each, or for two
-// of 32 rows, which fill a CU alone (16 x 4096 with 32 rows: 28 us, two a CU
-// 36); else two a CU that even out ragged lengths (16 x 4099 with 5 drafts: 24
-// and 26; 8 x 4099: 18.6 and 18.2), if those are 2.5 a sequence (24 x 4099: 36.7 us
-// split and 38.0 whole, 28 x 4096: 42.6 and 40.4) or long ones 2 (32 x 16000:
-// 83 and 94).
+// key head: 78 us, 32 rows 86; 8 x 784: 9.5 and 10.8).  A sequence is split
+// between workgroups from 641 tokens of its table on (8 sequences, 16 heads of
+// 128 over 4 key heads, 640 tokens: 8.2 us whole and 9.2 split; 704: 9.6 and 9.2;
+// 1024: 12.1 and 9.6; 1 sequence, 32 heads over 8, 704: 9.4 and 9.0; 4 with 5
+// drafts, 8 heads of 64, 704: 7.8 and 8.1, 1024: 9.2 and 8.1), where the card has
+// a workgroup a CU for three of each, or for two of 32 rows, which fill a CU
+// alone (16 x 4096 with 32 rows: 28 us, two a CU 36); else two a CU that even out
+// ragged lengths (16 x 4099 with 5 drafts, 8 heads of 80: 21.8 us, one a CU 24.5),
+// if those are 2.5 a sequence (24 of them: 27.7 us split and 32.2 whole; 28, which
+// stay whole: 30.8 and 32.6) or long ones 2 (32 x 16000, 8 heads of 128: 141 and
+// 153).  Short sequences in a wide table pay for it (8 x 300 in a table of 640
+// tokens: 6.2 us, of 4096: 10.0).
 CacheAttnPlan cache_attn_plan(const igc_cache_attn* p) {
     CacheAttnPlan x{};
     const igc_kv_cache& c = p->cache;

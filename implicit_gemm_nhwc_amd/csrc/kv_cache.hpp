@@ -8,9 +8,9 @@
 // the same tokens, and then their values: together they go through whole rows
 // of the 16-bit tensors (16 x 4096 tokens written and read, 8 heads of 128: 151
 // us; keys first, and heads by fours, 162).  With the rows asked for together
-// and the maxima over lanes by permutations the two take 60 to 75 and 59 us of
-// kernels (5.4 to 4.3 and 6.1 TB/s, vector units 69 and 43 % busy; ragged lengths,
-// of which the whole output is written back).
+// and the maxima over lanes by permutations the two take 64 to 82 and 58 to 63 us
+// of kernels (5.0 to 3.9 and 6.2 to 5.7 TB/s, vector units 72 and 43 % busy; ragged
+// lengths, of which the whole output is written back).
 #pragma once
 
 #include "cache_plan.hpp"

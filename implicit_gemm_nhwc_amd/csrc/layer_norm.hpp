@@ -9,7 +9,7 @@
 // chunks of 8 values a lane), so that the variance is taken about the mean
 // (no cancellation), the gradient needs no statistics of the forward pass, and
 // each value is read and written once.  100352 rows of 768 in bf16: 55 us forward
-// (308 MB, 5.6 TB/s), 91 backward (462 MB, 5.1) and 5.5 for the sum of the
+// (308 MB, 5.6 TB/s), 93 backward (462 MB, 5.0) and 5.9 for the sum of the
 // workgroups' weight gradients, which has to follow in a launch of its own to
 // keep its order; 65536 rows of 512 in fp16: 21 us (134 MB, 6.4 TB/s out of the
 // Infinity Cache).  A few rows are a launch and a round trip: 2.5 us.

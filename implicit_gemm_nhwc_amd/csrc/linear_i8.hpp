@@ -7,10 +7,11 @@
 // are scaled in fp32 and rounded once.
 //
 // The tile kernel stages its rows and columns in LDS by direct loads: 16384 x
-// 4096 x 4096 in 254 to 300 us (264 on average back to back, 2.08 PFLOP/s), 8192
-// x 8192 x 8192 in 482 (2.28).  The power limit bounds it: the matrix cores are
-// busy 49 to 59 % at about 2.0 GHz, and on such data they hold 1.65 GHz when they
-// do nothing else.  The few-rows kernel, which the weights' bytes bound, takes 16
+// 4096 x 4096 in 259 to 265 us for a few calls (2.1 PFLOP/s) and in 284 to 350 once
+// the clock has been held down, 8192 x 8192 x 8192 in 483 (2.28).  The power limit
+// bounds it: the matrix cores are busy 59 % at about 2.0 GHz, and on such data they
+// hold 1.65 GHz when they do nothing else.  The few-rows kernel, which the weights'
+// bytes bound, takes 16
 // columns a workgroup, gives each wave a part of k and reads both operands
 // straight into registers.
 #pragma once
@@ -85,8 +86,8 @@ __device__ __forceinline__ void lin_store4(const LinArgs& a, int m, int n, const
 
 // ---------------------------------------------------------------------------
 // At most 16 MT rows.  The waves take a line of 128 k of each row in turn, U = 2
-// at once: the weights of 8192 x 2048 arrive in 5.4 us, of 28672 x 4096 in 25.5
-// (4.6 TB/s; eight waves, or four lines at once, within 4 %).
+// at once: the weights of 8192 x 2048 arrive in 5.6 us, of 28672 x 4096 in 27.3
+// with the launch (4.3 TB/s; eight waves, or four lines at once, within 4 %).
 constexpr int kFewWaves = 4;
 template <int DT, int MT>
 __global__ __launch_bounds__(kFewWaves * 64) void linear_i8_few_kernel(LinArgs a) {

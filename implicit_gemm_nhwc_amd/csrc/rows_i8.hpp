@@ -99,8 +99,9 @@ struct QuantArgs {
 
 // Bound by HBM: a row stays in its lanes' registers between the maximum and
 // the rounding (LONG, past 16384 values: all but its last piece is read twice).
-// 16384 rows of 4096 out of HBM: 37 to 39 us (201 MB, 5.3 TB/s; vector units 73 %
-// busy); in rows of 1023 33 us, of 4096 32 out of the Infinity Cache.
+// 16384 rows of 4096 out of HBM: 36 to 43 us, 39 on average (201 MB, 5.1 TB/s;
+// vector units 78 % busy); in rows of 1023 33 us, of 4096 32 out of the Infinity
+// Cache.
 template <int DT, int LPR, int NC, int NT, bool LONG>
 __global__ __launch_bounds__(NT) void quantize_rows_kernel(QuantArgs a) {
     constexpr int W = LPR * NC * 8;
